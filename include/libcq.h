@@ -373,6 +373,113 @@ int cq_dequant_gemm_many(int n, const cq_matvec_desc* descs, int bits, int group
 int cq_repack(const uint8_t* src, int src_bits, uint8_t* dst, int dst_bits, int64_t n_groups,
               int group_size, void* stream);
 
+/* ---- Around the products: embedding, norm, 8-bit activations --------------
+ *
+ * What a model does before and between its products: the embedding lookup
+ * (also straight from the packed embedding) with its gradient, the residual
+ * addition with the root-mean-square norm and its gradient, the same norm
+ * written as 8-bit activations in the rotated space, and the product that
+ * reads those.  The conventions above hold (device pointers, contiguous
+ * row-major tensors, 16-byte alignment, validation before anything is
+ * enqueued, no overlap unless stated).  No call allocates: where one needs
+ * working memory, a host-only size function says how much, and the caller
+ * passes a 16-byte aligned device buffer that the stream owns until it has
+ * passed the call.  All calls may be captured into a HIP graph.  Results are
+ * deterministic (no atomics on values, fixed summation orders). */
+
+/* out[i] = scale * table[tokens[i]] for n token ids of token_bytes bytes each
+ * (4: int32, 8: int64).  table is vocab x dim, out n x dim, each CQ_F32 or
+ * CQ_BF16; the product is taken in float32 and rounded once.  An id outside
+ * [0, vocab) (padding) gives a row of zeros and reads nothing. */
+int cq_embed(const void* tokens, int token_bytes, int64_t n, const void* table, int table_dtype,
+             int64_t vocab, int64_t dim, float scale, void* out, int out_dtype, void* stream);
+
+/* The same lookup from the CQ form of the table (rows = vocab, cols = dim, as
+ * cq_quantize wrote it, any bit-width, group size and storage cq_dequantize
+ * takes): out[i] = scale * the dequantized row, i.e.
+ * (scale * norm / G) * H * levels[idx] per group in float32, without the
+ * table ever being unpacked ("How Needle 2 Model Compresses to a Single
+ * Binary", section Stage 3: packed tensors are decoded where they are used).
+ * Alignment of packed as for cq_dequantize. */
+int cq_embed_packed(const void* tokens, int token_bytes, int64_t n, const uint8_t* packed,
+                    const uint16_t* norms, int64_t vocab, int64_t dim, int bits, int group_size,
+                    const float* levels, int n_levels, float scale, void* out, int out_dtype, void* stream);
+
+/* Gradient of cq_embed (and, straight through the quantizer, of
+ * cq_embed_packed) with respect to the table:
+ * grad[v] = scale * sum of dout[i] over all i with tokens[i] == v, added in
+ * float32 and rounded once to grad_dtype.  dout is n x dim (dout_dtype).
+ * accumulate == 0: every one of the vocab x dim values is written (zeros for
+ * tokens that do not occur); 1: the sums are added to grad, and only rows of
+ * tokens that occur are touched.  Ids outside [0, vocab) contribute nothing.
+ * The positions are sorted by token first, so each row is summed in a fixed
+ * order.  workspace: cq_embed_grad_workspace bytes (host only, pure; about
+ * 8 to 16 bytes per position, plus dim / 8 per position past 64). */
+int cq_embed_grad_workspace(int64_t n, int64_t vocab, int64_t dim, int64_t* bytes);
+int cq_embed_grad(const void* tokens, int token_bytes, int64_t n, const void* dout, int dout_dtype,
+                  int64_t vocab, int64_t dim, float scale, int accumulate, void* grad, int grad_dtype,
+                  void* workspace, int64_t workspace_bytes, void* stream);
+
+/* h = x + residual; out = h * rsqrt(mean(h^2) + eps) * weight, per row of
+ * cols values.  x, residual (nullable: h = x) and sum are `dtype` (CQ_F32 or
+ * CQ_BF16), weight (nullable: ones) weight_dtype, out out_dtype.  h is formed
+ * and normalised in float32; sum (nullable) receives it rounded to `dtype`
+ * and may be x or residual itself.  cols <= 32768 (CQ_ERR_UNSUPPORTED
+ * otherwise: a row is held in registers).  eps >= 0. */
+int cq_add_rms_norm(const void* x, const void* residual, int dtype, const void* weight, int weight_dtype,
+                    int64_t rows, int64_t cols, float eps, void* sum, void* out, int out_dtype, void* stream);
+
+/* cq_add_rms_norm with its output rotated and held in 8 bits: each G-group of
+ * the normalised row is rotated by the orthonormal Hadamard matrix (what the
+ * products do to their activations), s = the row's largest magnitude / 127,
+ * q = round(rotated / s), ties to even, in [-127, 127].  q is rows x cols
+ * int8, scale has rows float32 values: the rotated activations are q * s.
+ * cols must be a multiple of group_size (32, 64, 128 or 256).  A row whose
+ * rotated values all lie below 2^-118 has scale 0 and q 0; a row with a
+ * value that is not finite has scale NaN and q 0. */
+int cq_add_rms_norm_q8(const void* x, const void* residual, int dtype, const void* weight, int weight_dtype,
+                       int64_t rows, int64_t cols, int group_size, float eps, void* sum, int8_t* q,
+                       float* scale, void* stream);
+
+/* Gradient of cq_add_rms_norm at its stored sum h: with u = weight * dout and
+ * r = rsqrt(mean(h^2) + eps),
+ *   dx = dsum + r u - h r^3 mean(u h)        (for x and residual alike),
+ *   dweight = sum over rows of dout h r      (float32 [cols], nullable).
+ * dout, sum, dsum (the gradient that reaches sum by other ways; nullable:
+ * zero) and dx are `dtype`; dx may be dsum.  cols <= 32768.  workspace:
+ * cq_rms_norm_grad_workspace bytes (0 bytes without dweight may be NULL). */
+int cq_rms_norm_grad_workspace(int64_t rows, int64_t cols, int dtype, int64_t* bytes);
+int cq_rms_norm_grad(const void* dout, const void* sum, const void* dsum, int dtype, const void* weight,
+                     int weight_dtype, int64_t rows, int64_t cols, float eps, void* dx, float* dweight,
+                     void* workspace, int64_t workspace_bytes, void* stream);
+
+/* The codebook of the 8-bit product: level k ~ scale * (256 hi[k] + lo[k]).
+ * cq_q8_levels picks the scale that fits the levels (nullable: built-in table
+ * of the width) best in the mean square over N(0,1), once per codebook; each
+ * level is met to within 2.1e-5 of the largest. */
+typedef struct {
+  int8_t hi[CQ_MAX_LEVELS];
+  int8_t lo[CQ_MAX_LEVELS];
+  float scale;
+  int32_t n_levels;
+} cq_q8_table;
+int cq_q8_levels(int bits, const float* levels, int n_levels, cq_q8_table* table);
+
+/* y = x . W_hat^T for the quantized n_out x k matrix W (as cq_dequant_matvec)
+ * and activations in the form cq_add_rms_norm_q8 writes: q int8 [batch][k]
+ * and scale float32 [batch] stand for the rotated activations q * scale, so
+ *   y[b][n] = scale[b] * sum_g norm[n][g] / sqrt(G) * sum_{j in g} q[b][j] level[n][j].
+ * y is batch x n_out, y_dtype CQ_F32 or CQ_BF16.  One batch row (a decode
+ * step) to many.  The sums within a group are exact integers on the table's
+ * 16-bit levels, the sum over groups float32.  k a multiple of G, at most
+ * 2^22; trit storage is converted with cq_repack first.  table: host.
+ * workspace: cq_dequant_gemm_q8_workspace bytes (0 for most calls: NULL). */
+int cq_dequant_gemm_q8_workspace(int64_t n_out, int64_t k, int64_t batch, int group_size, int64_t* bytes);
+int cq_dequant_gemm_q8(const uint8_t* packed, const uint16_t* norms, int64_t n_out, int64_t k, int bits,
+                       int group_size, const cq_q8_table* table, const int8_t* q, const float* scale,
+                       int64_t batch, void* y, int y_dtype, void* workspace, int64_t workspace_bytes,
+                       void* stream);
+
 /* Static description of a status code. */
 const char* cq_status_str(int status);
 

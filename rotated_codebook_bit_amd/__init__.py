@@ -19,7 +19,8 @@ __all__ = [
     "model_bytes", "codebook", "codebook_train", "quantize", "dequantize", "dequant_matvec", "dequant_matvec_many",
     "dequant_matvec_many_noalloc",
     "fake_quant", "blob_layout", "quantize_many", "dequantize_many", "dequant_gemm",
-    "dequant_gemm_many",
+    "dequant_gemm_many", "embed", "embed_packed", "embed_grad", "add_rms_norm", "add_rms_norm_q8", "rms_norm_grad",
+    "Q8Table", "q8_levels", "dequant_gemm_q8",
 ]
 
 TERNARY = 158
@@ -58,6 +59,13 @@ class MatvecDesc(ctypes.Structure):
                 ("k", ctypes.c_int64), ("x", ctypes.c_void_p), ("y", ctypes.c_void_p)]
 
 
+class Q8Table(ctypes.Structure):
+    """cq_q8_table: the 16-bit levels of the 8-bit product, made by
+    q8_levels() once per codebook."""
+    _fields_ = [("hi", ctypes.c_int8 * 16), ("lo", ctypes.c_int8 * 16), ("scale", ctypes.c_float),
+                ("n_levels", ctypes.c_int32)]
+
+
 def lib() -> ctypes.CDLL:
     """Load libcq.so (built in place by ``rotated_codebook_bit_amd.build``)."""
     global _lib
@@ -94,6 +102,23 @@ def lib() -> ctypes.CDLL:
         L.cq_dequant_matvec_many.argtypes = [i32, ctypes.POINTER(MatvecDesc), i32, i32,
                                              ctypes.POINTER(ctypes.c_float), i32, i64, vp]
         L.cq_dequant_matvec_many_noalloc.argtypes = L.cq_dequant_matvec_many.argtypes
+        f32, fp, p64 = ctypes.c_float, ctypes.POINTER(ctypes.c_float), ctypes.POINTER(i64)
+        L.cq_embed.argtypes = [vp, i32, i64, vp, i32, i64, i64, f32, vp, i32, vp]
+        L.cq_embed_packed.argtypes = [vp, i32, i64, vp, vp, i64, i64, i32, i32, fp, i32, f32, vp, i32, vp]
+        L.cq_embed_grad_workspace.argtypes = [i64, i64, i64, p64]
+        L.cq_embed_grad.argtypes = [vp, i32, i64, vp, i32, i64, i64, f32, i32, vp, i32, vp, i64, vp]
+        L.cq_add_rms_norm.argtypes = [vp, vp, i32, vp, i32, i64, i64, f32, vp, vp, i32, vp]
+        L.cq_add_rms_norm_q8.argtypes = [vp, vp, i32, vp, i32, i64, i64, i32, f32, vp, vp, vp, vp]
+        L.cq_rms_norm_grad_workspace.argtypes = [i64, i64, i32, p64]
+        L.cq_rms_norm_grad.argtypes = [vp, vp, vp, i32, vp, i32, i64, i64, f32, vp, vp, vp, i64, vp]
+        L.cq_q8_levels.argtypes = [i32, fp, i32, ctypes.POINTER(Q8Table)]
+        L.cq_dequant_gemm_q8_workspace.argtypes = [i64, i64, i64, i32, p64]
+        L.cq_dequant_gemm_q8.argtypes = [vp, vp, i64, i64, i32, i32, ctypes.POINTER(Q8Table), vp, vp, i64, vp, i32, vp,
+                                         i64, vp]
+        for name in ("cq_embed", "cq_embed_packed", "cq_embed_grad_workspace", "cq_embed_grad", "cq_add_rms_norm",
+                     "cq_add_rms_norm_q8", "cq_rms_norm_grad_workspace", "cq_rms_norm_grad", "cq_q8_levels",
+                     "cq_dequant_gemm_q8_workspace", "cq_dequant_gemm_q8"):
+            getattr(L, name).restype = i32
         for name in ("cq_layout", "cq_model_bytes", "cq_codebook", "cq_codebook_train", "cq_quantize", "cq_dequantize",
                      "cq_fake_quant", "cq_dequant_matvec", "cq_dequant_matvec_many",
                      "cq_dequant_matvec_many_noalloc", "cq_blob_layout",
@@ -476,3 +501,281 @@ def repack(src, src_bits: int, dst_bits: int, dst=None, group_size: int = GROUP,
     _check("cq_repack", lib().cq_repack(_ptr(src), src_bits, _ptr(dst), dst_bits, n_groups, group_size,
                                         _stream_ptr(stream)))
     return dst
+
+
+# -- around the products: embedding, norm, 8-bit activations ---------------------
+
+class _On:
+    """The device and stream of a call: `with _On(tensors, stream) as s:` makes
+    the tensors' device (and a given stream) current, so that what the body
+    allocates belongs to that stream, and yields the stream pointer.  Tensors
+    handed to a stream other than the current one are recorded on it."""
+    __slots__ = ("stream", "tensors", "guards")
+
+    def __init__(self, tensors, stream):
+        self.tensors, self.stream, self.guards = tensors, stream, []
+
+    def __enter__(self):
+        import torch
+        dev = None
+        for name, t in self.tensors:
+            if t is None:
+                continue
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be a CUDA tensor")
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
+        if dev.index != torch.cuda.current_device():
+            self._push(torch.cuda.device(dev))
+        if self.stream is not None:
+            if self.stream.device != dev:
+                self.__exit__(None, None, None)
+                raise ValueError(f"the stream is on {self.stream.device}, the tensors on {dev}")
+            if self.stream != torch.cuda.current_stream():
+                self._push(torch.cuda.stream(self.stream))
+                for _, t in self.tensors:
+                    if t is not None:
+                        t.record_stream(self.stream)
+        return torch.cuda.current_stream().cuda_stream
+
+    def _push(self, guard):
+        guard.__enter__()
+        self.guards.append(guard)
+
+    def __exit__(self, *exc):
+        while self.guards:
+            self.guards.pop().__exit__(*exc)
+        return False
+
+
+def _dtype_code(name, t_or_dtype) -> int:
+    import torch
+    dt = getattr(t_or_dtype, "dtype", t_or_dtype)
+    if dt == torch.float32:
+        return F32
+    if dt == torch.bfloat16:
+        return BF16
+    raise TypeError(f"{name}: unsupported dtype {dt}")
+
+
+def _out_tensor(name, given, shape, dtype, device):
+    """`given` if it has the wanted shape and dtype, or a new tensor."""
+    import torch
+    if given is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if given.dtype != dtype or tuple(given.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, got {given.dtype} {tuple(given.shape)}")
+    return given
+
+
+def _opt(t):
+    return None if t is None else t.data_ptr()
+
+
+def _token_bytes(tokens) -> int:
+    import torch
+    if tokens.dtype == torch.int64:
+        return 8
+    if tokens.dtype == torch.int32:
+        return 4
+    raise TypeError(f"tokens must be int32 or int64, got {tokens.dtype}")
+
+
+def _workspace(query, args, given, device):
+    """(tensor or None, bytes) for a call that needs `query(*args)` bytes."""
+    import torch
+    need = ctypes.c_int64()
+    _check(query, getattr(lib(), query)(*args, ctypes.byref(need)))
+    if given is not None:
+        return given, given.numel() * given.element_size()
+    return (torch.empty(need.value, dtype=torch.uint8, device=device) if need.value else None), need.value
+
+
+def embed(tokens, table, scale: float = 1.0, out_dtype=None, out=None, stream=None):
+    """scale * table[tokens] for int32 or int64 tokens of any shape and a
+    [vocab, dim] float32 or bfloat16 table: [*tokens.shape, dim] in out_dtype
+    (default: the table's).  Tokens outside the table give zero rows."""
+    if table.dim() != 2:
+        raise ValueError("table must be [vocab, dim]")
+    tb, td = _token_bytes(tokens), _dtype_code("table", table)
+    od = table.dtype if out_dtype is None else out_dtype
+    oc = _dtype_code("out_dtype", od)
+    vocab, dim = table.shape
+    with _On((("table", table), ("tokens", tokens), ("out", out)), stream) as s:
+        out = _out_tensor("out", out, (*tokens.shape, dim), od, table.device)
+        _check("cq_embed", lib().cq_embed(tokens.data_ptr(), tb, tokens.numel(), table.data_ptr(), td, vocab, dim, scale,
+                                          out.data_ptr(), oc, s))
+    return out
+
+
+def embed_packed(tokens, packed, norms, vocab: int, dim: int, bits: int, levels, scale: float = 1.0, out_dtype=None,
+                 group_size: int = GROUP, out=None, stream=None):
+    """The same lookup from the CQ form of a [vocab, dim] table (packed and
+    norms as quantize() returns them): scale * the dequantized rows, float32
+    by default or bfloat16."""
+    import torch
+    tb = _token_bytes(tokens)
+    od = torch.float32 if out_dtype is None else out_dtype
+    oc = _dtype_code("out_dtype", od)
+    _check_stored(packed, norms, vocab, dim, bits, group_size)
+    lv, lvp = _levels_arg(levels)
+    with _On((("packed", packed), ("norms", norms), ("tokens", tokens), ("out", out)), stream) as s:
+        out = _out_tensor("out", out, (*tokens.shape, dim), od, packed.device)
+        _check("cq_embed_packed", lib().cq_embed_packed(
+            tokens.data_ptr(), tb, tokens.numel(), packed.data_ptr(), norms.data_ptr(), vocab, dim, bits, group_size, lvp,
+            _nlev(lv), scale, out.data_ptr(), oc, s))
+    return out
+
+
+def _check_stored(packed, norms, rows, cols, bits, group_size):
+    """The stored form's tensors hold what the call will read."""
+    import torch
+    if group_size < 1 or rows < 0 or cols < 0:
+        raise ValueError("negative size")
+    ng = rows * -(-cols // group_size)
+    if packed.dtype != torch.uint8 or packed.numel() != ng * group_bytes(bits, group_size):
+        raise ValueError(f"packed must hold {ng * group_bytes(bits, group_size)} uint8 values")
+    if norms.dtype != torch.float16 or norms.numel() != ng:
+        raise ValueError(f"norms must hold {ng} float16 values")
+
+
+def embed_grad(tokens, dout, vocab: int, scale: float = 1.0, grad_dtype=None, grad=None, accumulate: bool = False,
+               workspace=None, stream=None):
+    """Gradient of the lookup with respect to the [vocab, dim] table:
+    row v is scale * the sum of dout over the positions with token v (dout
+    [*tokens.shape, dim], float32 or bfloat16).  grad_dtype float32 by default;
+    accumulate=True adds to the given `grad`."""
+    import torch
+    tb, dd = _token_bytes(tokens), _dtype_code("dout", dout)
+    if tuple(dout.shape[:-1]) != tuple(tokens.shape):
+        raise ValueError(f"dout must be [*{tuple(tokens.shape)}, dim], got {tuple(dout.shape)}")
+    if accumulate and grad is None:
+        raise ValueError("accumulate needs grad")
+    gd = grad.dtype if grad is not None else torch.float32 if grad_dtype is None else grad_dtype
+    gc = _dtype_code("grad", gd)
+    n, dim = tokens.numel(), dout.shape[-1]
+    with _On((("dout", dout), ("tokens", tokens), ("grad", grad), ("workspace", workspace)), stream) as s:
+        grad = _out_tensor("grad", grad, (vocab, dim), gd, dout.device)
+        ws, wb = _workspace("cq_embed_grad_workspace", (n, vocab, dim), workspace, dout.device)
+        _check("cq_embed_grad", lib().cq_embed_grad(
+            tokens.data_ptr(), tb, n, dout.data_ptr(), dd, vocab, dim, scale, int(bool(accumulate)), grad.data_ptr(), gc,
+            _opt(ws), wb, s))
+    return grad
+
+
+def _norm_args(x, residual, weight, sum_out):
+    xd = _dtype_code("x", x)
+    rows, cols = _rows_cols(x.shape)
+    for name, t in (("residual", residual), ("sum_out", sum_out)):
+        if t is not None and (t.dtype != x.dtype or t.shape != x.shape):
+            raise ValueError(f"{name} must be {x.dtype} of shape {tuple(x.shape)}")
+    return xd, rows, cols, _weight_code(weight, cols)
+
+
+def _weight_code(weight, cols):
+    if weight is None:
+        return F32
+    if weight.numel() != cols:
+        raise ValueError(f"weight must hold {cols} values")
+    return _dtype_code("weight", weight)
+
+
+def add_rms_norm(x, residual=None, weight=None, eps: float = 1e-6, out_dtype=None, sum_out=None, out=None, stream=None):
+    """(out, sum): sum = x + residual and out = its root-mean-square norm over
+    the last axis times weight.  x and residual float32 or bfloat16 of one
+    shape, weight float32 or bfloat16 [cols] (None: ones).  sum has x's dtype
+    and is x itself without a residual; sum_out may be x or residual.  out is
+    out_dtype (default x's)."""
+    import torch
+    xd, rows, cols, wd = _norm_args(x, residual, weight, sum_out)
+    od = x.dtype if out_dtype is None else out_dtype
+    oc = _dtype_code("out_dtype", od)
+    with _On((("x", x), ("residual", residual), ("weight", weight), ("sum_out", sum_out), ("out", out)), stream) as s:
+        if sum_out is None and residual is not None:
+            sum_out = torch.empty_like(x)
+        out = _out_tensor("out", out, x.shape, od, x.device)
+        _check("cq_add_rms_norm", lib().cq_add_rms_norm(
+            x.data_ptr(), _opt(residual), xd, _opt(weight), wd, rows, cols, eps, _opt(sum_out), out.data_ptr(), oc, s))
+    return out, x if sum_out is None else sum_out
+
+
+def add_rms_norm_q8(x, residual=None, weight=None, eps: float = 1e-6, group_size: int = GROUP, sum_out=None, q=None,
+                    scale=None, stream=None):
+    """(q, scale, sum): add_rms_norm with its output rotated per group and
+    held in 8 bits: q int8 of x's shape, scale float32 [*x.shape[:-1]]; q *
+    scale are the rotated activations that dequant_gemm_q8 reads."""
+    import torch
+    xd, rows, cols, wd = _norm_args(x, residual, weight, sum_out)
+    with _On((("x", x), ("residual", residual), ("weight", weight), ("sum_out", sum_out), ("q", q), ("scale", scale)),
+             stream) as s:
+        if sum_out is None and residual is not None:
+            sum_out = torch.empty_like(x)
+        q = _out_tensor("q", q, x.shape, torch.int8, x.device)
+        scale = _out_tensor("scale", scale, x.shape[:-1], torch.float32, x.device)
+        _check("cq_add_rms_norm_q8", lib().cq_add_rms_norm_q8(
+            x.data_ptr(), _opt(residual), xd, _opt(weight), wd, rows, cols, group_size, eps, _opt(sum_out), q.data_ptr(),
+            scale.data_ptr(), s))
+    return q, scale, x if sum_out is None else sum_out
+
+
+def rms_norm_grad(dout, sum, weight=None, dsum=None, eps: float = 1e-6, dx=None, dweight=None, workspace=None,
+                  stream=None):
+    """(dx, dweight) of add_rms_norm at its sum: dx (for x and residual alike)
+    in sum's dtype, dweight float32 [cols].  dout and dsum (the gradient that
+    reaches sum by other ways, None: zero) have sum's dtype and shape; dx may
+    be dsum."""
+    import torch
+    sd = _dtype_code("sum", sum)
+    for name, t in (("dout", dout), ("dsum", dsum), ("dx", dx)):
+        if t is not None and (t.dtype != sum.dtype or t.shape != sum.shape):
+            raise ValueError(f"{name} must be {sum.dtype} of shape {tuple(sum.shape)}")
+    rows, cols = _rows_cols(sum.shape)
+    wd = _weight_code(weight, cols)
+    with _On((("sum", sum), ("dout", dout), ("weight", weight), ("dsum", dsum), ("dx", dx), ("dweight", dweight),
+              ("workspace", workspace)), stream) as s:
+        dx = torch.empty_like(sum) if dx is None else dx
+        dweight = _out_tensor("dweight", dweight, (cols,), torch.float32, sum.device)
+        ws, wb = _workspace("cq_rms_norm_grad_workspace", (rows, cols, sd), workspace, sum.device)
+        _check("cq_rms_norm_grad", lib().cq_rms_norm_grad(
+            dout.data_ptr(), sum.data_ptr(), _opt(dsum), sd, _opt(weight), wd, rows, cols, eps, dx.data_ptr(),
+            dweight.data_ptr(), _opt(ws), wb, s))
+    return dx, dweight
+
+
+def q8_levels(bits: int, levels=None) -> Q8Table:
+    """The 16-bit form of a codebook (None: the built-in one) that
+    dequant_gemm_q8 multiplies with; made once per codebook."""
+    table = Q8Table()
+    lv, lvp = _levels_arg(levels)
+    _check("cq_q8_levels", lib().cq_q8_levels(bits, lvp, _nlev(lv), ctypes.byref(table)))
+    return table
+
+
+def dequant_gemm_q8(packed, norms, n_out: int, k: int, bits: int, table: Q8Table, q, scale, group_size: int = GROUP,
+                    out_dtype=None, y=None, workspace=None, stream=None):
+    """y = x . W_hat^T with W the quantized n_out x k matrix and x given as
+    add_rms_norm_q8 writes it (q int8 [..., k], scale float32 [...]): [...,
+    n_out], float32 by default or bfloat16."""
+    import torch
+    od = torch.float32 if out_dtype is None else out_dtype
+    oc = _dtype_code("out_dtype", od)
+    if not isinstance(table, Q8Table):
+        raise TypeError("table must come from q8_levels()")
+    if q.dtype != torch.int8 or q.dim() < 1 or q.shape[-1] != k:
+        raise ValueError(f"q must be int8 [..., {k}], got {q.dtype} {tuple(q.shape)}")
+    if scale.dtype != torch.float32 or scale.shape != q.shape[:-1]:
+        raise ValueError(f"scale must be float32 {tuple(q.shape[:-1])}, got {scale.dtype} {tuple(scale.shape)}")
+    _check_stored(packed, norms, n_out, k, bits, group_size)
+    batch = scale.numel()
+    with _On((("packed", packed), ("norms", norms), ("q", q), ("scale", scale), ("y", y), ("workspace", workspace)),
+             stream) as s:
+        y = _out_tensor("y", y, (*q.shape[:-1], n_out), od, q.device)
+        ws, wb = _workspace("cq_dequant_gemm_q8_workspace", (n_out, k, batch, group_size), workspace, q.device)
+        _check("cq_dequant_gemm_q8", lib().cq_dequant_gemm_q8(
+            packed.data_ptr(), norms.data_ptr(), n_out, k, bits, group_size, ctypes.byref(table), q.data_ptr(),
+            scale.data_ptr(), batch, y.data_ptr(), oc, _opt(ws), wb, s))
+    return y

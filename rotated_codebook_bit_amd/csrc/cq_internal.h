@@ -620,4 +620,101 @@ hipError_t launch_gemm(const GemmDesc* table, const int64_t* bstart, int n, int6
                        const SplitLevels& sl, const uint16_t* ws, int64_t batch, int group_size,
                        hipStream_t stream);
 
+// ---- Norm (norm.hip) ------------------------------------------------------------
+
+constexpr int64_t kNormMaxCols = 32768;  // a row stays in the registers of at most 16 waves
+constexpr int kNormGradBlocks = 512;     // two per CU: shares of the weight gradient
+
+// All row-major [rows][cols], x's type unless said; out is float32 or bf16.
+// q != null: the 8-bit form (out unused), labels = lanes per rotated group,
+// unit = the factor from the largest unnormalised rotated magnitude to the
+// scale, 1 / (127 sqrt(G)).
+struct NormArgs {
+  const uint8_t* x;
+  const uint8_t* residual;  // null: none
+  const void* weight;       // null: ones
+  int w_bf16;
+  int64_t rows, cols;
+  float eps;
+  uint8_t* sum;  // null: not stored
+  uint8_t* out;
+  int out_bf16;
+  int8_t* q;
+  float* scale;
+  int labels;
+  float unit;
+};
+hipError_t launch_norm(const NormArgs& a, bool bf16, hipStream_t stream);
+
+struct NormGradArgs {
+  const uint8_t* dout;
+  const uint8_t* sum;
+  const uint8_t* dsum;  // null: zero
+  const void* weight;   // null: ones
+  int w_bf16;
+  int64_t rows, cols;
+  float eps;
+  uint8_t* dx;
+  float* part;  // set by the launcher
+};
+// ws: norm_grad_blocks * cols floats (unused for one block or no dweight).
+int norm_grad_blocks(int64_t rows, int64_t cols, bool bf16);
+hipError_t launch_norm_grad(NormGradArgs a, bool bf16, float* dweight, float* ws, hipStream_t stream);
+
+// ---- Embedding lookup and its gradient (embed.hip) ----------------------------------
+
+// Token ids of 4 or 8 bytes; an id outside [0, vocab) stands for no row.
+struct EmbedArgs {
+  const void* tokens;
+  int token_bytes;
+  int64_t n, vocab, dim;
+  float scale;
+  const uint8_t* table;  // dense: [vocab][dim]
+  int table_bf16;
+  const uint8_t* packed;  // CQ: the codec's layout, bytes per group gbytes
+  const uint16_t* norms;
+  int group, gbytes;
+  uint8_t* out;
+  int out_bf16;
+};
+hipError_t launch_embed(const EmbedArgs& a, hipStream_t stream);
+// storage: field width 2, 3, 4, or kTritStorage.
+hipError_t launch_embed_packed(const EmbedArgs& a, int storage, const LevelTable& lv, hipStream_t stream);
+
+struct EmbedGradArgs {
+  const void* tokens;
+  int token_bytes;
+  int64_t n, vocab, dim;
+  float scale;
+  const uint8_t* dout;  // [n][dim]
+  int dout_bf16;
+  uint8_t* grad;  // [vocab][dim]
+  int grad_bf16;
+  int accumulate;
+};
+int64_t embed_grad_workspace(int64_t n, int64_t vocab, int64_t dim);
+hipError_t launch_embed_grad(const EmbedGradArgs& a, uint8_t* ws, hipStream_t stream);
+
+// ---- Product of 8-bit activations (gemm_q8.hip) ---------------------------------------
+
+// levels ~ scale * (256 hi + lo), four per dword.
+struct Q8Levels {
+  uint32_t hi[4], lo[4];
+  float scale;
+};
+constexpr int64_t kQ8MaxK = int64_t(1) << 22;  // 32-bit offsets within a tile of rows
+struct GemmQ8Args {
+  const uint8_t* packed;
+  const uint16_t* norms;
+  int64_t n_out, k, batch;
+  const int8_t* q;     // [batch][k]
+  const float* scale;  // [batch]
+  uint8_t* y;          // [batch][n_out]
+  int y_bf16;
+};
+int64_t gemm_q8_workspace(int64_t n_out, int64_t k, int64_t batch, int group_size);
+hipError_t launch_gemm_q8_empty(const GemmQ8Args& a, hipStream_t stream);  // k = 0: zeros
+hipError_t launch_gemm_q8(const GemmQ8Args& a, int sbits, int group_size, const Q8Levels& lv, float* ws,
+                          hipStream_t stream);
+
 }  // namespace cq

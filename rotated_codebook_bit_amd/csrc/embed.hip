@@ -1,0 +1,752 @@
+// Embedding lookup with scaling, from floating-point rows or straight from CQ
+// storage, and the gradient of the table by sorted tokens.
+//
+// Lookup: out[i] = scale * W[token i].  From CQ storage a row is decoded as
+// dequantization decodes it ("Cactus Quants CQ2-bit Quantization: Extreme
+// Compression for Edge LLMs", section The CQ2-bit Implementation Pipeline):
+// (norm / G) H levels[idx] per group, H the +-1 Sylvester matrix, in one pass
+// from packed bytes to scaled output.  A lane owns 16 bytes of output (4
+// float32 or 8 bf16 columns), so a wave's store instruction writes whole
+// kilobytes; a group lies over G / 4 or G / 8 lanes, its first butterfly
+// stages inside a lane and the rest between lanes (lanes.h).
+//
+// Gradient: grad[v] = scale * sum of dout[i] over the positions i with
+// token i = v, added in position order.  The positions are sorted by token
+// (a stable radix sort), so that every table row is written once, by one
+// wave per 256 columns, with no atomics and no order that changes between
+// runs.  Tokens that occur more than kSegment times are cut into pieces of
+// the sorted list, whose sums are added in order afterwards.
+#include <utility>
+
+#include "lanes.h"
+
+namespace cq {
+namespace {
+
+constexpr int kBlock = 256;
+constexpr int kWaves = kBlock / kWave;
+
+__device__ __forceinline__ int64_t token_at(const void* tokens, int bytes, int64_t i) {
+  return bytes == 8 ? static_cast<const int64_t*>(tokens)[i] : static_cast<const int32_t*>(tokens)[i];
+}
+
+// E consecutive output columns from column c of a row of dim columns; WIDE:
+// rows start on and hold whole 16-byte pieces.
+template <bool BF16, int E, bool WIDE>
+__device__ __forceinline__ void store_columns(uint8_t* row, int64_t c, int64_t dim, const float (&v)[E]) {
+  if constexpr (WIDE) {
+    if (c >= dim) return;
+    constexpr int V = Piece<BF16>::kElems;
+    uint4* o = reinterpret_cast<uint4*>(row + c * Piece<BF16>::kBytes);
+#pragma unroll
+    for (int i = 0; i < E / V; ++i) o[i] = pack_piece<BF16>(v + i * V);
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; ++i)
+      if (c + i < dim) store_elem<BF16>(row, c + i, v[i]);
+  }
+}
+
+// ---- Dense lookup -----------------------------------------------------------------
+
+// One wave per unit: 64 E columns of one token's row, E = 8 when either type
+// is bf16, else 4.
+template <bool IN16, bool OUT16, bool WIDE>
+__global__ void __launch_bounds__(kBlock)
+embed_kernel(EmbedArgs a, int64_t units, uint32_t per_row) {
+  constexpr int E = IN16 || OUT16 ? 8 : 4, V = Piece<IN16>::kElems;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int64_t u = static_cast<int64_t>(blockIdx.x) * kWaves +
+                    __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  if (u >= units) return;
+  const int64_t i = u / per_row;
+  const int64_t c = ((u - i * per_row) * kWave + lane) * E;
+  const int64_t tok = token_at(a.tokens, a.token_bytes, i);
+  const bool in = tok >= 0 && tok < a.vocab;
+  float v[E];
+  if (in) {
+    const uint8_t* row = a.table + tok * a.dim * Piece<IN16>::kBytes;
+    if constexpr (WIDE) {
+      const int64_t cc = c < a.dim ? c : 0;
+#pragma unroll
+      for (int k = 0; k < E / V; ++k)
+        unpack_piece<IN16>(reinterpret_cast<const uint4*>(row + cc * Piece<IN16>::kBytes)[k], v + k * V);
+    } else {
+#pragma unroll
+      for (int k = 0; k < E; ++k) v[k] = load_elem<IN16>(row, c + k < a.dim ? c + k : 0);
+    }
+#pragma unroll
+    for (int k = 0; k < E; ++k) v[k] *= a.scale;
+  } else {
+#pragma unroll
+    for (int k = 0; k < E; ++k) v[k] = 0.0f;
+  }
+  store_columns<OUT16, E, WIDE>(a.out + i * a.dim * Piece<OUT16>::kBytes, c, a.dim, v);
+}
+
+// ---- Lookup from CQ storage ----------------------------------------------------------
+
+// The E codes of columns `within` .. of a group at p (gbytes long), as bit
+// fields from bit 0 (trit storage: 2-bit fields).
+template <int SB, int E>
+__device__ __forceinline__ uint32_t load_codes(const uint8_t* p, int within, int gbytes, const uint16_t* trits) {
+  if constexpr (SB == kTritStorage) {
+    const int b = within / 5, last = gbytes - 1;
+    uint32_t f = trits[p[b]] | (static_cast<uint32_t>(trits[p[b + 1 < last ? b + 1 : last]]) << 10);
+    if constexpr (E == 8) f |= static_cast<uint32_t>(trits[p[b + 2 < last ? b + 2 : last]]) << 20;
+    return f >> (2 * (within - 5 * b));
+  } else if constexpr (SB == 3) {
+    const uint8_t* b = p + (within * 3) / 8;
+    if constexpr (E == 8) return b[0] | (b[1] << 8) | (static_cast<uint32_t>(b[2]) << 16);
+    return (b[0] | (b[1] << 8)) >> ((within * 3) & 7);
+  } else {
+    const uint8_t* b = p + (within * SB) / 8;
+    if constexpr (SB * E == 8) return *b;
+    if constexpr (SB * E == 16) return *reinterpret_cast<const uint16_t*>(b);
+    return *reinterpret_cast<const uint32_t*>(b);
+  }
+}
+
+// P units of 64 E columns per wave, their loads issued together.
+template <int SB, bool OUT16, bool WIDE, int P>
+__global__ void __launch_bounds__(kBlock)
+embed_packed_kernel(EmbedArgs a, LevelTable lv, int64_t units, uint32_t per_row) {
+  constexpr int E = OUT16 ? 8 : 4;
+  constexpr int FB = SB == kTritStorage ? 2 : SB;
+  __shared__ float tab[kMaxLevels];  // 16 banks: any mix of codes reads without conflict
+  __shared__ uint16_t trits[SB == kTritStorage ? 256 : 1];
+  if (threadIdx.x < kMaxLevels) {
+    const float l = level_at(lv, threadIdx.x);
+    tab[threadIdx.x] = l;
+    wait_lds_writes();
+    hold_value(l);
+  }
+  if constexpr (SB == kTritStorage) {
+    const uint32_t f = trit_table_entry(threadIdx.x);
+    trits[threadIdx.x] = static_cast<uint16_t>(f);
+    wait_lds_writes();
+    hold_value(f);
+  }
+  __syncthreads();
+  const int lane = threadIdx.x & (kWave - 1), label = lane_label(lane);
+  const int64_t u0 = (static_cast<int64_t>(blockIdx.x) * kWaves +
+                      __builtin_amdgcn_readfirstlane(threadIdx.x / kWave)) * P;
+  const int shift = __builtin_ctz(a.group);
+  const int64_t ngr = (a.dim + a.group - 1) >> shift, row_bytes = ngr * a.gbytes;
+  uint32_t raw[P];
+  float f[P];
+  int64_t col[P], tok_i[P];
+#pragma unroll
+  for (int j = 0; j < P; ++j) {
+    const int64_t u = u0 + j < units ? u0 + j : units - 1;
+    const int64_t i = u / per_row;
+    const int64_t c = ((u - i * per_row) * kWave + label) * E;
+    const int64_t tok = token_at(a.tokens, a.token_bytes, i);
+    tok_i[j] = i;
+    col[j] = c;
+    raw[j] = 0;
+    f[j] = 0.0f;
+    if (tok >= 0 && tok < a.vocab) {
+      int64_t g = c >> shift;
+      const int within = g < ngr ? static_cast<int>(c & (a.group - 1)) : 0;
+      g = g < ngr ? g : 0;
+      raw[j] = load_codes<SB, E>(a.packed + tok * row_bytes + g * a.gbytes, within, a.gbytes, trits);
+      f[j] = static_cast<float>(__builtin_bit_cast(_Float16, a.norms[tok * ngr + g]));
+    }
+  }
+  const float unit = a.scale / static_cast<float>(a.group);
+#pragma unroll
+  for (int j = 0; j < P; ++j) {
+    float y[E];
+#pragma unroll
+    for (int k = 0; k < E; ++k) y[k] = tab[(raw[j] >> (FB * k)) & ((1u << FB) - 1u)];
+    lane_butterfly(y);
+    label_butterfly(y, label, a.group / E);
+    const float s = f[j] * unit;
+    // A token outside the table has a zero row, whatever its codes decode to.
+#pragma unroll
+    for (int k = 0; k < E; ++k) y[k] = s == 0.0f ? 0.0f : y[k] * s;
+    if (u0 + j < units)
+      store_columns<OUT16, E, WIDE>(a.out + tok_i[j] * a.dim * Piece<OUT16>::kBytes, col[j], a.dim, y);
+  }
+}
+
+// ---- Gradient: sorting the positions by token --------------------------------------------
+
+constexpr int kDigit = 256;       // 8-bit digits, least significant first
+constexpr int kSortTile = 4096;   // keys per block of the many-block sort
+constexpr int kSortOne = 16384;   // keys that one block sorts by itself
+
+// Sort key: the token, or vocab (past every row) where it is outside the table.
+__device__ __forceinline__ uint32_t token_key(const EmbedGradArgs& a, int64_t i) {
+  const int64_t t = token_at(a.tokens, a.token_bytes, i);
+  return static_cast<uint32_t>(t >= 0 && t < a.vocab ? t : a.vocab);
+}
+
+// Lanes of the wave whose digit equals this lane's.
+__device__ __forceinline__ uint64_t same_digit(uint32_t d) {
+  uint64_t m = ~0ull;
+#pragma unroll
+  for (int b = 0; b < 8; ++b) {
+    const bool one = (d >> b) & 1u;
+    const uint64_t v = __ballot(one);
+    m &= one ? v : ~v;
+  }
+  return m;
+}
+
+// Ranks a wave's keys digit by digit in order: rank = keys of the same digit
+// seen before by this wave.  hist: the wave's 256 counters in LDS, zeroed.
+// volatile: other lanes of the wave change them between steps (the LDS serves
+// a wave's operations in order).
+template <int IPT>
+__device__ __forceinline__ void rank_keys(const uint32_t (&key)[IPT], int shift, volatile uint32_t* hist,
+                                          uint32_t (&rank)[IPT]) {
+  const int lane = threadIdx.x & (kWave - 1);
+#pragma unroll
+  for (int i = 0; i < IPT; ++i) {
+    const uint32_t d = (key[i] >> shift) & (kDigit - 1);
+    const uint64_t m = same_digit(d);
+    const uint32_t below = __popcll(m & ((1ull << lane) - 1ull));
+    const uint32_t base = hist[d];
+    rank[i] = base + below;
+    const uint32_t next = base + static_cast<uint32_t>(__popcll(m));
+    if (below == 0) hist[d] = next;
+    wait_lds_writes();
+    hold_value(next);
+  }
+}
+
+// Exclusive sum over the first 256 threads' values (one per digit).
+__device__ __forceinline__ uint32_t digit_scan(uint32_t v, uint32_t* part) {
+  const int t = threadIdx.x, lane = t & (kWave - 1);
+  uint32_t x = v;
+#pragma unroll
+  for (int h = 1; h < kWave; h <<= 1) {
+    const uint32_t o = __shfl_up(x, h, kWave);
+    if (lane >= h) x += o;
+  }
+  if (t < kDigit && lane == kWave - 1) {
+    part[t / kWave] = x;
+  }
+  wait_lds_writes();
+  hold_value(x);
+  __syncthreads();
+  uint32_t before = 0;
+  if (t < kDigit)
+    for (int w = 0; w < t / kWave; ++w) before += part[w];
+  return before + x - v;
+}
+
+// The whole sort in one block of 16 waves: wave w holds the keys
+// 64 IPT w .. of the current order, IPT per lane.  Positions past n carry the
+// largest key and stay last.
+constexpr int kOneThreads = 1024, kOneWaves = kOneThreads / kWave;
+template <int IPT>
+__global__ void __launch_bounds__(kOneThreads)
+sort_one_kernel(EmbedGradArgs a, int passes, uint32_t* __restrict__ keys, uint32_t* __restrict__ order) {
+  __shared__ uint32_t hist[kOneWaves][kDigit];
+  __shared__ uint32_t part[kDigit / kWave];
+  __shared__ uint32_t xkey[kOneThreads * IPT];
+  __shared__ uint32_t xpos[kOneThreads * IPT];
+  const int t = threadIdx.x, lane = t & (kWave - 1), wave = t / kWave;
+  const int first = wave * kWave * IPT + lane;
+  const int n = static_cast<int>(a.n);
+  uint32_t key[IPT], pos[IPT], rank[IPT];
+#pragma unroll
+  for (int i = 0; i < IPT; ++i) {
+    const int p = first + i * kWave;
+    pos[i] = p;
+    key[i] = p < n ? token_key(a, p) : 0xFFFFFFFFu;
+  }
+  const uint32_t zero = 0;
+  for (int pass = 0; pass < passes; ++pass) {
+    for (int i = t; i < kOneWaves * kDigit; i += kOneThreads) hist[i / kDigit][i % kDigit] = zero;
+    wait_lds_writes();
+    hold_value(zero);
+    __syncthreads();
+    rank_keys<IPT>(key, 8 * pass, hist[wave], rank);
+    __syncthreads();
+    uint32_t total = 0;
+    if (t < kDigit) {
+#pragma unroll
+      for (int w = 0; w < kOneWaves; ++w) total += hist[w][t];
+    }
+    uint32_t run = digit_scan(total, part);
+    if (t < kDigit) {
+#pragma unroll 1
+      for (int w = 0; w < kOneWaves; w += 4) {  // four at a time: registers
+        uint32_t at[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          at[i] = run;
+          run += hist[w + i][t];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) hist[w + i][t] = at[i];
+        wait_lds_writes();
+        hold_values(at[0], at[1], at[2], at[3]);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < IPT; ++i) {
+      const uint32_t to = rank[i] + hist[wave][(key[i] >> (8 * pass)) & (kDigit - 1)];
+      xkey[to] = key[i];
+      xpos[to] = pos[i];
+    }
+    wait_lds_writes();
+#pragma unroll
+    for (int i = 0; i < IPT; ++i) hold_values(key[i], pos[i]);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < IPT; ++i) {
+      key[i] = xkey[first + i * kWave];
+      pos[i] = xpos[first + i * kWave];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < IPT; ++i) {
+    const int p = first + i * kWave;
+    if (p < n) {
+      keys[p] = key[i];
+      order[p] = pos[i];
+    }
+  }
+}
+
+// One pass of the many-block sort.  count_kernel leaves every tile's digit
+// counts in counts[tile][256]; scatter_kernel adds the counts of smaller
+// digits and of earlier tiles itself (tiles * 1 KiB from the L2, a fraction
+// of a tile's own keys up to thousands of tiles) and moves its tile's keys.
+constexpr int kTileIpt = kSortTile / kBlock;
+
+__device__ __forceinline__ void tile_keys(const EmbedGradArgs& a, const uint32_t* keys, const uint32_t* order,
+                                          uint32_t (&key)[kTileIpt], uint32_t (&pos)[kTileIpt]) {
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+#pragma unroll
+  for (int i = 0; i < kTileIpt; ++i) {
+    const int64_t p = static_cast<int64_t>(blockIdx.x) * kSortTile + (wave * kTileIpt + i) * kWave + lane;
+    const bool in = p < a.n;
+    const int64_t pc = in ? p : 0;
+    key[i] = keys ? keys[pc] : token_key(a, pc);
+    pos[i] = order ? order[pc] : static_cast<uint32_t>(pc);
+    if (!in) key[i] = 0xFFFFFFFFu;
+  }
+}
+
+__global__ void __launch_bounds__(kBlock)
+count_kernel(EmbedGradArgs a, int shift, const uint32_t* __restrict__ keys, uint32_t* __restrict__ counts) {
+  __shared__ uint32_t hist[kDigit];
+  const uint32_t zero = 0;
+  hist[threadIdx.x] = zero;
+  wait_lds_writes();
+  hold_value(zero);
+  __syncthreads();
+  uint32_t key[kTileIpt], pos[kTileIpt];
+  tile_keys(a, keys, nullptr, key, pos);
+  const uint32_t one = 1;
+#pragma unroll
+  for (int i = 0; i < kTileIpt; ++i) atomicAdd(&hist[(key[i] >> shift) & (kDigit - 1)], one);
+  wait_lds_writes();
+  hold_value(one);
+  __syncthreads();
+  counts[static_cast<int64_t>(blockIdx.x) * kDigit + threadIdx.x] = hist[threadIdx.x];
+}
+
+__global__ void __launch_bounds__(kBlock)
+scatter_kernel(EmbedGradArgs a, int shift, const uint32_t* __restrict__ counts, const uint32_t* __restrict__ keys,
+               const uint32_t* __restrict__ order, uint32_t* __restrict__ keys_out, uint32_t* __restrict__ order_out) {
+  __shared__ uint32_t hist[kWaves][kDigit];
+  __shared__ uint32_t part[kDigit / kWave];
+  const int t = threadIdx.x, wave = t / kWave;
+  const uint32_t zero = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) hist[w][t] = zero;
+  wait_lds_writes();
+  hold_value(zero);
+  __syncthreads();
+  uint32_t key[kTileIpt], pos[kTileIpt], rank[kTileIpt];
+  tile_keys(a, keys, order, key, pos);
+  rank_keys<kTileIpt>(key, shift, hist[wave], rank);
+  uint32_t before = 0, total = 0;  // of digit t: in earlier tiles, in all
+#pragma unroll 8
+  for (uint32_t b = 0; b < gridDim.x; ++b) {
+    const uint32_t c = counts[static_cast<int64_t>(b) * kDigit + t];
+    before += b < blockIdx.x ? c : 0u;
+    total += c;
+  }
+  __syncthreads();
+  uint32_t run = digit_scan(total, part) + before;
+  uint32_t at[kWaves];
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    at[w] = run;
+    run += hist[w][t];
+  }
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) hist[w][t] = at[w];
+  wait_lds_writes();
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) hold_value(at[w]);
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kTileIpt; ++i) {
+    const uint32_t to = rank[i] + hist[wave][(key[i] >> shift) & (kDigit - 1)];
+    // Slots past n (only the last tile has them) carry the largest key: they
+    // rank last and land past n.
+    if (to < a.n) {
+      keys_out[to] = key[i];
+      order_out[to] = pos[i];
+    }
+  }
+}
+
+// ---- Gradient: the sums -------------------------------------------------------------
+
+constexpr int kSegment = 64;   // longest run of one token that one wave adds by itself
+constexpr int kSlice = 256;    // columns per wave: four per lane
+constexpr int kRowsMax = 32;   // table rows per block
+
+// First sorted index whose key is at least v.
+__device__ __forceinline__ uint32_t lower_bound(const uint32_t* __restrict__ keys, uint32_t n, uint32_t v) {
+  uint32_t lo = 0, len = n;
+  while (len > 0) {
+    const uint32_t half = len / 2;
+    const bool right = keys[lo + half] < v;
+    lo = right ? lo + half + 1 : lo;
+    len = right ? len - half - 1 : half;
+  }
+  return lo;
+}
+
+// Four columns of lane `lane` in slice s: consecutive (WIDE), or 64 apart.
+template <bool WIDE>
+__device__ __forceinline__ int64_t slice_column(int64_t s, int lane, int k) {
+  return s * kSlice + (WIDE ? lane * 4 + k : k * kWave + lane);
+}
+
+template <bool BF16, bool WIDE>
+__device__ __forceinline__ void load_four(const uint8_t* row, int64_t s, int lane, int64_t dim, float (&v)[4]) {
+  if constexpr (WIDE) {
+    const int64_t c = slice_column<WIDE>(s, lane, 0), cc = c < dim ? c : 0;
+    if constexpr (BF16) {
+      const uint2 u = *reinterpret_cast<const uint2*>(row + cc * 2);
+      v[0] = bf16_low(u.x);
+      v[1] = bf16_high(u.x);
+      v[2] = bf16_low(u.y);
+      v[3] = bf16_high(u.y);
+    } else {
+      unpack_piece<false>(*reinterpret_cast<const uint4*>(row + cc * 4), v);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t c = slice_column<WIDE>(s, lane, k);
+      v[k] = load_elem<BF16>(row, c < dim ? c : 0);
+    }
+  }
+}
+
+template <bool WIDE>
+__device__ __forceinline__ void store_four(uint8_t* row, bool bf16, int64_t s, int lane, int64_t dim,
+                                           const float (&v)[4]) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  if constexpr (WIDE) {
+    const int64_t c = slice_column<WIDE>(s, lane, 0);
+    if (c >= dim) return;
+    if (bf16) {
+      __builtin_nontemporal_store(u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])},
+                                  reinterpret_cast<u32x2*>(row + c * 2));
+    } else {
+      const uint4 p = pack_piece<false>(v);
+      __builtin_nontemporal_store(u32x4{p.x, p.y, p.z, p.w}, reinterpret_cast<u32x4*>(row + c * 4));
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t c = slice_column<WIDE>(s, lane, k);
+      if (c >= dim) continue;
+      if (bf16)
+        store_elem<true>(row, c, v[k]);
+      else
+        store_elem<false>(row, c, v[k]);
+    }
+  }
+}
+
+// Sum of dout rows order[lo .. hi) over one slice, in order.
+template <bool BF16, bool WIDE>
+__device__ __forceinline__ void add_rows(const EmbedGradArgs& a, const uint32_t* __restrict__ order, uint32_t lo,
+                                         uint32_t hi, int64_t s, int lane, float (&acc)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) acc[k] = 0.0f;
+  const int64_t bytes = a.dim * Piece<BF16>::kBytes;
+  uint32_t j = lo;
+  for (; j + 4 <= hi; j += 4) {
+    float v[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load_four<BF16, WIDE>(a.dout + order[j + i] * bytes, s, lane, a.dim, v[i]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[k] += v[i][k];
+  }
+  for (; j < hi; ++j) {
+    float v[4];
+    load_four<BF16, WIDE>(a.dout + order[j] * bytes, s, lane, a.dim, v);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k] += v[k];
+  }
+}
+
+// Scaled sum into grad row v (added to it when accumulating).
+template <bool WIDE>
+__device__ __forceinline__ void put_row(const EmbedGradArgs& a, int64_t v, int64_t s, int lane, float (&acc)[4]) {
+  uint8_t* row = a.grad + v * a.dim * (a.grad_bf16 ? 2 : 4);
+  float old[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (a.accumulate) {
+    if (a.grad_bf16)
+      load_four<true, WIDE>(row, s, lane, a.dim, old);
+    else
+      load_four<false, WIDE>(row, s, lane, a.dim, old);
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) acc[k] = a.accumulate ? __builtin_fmaf(acc[k], a.scale, old[k]) : acc[k] * a.scale;
+  store_four<WIDE>(row, a.grad_bf16, s, lane, a.dim, acc);
+}
+
+// Blocks [0, piece_blocks): piece c of kSegment sorted positions, 1024
+// columns.  A run longer than kSegment that meets the piece holds its first or
+// its last position; the sum of the run's part goes to slot 2c (the run of
+// the first position) or 2c + 1 (a later run, the last position's).
+// The other blocks: `rows` table rows each, all columns; runs of up to
+// kSegment positions are added and every absent row is cleared.
+template <bool BF16, bool WIDE>
+__global__ void __launch_bounds__(kBlock)
+embed_grad_kernel(EmbedGradArgs a, const uint32_t* __restrict__ keys, const uint32_t* __restrict__ order,
+                  float* __restrict__ partial, uint32_t piece_blocks, int rows) {
+  __shared__ uint32_t start[kRowsMax + 1];
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const uint32_t n = static_cast<uint32_t>(a.n);
+  const int64_t slices = (a.dim + kSlice - 1) / kSlice;
+  if (blockIdx.x < piece_blocks) {
+    const uint32_t per = static_cast<uint32_t>((slices + kWaves - 1) / kWaves);
+    const uint32_t c = blockIdx.x / per;
+    const int64_t s = static_cast<int64_t>(blockIdx.x - c * per) * kWaves + wave;
+    if (s >= slices) return;
+    const uint32_t lo = c * kSegment, hi = lo + kSegment < n ? lo + kSegment : n;
+    const uint32_t k0 = keys[lo], k1 = keys[hi - 1];
+    // Lanes 0 .. 3: where the runs of k0 and k1 begin and end.
+    const uint32_t b = lower_bound(keys, n, (lane & 2 ? k1 : k0) + (lane & 1));
+    const uint32_t s0 = __builtin_amdgcn_readlane(b, 0), e0 = __builtin_amdgcn_readlane(b, 1);
+    const uint32_t s1 = __builtin_amdgcn_readlane(b, 2), e1 = __builtin_amdgcn_readlane(b, 3);
+    float acc[4];
+    if (k0 < a.vocab && e0 - s0 > kSegment) {
+      add_rows<BF16, WIDE>(a, order, lo, e0 < hi ? e0 : hi, s, lane, acc);
+      store_four<WIDE>(reinterpret_cast<uint8_t*>(partial + 2 * static_cast<int64_t>(c) * a.dim), false, s, lane, a.dim, acc);
+    }
+    if (k1 != k0 && k1 < a.vocab && e1 - s1 > kSegment) {
+      add_rows<BF16, WIDE>(a, order, s1, hi, s, lane, acc);
+      store_four<WIDE>(reinterpret_cast<uint8_t*>(partial + (2 * static_cast<int64_t>(c) + 1) * a.dim), false, s, lane, a.dim, acc);
+    }
+    return;
+  }
+  const int64_t v0 = static_cast<int64_t>(blockIdx.x - piece_blocks) * rows;
+  const int here = a.vocab - v0 < rows ? static_cast<int>(a.vocab - v0) : rows;
+  if (threadIdx.x <= here) {
+    const uint32_t b = lower_bound(keys, n, static_cast<uint32_t>(v0 + threadIdx.x));
+    start[threadIdx.x] = b;
+    wait_lds_writes();
+    hold_value(b);
+  }
+  __syncthreads();
+  const int64_t units = here * slices;
+  for (int64_t u = wave; u < units; u += kWaves) {
+    const int r = static_cast<int>(u / slices);
+    const int64_t s = u - r * slices;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(start[r]), hi = __builtin_amdgcn_readfirstlane(start[r + 1]);
+    if (hi - lo > kSegment || (hi == lo && a.accumulate)) continue;
+    float acc[4];
+    add_rows<BF16, WIDE>(a, order, lo, hi, s, lane, acc);
+    put_row<WIDE>(a, v0 + r, s, lane, acc);
+  }
+}
+
+// Rows of runs longer than kSegment: block (c, slice) serves the run that
+// begins in piece c, if any; its waves add a quarter of the pieces each, the
+// quarters are added in order.
+template <bool WIDE>
+__global__ void __launch_bounds__(kBlock)
+embed_grad_join_kernel(EmbedGradArgs a, const uint32_t* __restrict__ keys, const float* __restrict__ partial) {
+  __shared__ float sums[kWaves][kSlice];
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const uint32_t n = static_cast<uint32_t>(a.n);
+  const int64_t slices = (a.dim + kSlice - 1) / kSlice;
+  const uint32_t c = static_cast<uint32_t>(blockIdx.x / slices);
+  const int64_t s = blockIdx.x - c * slices;
+  const uint32_t lo = c * kSegment, hi = lo + kSegment < n ? lo + kSegment : n;
+  const uint32_t key = keys[hi - 1];
+  const uint32_t b = lower_bound(keys, n, key + (lane & 1));
+  const uint32_t first = __builtin_amdgcn_readlane(b, 0), end = __builtin_amdgcn_readlane(b, 1);
+  if (key >= a.vocab || first < lo || end - first <= kSegment) return;  // the whole block
+  const uint32_t pieces = (end - 1) / kSegment - c + 1, quarter = (pieces + kWaves - 1) / kWaves;
+  const uint32_t p0 = wave * quarter, p1 = p0 + quarter < pieces ? p0 + quarter : pieces;
+  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (uint32_t p = p0; p < p1; ++p) {
+    const int64_t slot = p == 0 && first != lo ? 2 * static_cast<int64_t>(c) + 1 : 2 * static_cast<int64_t>(c + p);
+    float v[4];
+    load_four<false, WIDE>(reinterpret_cast<const uint8_t*>(partial + slot * a.dim), s, lane, a.dim, v);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k] += v[k];
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) sums[wave][k * kWave + lane] = acc[k];
+  wait_lds_writes();
+#pragma unroll
+  for (int k = 0; k < 4; ++k) hold_value(acc[k]);
+  __syncthreads();
+  if (wave != 0) return;
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k] += sums[w][k * kWave + lane];
+  put_row<WIDE>(a, key, s, lane, acc);
+}
+
+uint32_t blocks_of(int64_t waves) { return static_cast<uint32_t>((waves + kWaves - 1) / kWaves); }
+
+int64_t align256(int64_t b) { return (b + 255) & ~int64_t(255); }
+int64_t pieces_of(int64_t n) { return (n + kSegment - 1) / kSegment; }
+
+// Workspace: sorted keys and positions (twice in the many-block sort), the
+// tiles' digit counts, the pieces' sums.
+struct GradSpace {
+  int64_t list, counts, partial, total;
+};
+GradSpace grad_space(int64_t n, int64_t dim) {
+  GradSpace g;
+  g.list = align256(4 * n);
+  const bool many = n > kSortOne;
+  g.counts = many ? align256((n + kSortTile - 1) / kSortTile * kDigit * 4) : 0;
+  g.partial = n > kSegment ? align256(2 * pieces_of(n) * dim * 4) : 0;
+  g.total = g.list * (many ? 4 : 2) + g.counts + g.partial;
+  return g;
+}
+
+template <int SB, bool OUT16, bool WIDE>
+hipError_t launch_packed_at(const EmbedArgs& a, const LevelTable& lv, hipStream_t s) {
+  const int64_t per_row = (a.dim + kWave * (OUT16 ? 8 : 4) - 1) / (kWave * (OUT16 ? 8 : 4));
+  const int64_t units = a.n * per_row;
+  // Few units: one per wave, to spread over the CUs.
+  if (units < 16 * static_cast<int64_t>(device_cu_count()))
+    embed_packed_kernel<SB, OUT16, WIDE, 1><<<dim3(blocks_of(units)), dim3(kBlock), 0, s>>>(
+        a, lv, units, static_cast<uint32_t>(per_row));
+  else
+    embed_packed_kernel<SB, OUT16, WIDE, 4><<<dim3(blocks_of((units + 3) / 4)), dim3(kBlock), 0, s>>>(
+        a, lv, units, static_cast<uint32_t>(per_row));
+  return hipGetLastError();
+}
+
+template <int SB>
+hipError_t launch_packed_for(const EmbedArgs& a, const LevelTable& lv, hipStream_t s) {
+  if (a.out_bf16)
+    return a.dim % 8 == 0 ? launch_packed_at<SB, true, true>(a, lv, s) : launch_packed_at<SB, true, false>(a, lv, s);
+  return a.dim % 4 == 0 ? launch_packed_at<SB, false, true>(a, lv, s) : launch_packed_at<SB, false, false>(a, lv, s);
+}
+
+template <bool IN16, bool OUT16>
+hipError_t launch_embed_at(const EmbedArgs& a, hipStream_t s) {
+  constexpr int E = IN16 || OUT16 ? 8 : 4;
+  const int64_t per_row = (a.dim + kWave * E - 1) / (kWave * E), units = a.n * per_row;
+  const dim3 grid(blocks_of(units)), block(kBlock);
+  if (a.dim % E == 0)
+    embed_kernel<IN16, OUT16, true><<<grid, block, 0, s>>>(a, units, static_cast<uint32_t>(per_row));
+  else
+    embed_kernel<IN16, OUT16, false><<<grid, block, 0, s>>>(a, units, static_cast<uint32_t>(per_row));
+  return hipGetLastError();
+}
+
+template <bool WIDE>
+hipError_t launch_grad_sums(const EmbedGradArgs& a, const uint32_t* keys, const uint32_t* order, float* partial,
+                            hipStream_t s) {
+  const int64_t slices = (a.dim + kSlice - 1) / kSlice;
+  const bool runs = a.n > kSegment;  // a longer run than kSegment may exist
+  const int64_t pb = runs ? pieces_of(a.n) * ((slices + kWaves - 1) / kWaves) : 0;
+  // Rows per block: about 8 blocks per CU, so that the blocks' searches for
+  // their rows' runs hide behind other blocks' stores.
+  int64_t rows = a.vocab / (8 * static_cast<int64_t>(device_cu_count()));
+  rows = rows < 1 ? 1 : rows > kRowsMax ? kRowsMax : rows;
+  const int64_t blocks = pb + (a.vocab + rows - 1) / rows;
+  if (a.dout_bf16)
+    embed_grad_kernel<true, WIDE><<<dim3(static_cast<uint32_t>(blocks)), dim3(kBlock), 0, s>>>(
+        a, keys, order, partial, static_cast<uint32_t>(pb), static_cast<int>(rows));
+  else
+    embed_grad_kernel<false, WIDE><<<dim3(static_cast<uint32_t>(blocks)), dim3(kBlock), 0, s>>>(
+        a, keys, order, partial, static_cast<uint32_t>(pb), static_cast<int>(rows));
+  if (runs)
+    embed_grad_join_kernel<WIDE><<<dim3(static_cast<uint32_t>(pieces_of(a.n) * slices)), dim3(kBlock), 0, s>>>(
+        a, keys, partial);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_embed(const EmbedArgs& a, hipStream_t s) {
+  if (a.table_bf16) return a.out_bf16 ? launch_embed_at<true, true>(a, s) : launch_embed_at<true, false>(a, s);
+  return a.out_bf16 ? launch_embed_at<false, true>(a, s) : launch_embed_at<false, false>(a, s);
+}
+
+hipError_t launch_embed_packed(const EmbedArgs& a, int storage, const LevelTable& lv, hipStream_t s) {
+  if (storage == 2) return launch_packed_for<2>(a, lv, s);
+  if (storage == 3) return launch_packed_for<3>(a, lv, s);
+  if (storage == 4) return launch_packed_for<4>(a, lv, s);
+  return launch_packed_for<kTritStorage>(a, lv, s);
+}
+
+int64_t embed_grad_workspace(int64_t n, int64_t vocab, int64_t dim) {
+  (void)vocab;
+  return grad_space(n, dim).total;
+}
+
+hipError_t launch_embed_grad(const EmbedGradArgs& a, uint8_t* ws, hipStream_t s) {
+  const GradSpace g = grad_space(a.n, a.dim);
+  auto at = [&](int64_t off) { return reinterpret_cast<uint32_t*>(ws + off); };
+  uint32_t *keys = at(0), *order = at(g.list);
+  float* partial;
+  int passes = 1;  // keys run from 0 to vocab
+  while (passes < 4 && (a.vocab >> (8 * passes))) ++passes;
+  if (a.n <= kSortOne) {
+    partial = reinterpret_cast<float*>(at(2 * g.list));
+    if (a.n > 4 * kOneThreads)
+      sort_one_kernel<16><<<dim3(1), dim3(kOneThreads), 0, s>>>(a, passes, keys, order);
+    else if (a.n > kOneThreads)
+      sort_one_kernel<4><<<dim3(1), dim3(kOneThreads), 0, s>>>(a, passes, keys, order);
+    else if (a.n > 0)
+      sort_one_kernel<1><<<dim3(1), dim3(kOneThreads), 0, s>>>(a, passes, keys, order);
+  } else {
+    uint32_t *keys2 = at(2 * g.list), *order2 = at(3 * g.list), *counts = at(4 * g.list);
+    partial = reinterpret_cast<float*>(at(4 * g.list + g.counts));
+    const dim3 grid(static_cast<uint32_t>((a.n + kSortTile - 1) / kSortTile)), block(kBlock);
+    const uint32_t *in_keys = nullptr, *in_order = nullptr;  // the first pass reads the tokens
+    for (int p = 0; p < passes; ++p) {
+      count_kernel<<<grid, block, 0, s>>>(a, 8 * p, in_keys, counts);
+      scatter_kernel<<<grid, block, 0, s>>>(a, 8 * p, counts, in_keys, in_order, keys2, order2);
+      in_keys = keys2;
+      in_order = order2;
+      std::swap(keys, keys2);
+      std::swap(order, order2);
+    }
+    // The last pass wrote what the swap made `keys` and `order`.
+  }
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  return a.dim % 4 == 0 ? launch_grad_sums<true>(a, keys, order, partial, s)
+                        : launch_grad_sums<false>(a, keys, order, partial, s);
+}
+
+}  // namespace cq

@@ -961,6 +961,400 @@ int cq_dequant_matvec_many(int n, const cq_matvec_desc* descs, int bits, int gro
   return cq::matvec_many_impl(n, descs, bits, group_size, levels, n_levels, batch, stream, nullptr, 0);
 }
 
+// ---- Around the products: embedding, norm, 8-bit activations ---------------------
+
+namespace {
+
+bool is_dtype(int d) { return d == CQ_F32 || d == CQ_BF16; }
+int64_t dtype_bytes(int d) { return d == CQ_F32 ? 4 : 2; }
+
+// rows * cols values of `bytes` bytes each stay within 2^62.
+bool fits(int64_t rows, int64_t cols, int64_t bytes) {
+  int64_t v;
+  return !__builtin_mul_overflow(rows, cols, &v) && !__builtin_mul_overflow(v, bytes, &v) && v < (int64_t(1) << 62);
+}
+constexpr int64_t kMaxIndex = (int64_t(1) << 31) - 2;  // rows, tokens and vocabularies: 32-bit indices on the device
+
+// Output `out` against the inputs of a call (NULL or empty: no conflict).
+struct Region {
+  const void* p;
+  int64_t bytes;
+};
+bool meets_any(const void* out, int64_t bytes, std::initializer_list<Region> others) {
+  for (const Region& r : others)
+    if (out && r.p && overlap(out, static_cast<size_t>(bytes), r.p, static_cast<size_t>(r.bytes))) return true;
+  return false;
+}
+
+int check_workspace(const void* ws, int64_t have, int64_t need) {
+  if (need == 0) return CQ_OK;
+  if (!ws) return fail(CQ_ERR_NULL, "workspace is NULL (%lld bytes needed)", (long long)need);
+  if (have < need) return fail(CQ_ERR_ARG, "workspace of %lld bytes, %lld needed", (long long)have, (long long)need);
+  if (!aligned(ws, 16)) return fail(CQ_ERR_ALIGN, "workspace needs 16-byte alignment");
+  return CQ_OK;
+}
+
+int check_lookup(const void* tokens, int token_bytes, int64_t n, int64_t vocab, int64_t dim, float scale) {
+  if (token_bytes != 4 && token_bytes != 8) return fail(CQ_ERR_ARG, "token_bytes=%d must be 4 or 8", token_bytes);
+  if (n < 0 || vocab < 0 || dim < 0) return fail(CQ_ERR_ARG, "negative size");
+  if (!std::isfinite(scale)) return fail(CQ_ERR_ARG, "scale is not finite");
+  if (n > kMaxIndex || vocab > kMaxIndex || dim > kMaxIndex || !fits(n, dim, 4) || !fits(vocab, dim, 4))
+    return fail(CQ_ERR_UNSUPPORTED, "n, vocab and dim must be at most 2^31 - 2");
+  // One block of four waves, each at least 256 columns.
+  if (n && ceil_div(dim, 256) > (int64_t(1) << 32) / n)
+    return fail(CQ_ERR_UNSUPPORTED, "n * dim is past this call's grid");
+  if (n && dim && !tokens) return fail(CQ_ERR_NULL, "tokens is NULL");
+  if (!aligned(tokens, token_bytes)) return fail(CQ_ERR_ALIGN, "tokens need %d-byte alignment", token_bytes);
+  return CQ_OK;
+}
+
+int check_norm(int dtype, const void* weight, int weight_dtype, int64_t rows, int64_t cols, float eps) {
+  if (!is_dtype(dtype)) return fail(CQ_ERR_ARG, "unknown dtype %d", dtype);
+  if (weight && !is_dtype(weight_dtype)) return fail(CQ_ERR_ARG, "unknown weight_dtype %d", weight_dtype);
+  if (rows < 0 || cols < 0) return fail(CQ_ERR_ARG, "negative size");
+  if (!(eps >= 0.0f) || !std::isfinite(eps)) return fail(CQ_ERR_ARG, "eps must be finite and not negative");
+  if (rows > kMaxIndex) return fail(CQ_ERR_UNSUPPORTED, "rows must be at most 2^31 - 2");
+  if (cols > cq::kNormMaxCols)
+    return fail(CQ_ERR_UNSUPPORTED, "cols=%lld: a row may hold at most %lld values", (long long)cols,
+                (long long)cq::kNormMaxCols);
+  if (!aligned(weight, 16)) return fail(CQ_ERR_ALIGN, "weight needs 16-byte alignment");
+  return CQ_OK;
+}
+
+// The shared part of both forms of cq_add_rms_norm; `a` gets its inputs.
+int norm_inputs(const void* x, const void* residual, int dtype, const void* weight, int weight_dtype, int64_t rows,
+                int64_t cols, float eps, void* sum, const void* out, int64_t out_bytes, cq::NormArgs* a) {
+  if (!x) return fail(CQ_ERR_NULL, "x is NULL");
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(sum, 16))
+    return fail(CQ_ERR_ALIGN, "x, residual and sum need 16-byte alignment");
+  const int64_t bytes = rows * cols * dtype_bytes(dtype);
+  const int64_t wbytes = weight ? cols * dtype_bytes(weight_dtype) : 0;
+  if (meets_any(out, out_bytes, {{x, bytes}, {residual, bytes}, {weight, wbytes}, {sum, bytes}}) ||
+      meets_any(sum, bytes, {{weight, wbytes}}) || (sum != x && meets_any(sum, bytes, {{x, bytes}})) ||
+      (sum != residual && meets_any(sum, bytes, {{residual, bytes}})))
+    return fail(CQ_ERR_ARG, "input and output buffers overlap");
+  a->x = static_cast<const uint8_t*>(x);
+  a->residual = static_cast<const uint8_t*>(residual);
+  a->weight = weight;
+  a->w_bf16 = weight_dtype == CQ_BF16;
+  a->rows = rows;
+  a->cols = cols;
+  a->eps = eps;
+  a->sum = static_cast<uint8_t*>(sum);
+  return CQ_OK;
+}
+
+}  // namespace
+
+int cq_embed(const void* tokens, int token_bytes, int64_t n, const void* table, int table_dtype, int64_t vocab,
+             int64_t dim, float scale, void* out, int out_dtype, void* stream) {
+  g_last_error[0] = 0;
+  if (!is_dtype(table_dtype) || !is_dtype(out_dtype)) return fail(CQ_ERR_ARG, "unknown dtype");
+  if (int rc = check_lookup(tokens, token_bytes, n, vocab, dim, scale)) return rc;
+  if (n == 0 || dim == 0) return CQ_OK;
+  if (!out || (vocab && !table)) return fail(CQ_ERR_NULL, "table/out is NULL");
+  if (!aligned(out, 16) || !aligned(table, 16)) return fail(CQ_ERR_ALIGN, "table and out need 16-byte alignment");
+  if (meets_any(out, n * dim * dtype_bytes(out_dtype),
+                {{table, vocab * dim * dtype_bytes(table_dtype)}, {tokens, n * token_bytes}}))
+    return fail(CQ_ERR_ARG, "input and output buffers overlap");
+  cq::EmbedArgs a{};
+  a.tokens = tokens;
+  a.token_bytes = token_bytes;
+  a.n = n;
+  a.vocab = vocab;
+  a.dim = dim;
+  a.scale = scale;
+  a.table = static_cast<const uint8_t*>(table);
+  a.table_bf16 = table_dtype == CQ_BF16;
+  a.out = static_cast<uint8_t*>(out);
+  a.out_bf16 = out_dtype == CQ_BF16;
+  return hip_status(cq::launch_embed(a, static_cast<hipStream_t>(stream)), "embed launch");
+}
+
+int cq_embed_packed(const void* tokens, int token_bytes, int64_t n, const uint8_t* packed, const uint16_t* norms,
+                    int64_t vocab, int64_t dim, int bits, int group_size, const float* levels, int n_levels,
+                    float scale, void* out, int out_dtype, void* stream) {
+  g_last_error[0] = 0;
+  int L, rc;
+  if ((rc = check_bits(bits, false, &L))) return rc;
+  if (!is_dtype(out_dtype)) return fail(CQ_ERR_ARG, "unknown out_dtype %d", out_dtype);
+  if ((rc = check_codec_group(group_size, bits))) return rc;
+  if ((rc = check_levels(levels, n_levels, L, bits))) return rc;
+  if ((rc = check_lookup(tokens, token_bytes, n, vocab, dim, scale))) return rc;
+  if (n == 0 || dim == 0) return CQ_OK;
+  if (!out || (vocab && (!packed || !norms))) return fail(CQ_ERR_NULL, "packed/norms/out is NULL");
+  if (!aligned(out, 16) || !aligned(packed, packed_align(bits, group_size)) || !aligned(norms, 2))
+    return fail(CQ_ERR_ALIGN, "out needs 16-byte, packed 16-byte (G != 128: 4-byte; trits: 2-byte, any at G != 128), norms 2-byte alignment");
+  const int64_t ng = vocab * ceil_div(dim, group_size);
+  if (meets_any(out, n * dim * dtype_bytes(out_dtype),
+                {{packed, ng * group_bytes(bits, group_size)}, {norms, ng * 2}, {tokens, n * token_bytes}}))
+    return fail(CQ_ERR_ARG, "input and output buffers overlap");
+  cq::EmbedArgs a{};
+  a.tokens = tokens;
+  a.token_bytes = token_bytes;
+  a.n = n;
+  a.vocab = vocab;
+  a.dim = dim;
+  a.scale = scale;
+  a.packed = packed;
+  a.norms = norms;
+  a.group = group_size;
+  a.gbytes = static_cast<int>(group_bytes(bits, group_size));
+  a.out = static_cast<uint8_t*>(out);
+  a.out_bf16 = out_dtype == CQ_BF16;
+  return hip_status(cq::launch_embed_packed(a, storage_code(bits), make_table(levels, L),
+                                            static_cast<hipStream_t>(stream)),
+                    "embed launch");
+}
+
+int cq_embed_grad_workspace(int64_t n, int64_t vocab, int64_t dim, int64_t* bytes) {
+  g_last_error[0] = 0;
+  if (int rc = check_lookup(nullptr, 4, n, vocab, 0, 1.0f)) return rc;
+  if (dim < 0) return fail(CQ_ERR_ARG, "negative size");
+  if (!fits(n, dim, 4)) return fail(CQ_ERR_UNSUPPORTED, "n * dim is too large");
+  if (!bytes) return fail(CQ_ERR_NULL, "bytes is NULL");
+  *bytes = dim == 0 || vocab == 0 ? 0 : cq::embed_grad_workspace(n, vocab, dim);
+  return CQ_OK;
+}
+
+int cq_embed_grad(const void* tokens, int token_bytes, int64_t n, const void* dout, int dout_dtype, int64_t vocab,
+                  int64_t dim, float scale, int accumulate, void* grad, int grad_dtype, void* workspace,
+                  int64_t workspace_bytes, void* stream) {
+  g_last_error[0] = 0;
+  if (!is_dtype(dout_dtype) || !is_dtype(grad_dtype)) return fail(CQ_ERR_ARG, "unknown dtype");
+  if (accumulate != 0 && accumulate != 1) return fail(CQ_ERR_ARG, "accumulate=%d must be 0 or 1", accumulate);
+  if (int rc = check_lookup(tokens, token_bytes, n, vocab, dim, scale)) return rc;
+  if (vocab == 0 || dim == 0 || (n == 0 && accumulate)) return CQ_OK;
+  if (!grad || (n && !dout)) return fail(CQ_ERR_NULL, "dout/grad is NULL");
+  if (!aligned(grad, 16) || !aligned(dout, 16)) return fail(CQ_ERR_ALIGN, "dout and grad need 16-byte alignment");
+  const int64_t need = cq::embed_grad_workspace(n, vocab, dim);
+  if (int rc = check_workspace(workspace, workspace_bytes, need)) return rc;
+  const int64_t gbytes = vocab * dim * dtype_bytes(grad_dtype), dbytes = n * dim * dtype_bytes(dout_dtype);
+  const Region ws{need ? workspace : nullptr, need};
+  if (meets_any(grad, gbytes, {{dout, dbytes}, {tokens, n * token_bytes}, ws}) ||
+      meets_any(ws.p, ws.bytes, {{dout, dbytes}, {tokens, n * token_bytes}}))
+    return fail(CQ_ERR_ARG, "input and output buffers overlap");
+  cq::EmbedGradArgs a{};
+  a.tokens = tokens;
+  a.token_bytes = token_bytes;
+  a.n = n;
+  a.vocab = vocab;
+  a.dim = dim;
+  a.scale = scale;
+  a.dout = static_cast<const uint8_t*>(dout);
+  a.dout_bf16 = dout_dtype == CQ_BF16;
+  a.grad = static_cast<uint8_t*>(grad);
+  a.grad_bf16 = grad_dtype == CQ_BF16;
+  a.accumulate = accumulate;
+  return hip_status(cq::launch_embed_grad(a, static_cast<uint8_t*>(workspace), static_cast<hipStream_t>(stream)),
+                    "embedding gradient launch");
+}
+
+int cq_add_rms_norm(const void* x, const void* residual, int dtype, const void* weight, int weight_dtype, int64_t rows,
+                    int64_t cols, float eps, void* sum, void* out, int out_dtype, void* stream) {
+  g_last_error[0] = 0;
+  if (int rc = check_norm(dtype, weight, weight_dtype, rows, cols, eps)) return rc;
+  if (!is_dtype(out_dtype)) return fail(CQ_ERR_ARG, "unknown out_dtype %d", out_dtype);
+  if (rows == 0 || cols == 0) return CQ_OK;
+  if (!out) return fail(CQ_ERR_NULL, "out is NULL");
+  if (!aligned(out, 16)) return fail(CQ_ERR_ALIGN, "out needs 16-byte alignment");
+  cq::NormArgs a{};
+  if (int rc = norm_inputs(x, residual, dtype, weight, weight_dtype, rows, cols, eps, sum, out,
+                           rows * cols * dtype_bytes(out_dtype), &a))
+    return rc;
+  a.out = static_cast<uint8_t*>(out);
+  a.out_bf16 = out_dtype == CQ_BF16;
+  return hip_status(cq::launch_norm(a, dtype == CQ_BF16, static_cast<hipStream_t>(stream)), "norm launch");
+}
+
+int cq_add_rms_norm_q8(const void* x, const void* residual, int dtype, const void* weight, int weight_dtype,
+                       int64_t rows, int64_t cols, int group_size, float eps, void* sum, int8_t* q, float* scale,
+                       void* stream) {
+  g_last_error[0] = 0;
+  if (int rc = check_norm(dtype, weight, weight_dtype, rows, cols, eps)) return rc;
+  if (int rc = check_codec_group(group_size, 0)) return rc;
+  if (cols % group_size)
+    return fail(CQ_ERR_UNSUPPORTED, "cols=%lld is not a multiple of %d", (long long)cols, group_size);
+  if (rows == 0 || cols == 0) return CQ_OK;
+  if (!q || !scale) return fail(CQ_ERR_NULL, "q/scale is NULL");
+  if (!aligned(q, 16) || !aligned(scale, 4)) return fail(CQ_ERR_ALIGN, "q needs 16-byte, scale 4-byte alignment");
+  const int64_t bytes = rows * cols * dtype_bytes(dtype), sbytes = rows * 4;
+  cq::NormArgs a{};
+  if (int rc = norm_inputs(x, residual, dtype, weight, weight_dtype, rows, cols, eps, sum, q, rows * cols, &a)) return rc;
+  if (meets_any(scale, sbytes,
+                {{x, bytes}, {residual, bytes}, {sum, bytes}, {q, rows * cols},
+                 {weight, weight ? cols * dtype_bytes(weight_dtype) : 0}}))
+    return fail(CQ_ERR_ARG, "input and output buffers overlap");
+  a.q = q;
+  a.scale = scale;
+  a.labels = group_size / (dtype == CQ_BF16 ? 8 : 4);
+  a.unit = 1.0f / (127.0f * std::sqrt(static_cast<float>(group_size)));
+  return hip_status(cq::launch_norm(a, dtype == CQ_BF16, static_cast<hipStream_t>(stream)), "norm launch");
+}
+
+static int64_t norm_grad_need(int64_t rows, int64_t cols, int dtype) {
+  const int blocks = rows ? cq::norm_grad_blocks(rows, cols, dtype == CQ_BF16) : 0;
+  return blocks > 1 ? blocks * cols * 4 : 0;
+}
+
+int cq_rms_norm_grad_workspace(int64_t rows, int64_t cols, int dtype, int64_t* bytes) {
+  g_last_error[0] = 0;
+  if (int rc = check_norm(dtype, nullptr, CQ_F32, rows, cols, 0.0f)) return rc;
+  if (!bytes) return fail(CQ_ERR_NULL, "bytes is NULL");
+  *bytes = norm_grad_need(rows, cols, dtype);
+  return CQ_OK;
+}
+
+int cq_rms_norm_grad(const void* dout, const void* sum, const void* dsum, int dtype, const void* weight,
+                     int weight_dtype, int64_t rows, int64_t cols, float eps, void* dx, float* dweight, void* workspace,
+                     int64_t workspace_bytes, void* stream) {
+  g_last_error[0] = 0;
+  if (int rc = check_norm(dtype, weight, weight_dtype, rows, cols, eps)) return rc;
+  if (cols == 0) return CQ_OK;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (!aligned(dweight, 16)) return fail(CQ_ERR_ALIGN, "dweight needs 16-byte alignment");
+  if (rows == 0) return dweight ? hip_status(cq::launch_zero(dweight, cols, s), "zero launch") : CQ_OK;
+  if (!dout || !sum || !dx) return fail(CQ_ERR_NULL, "dout/sum/dx is NULL");
+  if (!aligned(dout, 16) || !aligned(sum, 16) || !aligned(dsum, 16) || !aligned(dx, 16))
+    return fail(CQ_ERR_ALIGN, "dout, sum, dsum and dx need 16-byte alignment");
+  const int64_t need = dweight ? norm_grad_need(rows, cols, dtype) : 0;
+  if (int rc = check_workspace(workspace, workspace_bytes, need)) return rc;
+  const int64_t bytes = rows * cols * dtype_bytes(dtype), wbytes = weight ? cols * dtype_bytes(weight_dtype) : 0;
+  const Region ws{need ? workspace : nullptr, need};
+  const Region in[4] = {{dout, bytes}, {sum, bytes}, {weight, wbytes}, {dsum == dx ? nullptr : dsum, bytes}};
+  if (meets_any(dx, bytes, {in[0], in[1], in[2], in[3], ws, {dweight, cols * 4}}) ||
+      meets_any(dweight, cols * 4, {in[0], in[1], in[2], {dsum, bytes}, ws}) ||
+      meets_any(ws.p, ws.bytes, {in[0], in[1], in[2], {dsum, bytes}}))
+    return fail(CQ_ERR_ARG, "input and output buffers overlap");
+  cq::NormGradArgs a{};
+  a.dout = static_cast<const uint8_t*>(dout);
+  a.sum = static_cast<const uint8_t*>(sum);
+  a.dsum = static_cast<const uint8_t*>(dsum);
+  a.weight = weight;
+  a.w_bf16 = weight_dtype == CQ_BF16;
+  a.rows = rows;
+  a.cols = cols;
+  a.eps = eps;
+  a.dx = static_cast<uint8_t*>(dx);
+  return hip_status(cq::launch_norm_grad(a, dtype == CQ_BF16, dweight, static_cast<float*>(workspace), s),
+                    "norm gradient launch");
+}
+
+// Levels as 16-bit whole numbers m = 256 hi + lo: for every largest |m| in
+// [24576, 32639] (both bytes then fit), the rounded levels and the scale that
+// fits them best, weighted by the cells' shares of N(0,1); the best of all.
+// With the largest level simply at the top the error is up to 2.7e-5 of the
+// output at 16 levels; the search brings it to a few 1e-6.
+int cq_q8_levels(int bits, const float* levels, int n_levels, cq_q8_table* table) {
+  g_last_error[0] = 0;
+  int L, rc;
+  if ((rc = check_bits(bits, false, &L))) return rc;
+  if ((rc = check_levels(levels, n_levels, L, bits))) return rc;
+  if (!table) return fail(CQ_ERR_NULL, "table is NULL");
+  constexpr int kLow = 24576, kHigh = 32639;
+  double c[cq::kMaxLevels], p[cq::kMaxLevels], top = 0.0;
+  for (int i = 0; i < L; ++i) {
+    c[i] = levels[i];
+    top = std::max(top, std::fabs(c[i]));
+  }
+  double below = 0.0;
+  for (int i = 0; i < L; ++i) {
+    const double upto = i + 1 < L ? 0.5 * std::erfc(-0.5 * (c[i] + c[i + 1]) * 0.7071067811865476) : 1.0;
+    p[i] = std::max(upto - below, 1e-6);  // a cell no N(0,1) value meets still counts a little
+    below = upto;
+  }
+  double best = -1.0;
+  int m_best[cq::kMaxLevels] = {0};
+  for (int largest = kHigh; largest >= kLow; --largest) {
+    double cm = 0.0, mm = 0.0, err = 0.0;
+    int m[cq::kMaxLevels];
+    for (int i = 0; i < L; ++i) {
+      m[i] = static_cast<int>(std::lrint(c[i] / top * largest));
+      cm += p[i] * c[i] * m[i];
+      mm += p[i] * double(m[i]) * m[i];
+    }
+    const double a = cm / mm;
+    bool near = true;
+    for (int i = 0; i < L; ++i) {
+      const double d = c[i] - a * m[i];
+      err += p[i] * d * d;
+      near = near && std::fabs(d) <= 2.1e-5 * top;
+    }
+    if (near && (best < 0.0 || err < best)) {
+      best = err;
+      table->scale = static_cast<float>(a);
+      for (int i = 0; i < L; ++i) m_best[i] = m[i];
+    }
+  }
+  if (best < 0.0) return fail(CQ_ERR_ARG, "levels cannot be held in 16 bits");  // their largest overflows or vanishes
+  std::memset(table->hi, 0, sizeof(table->hi));
+  std::memset(table->lo, 0, sizeof(table->lo));
+  for (int i = 0; i < L; ++i) {
+    const int hi = (m_best[i] + 128 + 65536) / 256 - 256;  // floor((m + 128) / 256)
+    table->hi[i] = static_cast<int8_t>(hi);
+    table->lo[i] = static_cast<int8_t>(m_best[i] - 256 * hi);
+  }
+  table->n_levels = L;
+  return CQ_OK;
+}
+
+static int check_q8_sizes(int64_t n_out, int64_t k, int64_t batch, int group_size) {
+  if (int rc = check_codec_group(group_size, 0)) return rc;
+  if (n_out < 0 || k < 0) return fail(CQ_ERR_ARG, "negative size");
+  if (batch < 1) return fail(CQ_ERR_ARG, "batch must be >= 1");
+  if (k % group_size) return fail(CQ_ERR_UNSUPPORTED, "k=%lld is not a multiple of %d", (long long)k, group_size);
+  if (k > cq::kQ8MaxK) return fail(CQ_ERR_UNSUPPORTED, "k=%lld: this product takes k <= 2^22", (long long)k);
+  if (n_out > kMaxIndex || batch > kMaxIndex || !fits(n_out, std::max(k, batch), 4) || !fits(batch, k, 4) ||
+      ceil_div(n_out, 128) > kMaxIndex / ceil_div(batch, 128) / 8 || ceil_div(batch, 8) > kMaxIndex * 16 / std::max<int64_t>(n_out, 1))
+    return fail(CQ_ERR_UNSUPPORTED, "batch * n_out is past this call's grid");
+  return CQ_OK;
+}
+
+int cq_dequant_gemm_q8_workspace(int64_t n_out, int64_t k, int64_t batch, int group_size, int64_t* bytes) {
+  g_last_error[0] = 0;
+  if (int rc = check_q8_sizes(n_out, k, batch, group_size)) return rc;
+  if (!bytes) return fail(CQ_ERR_NULL, "bytes is NULL");
+  *bytes = cq::gemm_q8_workspace(n_out, k, batch, group_size);
+  return CQ_OK;
+}
+
+int cq_dequant_gemm_q8(const uint8_t* packed, const uint16_t* norms, int64_t n_out, int64_t k, int bits, int group_size,
+                       const cq_q8_table* table, const int8_t* q, const float* scale, int64_t batch, void* y,
+                       int y_dtype, void* workspace, int64_t workspace_bytes, void* stream) {
+  g_last_error[0] = 0;
+  int L, rc;
+  if ((rc = check_bits(bits, false, &L))) return rc;
+  if ((rc = reject_trits(bits))) return rc;
+  if (!is_dtype(y_dtype)) return fail(CQ_ERR_ARG, "unknown y_dtype %d", y_dtype);
+  if ((rc = check_q8_sizes(n_out, k, batch, group_size))) return rc;
+  if (!table) return fail(CQ_ERR_NULL, "table is NULL");
+  if (table->n_levels != L) return fail(CQ_ERR_ARG, "table of %d levels, this bit-width needs %d", table->n_levels, L);
+  if (!std::isfinite(table->scale)) return fail(CQ_ERR_ARG, "table scale is not finite");
+  if (n_out == 0) return CQ_OK;
+  if (!y) return fail(CQ_ERR_NULL, "y is NULL");
+  if (!aligned(y, 16)) return fail(CQ_ERR_ALIGN, "y needs 16-byte alignment");
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  cq::GemmQ8Args a{packed, norms, n_out, k, batch, q, scale, static_cast<uint8_t*>(y), y_dtype == CQ_BF16};
+  if (k == 0) return hip_status(cq::launch_gemm_q8_empty(a, s), "zero launch");
+  if (!packed || !norms || !q || !scale) return fail(CQ_ERR_NULL, "packed/norms/q/scale is NULL");
+  if (!aligned(packed, packed_align(bits, group_size)) || !aligned(norms, 2) || !aligned(q, 16) || !aligned(scale, 4))
+    return fail(CQ_ERR_ALIGN, "packed needs 16-byte (G != 128: 4-byte), q 16-byte, scale 4-byte, norms 2-byte alignment");
+  const int64_t need = cq::gemm_q8_workspace(n_out, k, batch, group_size);
+  if ((rc = check_workspace(workspace, workspace_bytes, need))) return rc;
+  const int64_t ng = n_out * (k / group_size), pbytes = ng * group_bytes(bits, group_size);
+  const int64_t ybytes = batch * n_out * dtype_bytes(y_dtype);
+  const Region ws{need ? workspace : nullptr, need};
+  if (meets_any(y, ybytes, {{packed, pbytes}, {norms, ng * 2}, {q, batch * k}, {scale, batch * 4}, ws}) ||
+      meets_any(ws.p, ws.bytes, {{packed, pbytes}, {norms, ng * 2}, {q, batch * k}, {scale, batch * 4}}))
+    return fail(CQ_ERR_ARG, "input and output buffers overlap");
+  cq::Q8Levels lv{};
+  std::memcpy(lv.hi, table->hi, sizeof(lv.hi));
+  std::memcpy(lv.lo, table->lo, sizeof(lv.lo));
+  lv.scale = table->scale;
+  return hip_status(cq::launch_gemm_q8(a, storage_bits(bits), group_size, lv, static_cast<float*>(workspace), s),
+                    "8-bit product launch");
+}
+
 }  // extern "C"
 
 namespace cq {
