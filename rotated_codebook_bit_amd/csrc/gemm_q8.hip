@@ -40,14 +40,20 @@ __device__ __forceinline__ void load_raw(const uint8_t* p, Raw<BYTES>& r) {
   __builtin_memcpy(r.w, p, BYTES);
 }
 
-// Four codes' selectors (one per byte) and the levels' bytes they select.
-// Codes 4i .. 4i + 3 of a lane's run, in the order in which ordered() puts
-// the activations: the natural one for 2 and 3 bits; at 4 bits the even
-// codes of 8, then the odd ones (two operations instead of five to spread
-// eight codes).
-template <int SB, int BYTES>
+// Four codes' selectors, one per byte: selectors() number i of a lane's run,
+// in the order in which ordered() puts the activations.
+//   3 bits: codes 4i .. 4i + 3.
+//   4 bits: of 8 codes the even ones, then the odd ones: two operations
+//     spread eight codes instead of ten, at two byte permutes per 8
+//     activations.
+//   2 bits: codes 4i .. 4i + 3, four operations; or, SHUFFLE, of 16 codes
+//     every fourth from code i % 4, seven operations for four selectors, at
+//     eight byte permutes per 16 activations.
+template <int SB, bool SHUFFLE, int BYTES>
 __device__ __forceinline__ uint32_t selectors(const Raw<BYTES>& r, int i) {
-  if constexpr (SB == 2) {
+  if constexpr (SB == 2 && SHUFFLE) {
+    return (r.w[i / 4] >> (2 * (i % 4))) & 0x03030303u;
+  } else if constexpr (SB == 2) {
     uint32_t t = __builtin_amdgcn_ubfe(r.w[i / 4], 8 * (i % 4), 8);
     t |= t << 12;
     t |= t << 6;
@@ -65,25 +71,35 @@ __device__ __forceinline__ uint32_t selectors(const Raw<BYTES>& r, int i) {
     return (r.w[i / 2] >> (4 * (i % 2))) & 0x0F0F0F0Fu;
   }
 }
+// The levels' bytes of four selectors.  At 4 bits the sixteen entries lie in
+// two tables of eight: v_perm_b32 takes bytes 0 .. 7 by selectors 0 .. 7 and
+// has fixed results for 8 .. 15 (the sign of byte 1, 3, 5, 7 of the table, 0,
+// then 255 three times), so
+//   entry(i) = permute(first, i) ^ permute(second, i ^ 8)
+// once each table holds its entries xor what the other one answers to the
+// same code (xor_tables() below).  Three operations instead of five per byte
+// lookup and none for a mask.
 template <int SB>
 __device__ __forceinline__ uint32_t pick(const uint32_t (&t)[4], uint32_t sel) {
   if constexpr (SB == 2) return __builtin_amdgcn_perm(0u, t[0], sel);
   if constexpr (SB == 3) return __builtin_amdgcn_perm(t[1], t[0], sel);
-  // Sixteen entries: both halves by the low three bits, then one by the top bit.
-  const uint32_t s7 = sel & 0x07070707u, m8 = sel & 0x08080808u, mask = (m8 << 5) - (m8 >> 3);
-  const uint32_t a = __builtin_amdgcn_perm(t[1], t[0], s7), b = __builtin_amdgcn_perm(t[3], t[2], s7);
-  return (b & mask) | (a & ~mask);
+  return __builtin_amdgcn_perm(t[1], t[0], sel) ^ __builtin_amdgcn_perm(t[3], t[2], sel ^ 0x08080808u);
 }
 
+__device__ __forceinline__ int byte_perm(int hi, int lo, uint32_t s) {
+  return static_cast<int>(__builtin_amdgcn_perm(static_cast<uint32_t>(hi), static_cast<uint32_t>(lo), s));
+}
 // Activations of 16 columns in the order of selectors().
-template <int SB>
+template <int SB, bool SHUFFLE>
 __device__ __forceinline__ i32x4 ordered(i32x4 q) {
   if constexpr (SB == 4) {
-    auto perm = [](int hi, int lo, uint32_t s) {
-      return static_cast<int>(__builtin_amdgcn_perm(static_cast<uint32_t>(hi), static_cast<uint32_t>(lo), s));
-    };
-    return i32x4{perm(q.y, q.x, 0x06040200u), perm(q.y, q.x, 0x07050301u), perm(q.w, q.z, 0x06040200u),
-                 perm(q.w, q.z, 0x07050301u)};
+    return i32x4{byte_perm(q.y, q.x, 0x06040200u), byte_perm(q.y, q.x, 0x07050301u), byte_perm(q.w, q.z, 0x06040200u),
+                 byte_perm(q.w, q.z, 0x07050301u)};
+  } else if constexpr (SB == 2 && SHUFFLE) {  // 4 x 4 bytes transposed
+    const int a = byte_perm(q.y, q.x, 0x05010400u), b = byte_perm(q.y, q.x, 0x07030602u);
+    const int c = byte_perm(q.w, q.z, 0x05010400u), d = byte_perm(q.w, q.z, 0x07030602u);
+    return i32x4{byte_perm(c, a, 0x05040100u), byte_perm(c, a, 0x07060302u), byte_perm(d, b, 0x05040100u),
+                 byte_perm(d, b, 0x07060302u)};
   } else {
     return q;
   }
@@ -91,124 +107,245 @@ __device__ __forceinline__ i32x4 ordered(i32x4 q) {
 
 // ---- Few batch rows -------------------------------------------------------------------
 
-// A block takes 16 outputs and up to 16 MT batch rows; its 8 waves take
+// A block takes 16 outputs and all batch rows (up to 64); its waves take
 // consecutive runs of groups and add their sums through LDS in wave order.
-// v_mfma_i32_16x16x64_i8: lane l holds batch row l % 16 and output l % 16,
-// columns of quarter l / 16 of the group, so each lane's codes of a group are
-// one load of G SB / 32 bytes (at G = 32 v_mfma_i32_16x16x32_i8).
-constexpr int kFewWaves = 8;
-constexpr int kFewBlock = kFewWaves * kWave;
+//
+// v_mfma_i32_16x16x64_i8 multiplies 16 activation rows with 16 outputs over
+// 64 columns, a quarter of the columns per 16 lanes.  With up to 8 batch rows
+// (P = 2) the 16 activation rows are 2 groups times 8 batch rows: row (p, b)
+// holds batch row b in the columns of group p and zeros elsewhere, so a
+// product covers two groups (a unit) whose sums stay apart, and they are
+// scaled together.  P = 2 with two row tiles serves up to 16 batch rows, P =
+// 1 with 2, 3 or 4 up to 64.
+//
+// The operands' lanes run over rows first, and a load instruction takes a
+// cycle per lane where neighbouring lanes meet different lines: with operands
+// loaded in place, 4-bit 4096 x 11008 at 37 batch rows spent about 400 cycles
+// per group and CU on them (18.7 us in all), 2-bit 11008 x 4096 at 64 rows
+// 29.8 us.  So a wave loads a unit's codes and activations in memory order
+// (whole lines), one unit ahead, passes them through its own piece of LDS
+// (rows an odd number of 16 bytes apart, so that 8 rows of one column fall on
+// different banks) and reads the operands there: 14.4 and 17.3 us.  What is
+// left at one batch row is mostly the decoding, about a vector operation and
+// a half per 2-bit code (11008 x 4096: 6.8 us, 4096 x 4096: 4.1, 32000 x 4096:
+// 12.8).
 
-template <int SB, int G, int MT, int U>
-__global__ void __launch_bounds__(kFewBlock)
+// What a wave stages per unit: 16 rows of codes, MT 16 / P rows of
+// activations and, for activation rows of the other group, a run of zeros.
+template <int SB, int G, int MT, int P>
+struct FewStage {
+  static constexpr int CL = G * P / 4;              // columns per lane and unit
+  static constexpr int CB = CL * SB / 8;            // their code bytes
+  static constexpr int kCodeRow = 4 * CB;           // code bytes of an output's unit
+  static constexpr int kGroupBytes = G * SB / 8;    // moved in pieces that do not cross groups
+  static constexpr int kCodePiece = kGroupBytes % 16 == 0 ? 16 : kGroupBytes % 8 == 0 ? 8 : 4;
+  static constexpr int kCodeStride = kCodeRow + (kCodeRow % 32 == 0 ? 16 : kCodeRow < 16 ? 8 : 0);
+  static constexpr int kCodeLoads = (16 * kCodeRow / kCodePiece + kWave - 1) / kWave;
+  static constexpr int kB = 16 / P;                 // batch rows of a row tile
+  static constexpr int kXRow = P * G;
+  static constexpr int kXStride = kXRow + 16;
+  static constexpr int kXLoads = (MT * kB * kXRow / 16 + kWave - 1) / kWave;
+  static constexpr int kZeros = P > 1 ? (CL + 15) / 16 * 16 : 0;
+  static constexpr int kXAt = 16 * kCodeStride;
+  static constexpr int kZeroAt = kXAt + MT * kB * kXStride;
+  static constexpr int kBytes = kZeroAt + kZeros;
+};
+
+constexpr int kFewWaves = 8;
+
+template <int BYTES>
+struct CodePiece {
+  uint32_t w[BYTES / 4];
+};
+
+// MT tiles of 16 / P batch rows; W: waves per block.
+template <int SB, int G, int MT, int P, int W>
+__global__ void __launch_bounds__(W* kWave)
 few_kernel(GemmQ8Args a, Q8Levels lv, float unit) {
-  constexpr int CB = G * SB / 32;             // code bytes per lane and group
-  constexpr int S = G >= 64 ? G / 64 : 1;     // products per group and term
-  constexpr int CL = G / 4;                   // columns per lane and group
-  __shared__ float part[kFewWaves][MT * 256];
+  using F = FewStage<SB, G, MT, P>;
+  constexpr int CL = F::CL, CB = F::CB, kB = F::kB;
+  constexpr int S = CL >= 16 ? CL / 16 : 1;   // products per unit and term
+  constexpr int SL = CL >= 16 ? 4 : 2;        // dwords per product (2: v_mfma_i32_16x16x32_i8)
+  // The activations are reordered once, on their way into LDS; at 2 bits that
+  // pays where there are few of them per code.
+  constexpr bool SHUFFLE = CL >= 16 && 8 * F::kXLoads < 9 * (CL / 16);
+  constexpr int kSums = MT * 4 * kWave;       // a wave's sums, left where its units were
+  constexpr int kWaveBytes = F::kBytes > 4 * kSums ? F::kBytes : 4 * kSums;
+  static_assert(kWaveBytes % 16 == 0, "every wave's piece starts on 16 bytes");
+  __shared__ __attribute__((aligned(16))) uint8_t stage[W * kWaveBytes];
   const int lane = threadIdx.x & (kWave - 1), r = lane & 15, j = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int ng = static_cast<int>(a.k / G);
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16, b0 = static_cast<int64_t>(blockIdx.y) * (16 * MT);
-  const int64_t n = n0 + r < a.n_out ? n0 + r : a.n_out - 1;
-  const uint8_t* const codes = a.packed + n * ng * (G * SB / 8) + j * CB;
-  const uint16_t* const norms = a.norms + n * ng;
-  const int8_t* q[MT];
+  uint8_t* const mine = stage + wave * kWaveBytes;
+  const int p = j * P / 4, piece = j % (4 / P);  // this lane's group of a unit, and its piece of it
+  const int ng = static_cast<int>(a.k / G), units = (ng + P - 1) / P;
+  const int batch = static_cast<int>(a.batch);
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
+  const int per = (units + W - 1) / W;
+  const int g0 = wave * per < units ? wave * per : units, g1 = g0 + per < units ? g0 + per : units;
+  const int last = a.n_out - n0 < 16 ? static_cast<int>(a.n_out - n0) - 1 : 15;  // last output of the tile
+  const int row_bytes = ng * F::kGroupBytes;
+  const uint8_t* const tile = a.packed + n0 * row_bytes;
+  const uint16_t* const norms = a.norms + (n0 + (r < last ? r : last)) * ng;
+  // The scale of this thread's first output, fetched ahead of the sums.
+  const int b_first = threadIdx.x / 16 % (MT * kB);
+  const float s_first = a.scale[b_first < batch ? b_first : batch - 1];
+
+  // The pieces of a unit this lane moves.
+  constexpr int kPer = F::kCodeRow / F::kCodePiece, kPerX = F::kXRow / 16;  // per output, per batch row
+  CodePiece<F::kCodePiece> c_reg[F::kCodeLoads];
+  i32x4 x_reg[F::kXLoads];
+  auto fetch = [&](int g) __attribute__((always_inline)) {
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int64_t b = b0 + 16 * m + r;
-    q[m] = a.q + (b < a.batch ? b : a.batch - 1) * a.k + j * CL;
+    for (int i = 0; i < F::kCodeLoads; ++i) {
+      const int e = lane + i * kWave, row = e / kPer < last ? e / kPer : last;
+      int at = g * F::kCodeRow + e % kPer * F::kCodePiece;
+      if (P > 1) at = at < row_bytes ? at : row_bytes - F::kCodePiece;  // the second group may be past the row
+      __builtin_memcpy(c_reg[i].w, tile + static_cast<int64_t>(row) * row_bytes + at, F::kCodePiece);
+    }
+#if defined(__HIP_DEVICE_COMPILE__)
+    // Batch rows past the batch are outside the buffer (or, where a whole
+    // load is past it, not loaded: they only meet sums that are not stored).
+    // Columns past k are the next row's, or outside; they are scaled by zero.
+    const auto src = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(a.q), 0, static_cast<int>(batch * a.k), 0x00020000);
+#pragma unroll
+    for (int i = 0; i < F::kXLoads; ++i) {
+      if (i * kWave / kPerX >= batch) break;
+      const int e = lane + i * kWave, b = e / kPerX;
+      const uint32_t off = b < batch ? static_cast<uint32_t>(b * a.k + e % kPerX * 16) : 0x80000000u;
+      x_reg[i] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(src, off, g * F::kXRow, 0));
+    }
+#endif
+  };
+  auto put = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < F::kCodeLoads; ++i) {
+      const int e = lane + i * kWave;
+      if (16 * kPer % kWave == 0 || e < 16 * kPer)
+        __builtin_memcpy(__builtin_assume_aligned(mine + e / kPer * F::kCodeStride + e % kPer * F::kCodePiece, F::kCodePiece),
+                         c_reg[i].w, F::kCodePiece);
+    }
+#pragma unroll
+    for (int i = 0; i < F::kXLoads; ++i) {
+      if (i * kWave / kPerX >= batch) break;
+      const int e = lane + i * kWave;
+      x_reg[i] = ordered<SB, SHUFFLE>(x_reg[i]);
+      if (MT * kB * kPerX % kWave == 0 || e < MT * kB * kPerX)
+        *reinterpret_cast<i32x4*>(mine + F::kXAt + e / kPerX * F::kXStride + e % kPerX * 16) = x_reg[i];
+    }
+    wait_lds_writes();
+#pragma unroll
+    for (int i = 0; i < F::kCodeLoads; ++i)
+#pragma unroll
+      for (int d = 0; d < F::kCodePiece / 4; ++d) hold_value(c_reg[i].w[d]);
+#pragma unroll
+    for (int i = 0; i < F::kXLoads; ++i) hold_values(x_reg[i].x, x_reg[i].y, x_reg[i].z, x_reg[i].w);
+  };
+  if constexpr (F::kZeros > 0) {
+    const i32x4 zero = {0, 0, 0, 0};
+    if (lane < F::kZeros / 16) *reinterpret_cast<i32x4*>(mine + F::kZeroAt + lane * 16) = zero;
+    wait_lds_writes();
+    hold_values(zero.x, zero.y, zero.z, zero.w);
   }
-  const int per = (ng + kFewWaves - 1) / kFewWaves;
-  const int g0 = wave * per < ng ? wave * per : ng, g1 = g0 + per < ng ? g0 + per : ng;
 
   float acc[MT][4];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[m][i] = 0.0f;
-
-  for (int g = g0; g < g1; g += U) {
-    Raw<CB> raw[U];
-    uint32_t nb[U];
-    i32x4 x[U][MT][S];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int gu = g + u < g1 ? g + u : g1 - 1;  // past the run: loaded again, scaled by zero
-      load_raw<CB>(codes + static_cast<int64_t>(gu) * (G * SB / 8), raw[u]);
-      nb[u] = norms[gu];
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-          const int8_t* p = q[m] + static_cast<int64_t>(gu) * G + 16 * s;
-          if constexpr (G >= 64) {
-            x[u][m][s] = *reinterpret_cast<const i32x4*>(p);
-          } else {
-            const int2 h = *reinterpret_cast<const int2*>(p);
-            x[u][m][s] = i32x4{h.x, h.y, 0, 0};
-          }
-        }
+  auto product = [](i32x4 av, i32x4 bv, i32x4 c) __attribute__((always_inline)) {
+    if constexpr (CL >= 16) {
+      return __builtin_amdgcn_mfma_i32_16x16x64_i8(av, bv, c, 0, 0, 0);
+    } else {
+      typedef int i32x2 __attribute__((ext_vector_type(2)));
+      return __builtin_amdgcn_mfma_i32_16x16x32_i8(__builtin_bit_cast(int64_t, (i32x2{av.x, av.y})),
+                                                   __builtin_bit_cast(int64_t, (i32x2{bv.x, bv.y})), c, 0, 0, 0);
     }
+  };
+
+  // Norms of four groups: lane (j, r) holds output r's of group (first of the
+  // quad) + j; one load instruction per four groups.
+  uint32_t quad = 0;
+  auto fetch_norms = [&](int g) __attribute__((always_inline)) -> uint32_t {
+    const int at = g * P + j;
+    return norms[at < ng ? at : ng - 1];
+  };
+  constexpr int kUnitsPerQuad = 4 / P;
+  int turn = 0;
+  if (g0 < g1) {
+    fetch(g0);
+    quad = fetch_norms(g0);
+  }
+  for (int g = g0; g < g1; ++g) {
+    put();
+    const uint32_t nb = static_cast<uint32_t>(__shfl(static_cast<int>(quad), r + 16 * (turn * P + p), kWave));
+    turn = turn + 1 == kUnitsPerQuad ? 0 : turn + 1;
+    if (g + 1 < g1) {
+      fetch(g + 1);
+      if (turn == 0) quad = fetch_norms(g + 1);
+    }
+    Raw<CB> raw;
+    if constexpr (CB % 4) raw.w[CB / 4] = 0;
+    __builtin_memcpy(raw.w, __builtin_assume_aligned(mine + r * F::kCodeStride + j * CB, CB % 16 == 0 ? 16 : CB % 8 == 0 ? 8 : CB % 4 == 0 ? 4 : CB % 2 == 0 ? 2 : 1), CB);
+    i32x4 ch[MT], cl[MT];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      i32x4 hi[S], lo[S];
+    for (int m = 0; m < MT; ++m) ch[m] = cl[m] = i32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int s = 0; s < S; ++s)
+    for (int s = 0; s < S; ++s) {
+      i32x4 hi = {0, 0, 0, 0}, lo = {0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < (G >= 64 ? 4 : 2); ++i) {
-          const uint32_t sel = selectors<SB, CB>(raw[u], 4 * s + i);
-          hi[s][i] = static_cast<int>(pick<SB>(lv.hi, sel));
-          lo[s][i] = static_cast<int>(pick<SB>(lv.lo, sel));
-        }
-      const float w = g + u < g1 ? half_value(nb[u]) : 0.0f;
+      for (int i = 0; i < SL; ++i) {
+        const uint32_t sel = selectors<SB, SHUFFLE, CB>(raw, 4 * s + i);
+        hi[i] = static_cast<int>(pick<SB>(lv.hi, sel));
+        lo[i] = static_cast<int>(pick<SB>(lv.lo, sel));
+      }
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        i32x4 t = {0, 0, 0, 0};
-        auto product = [](i32x4 av, i32x4 bv, i32x4 c) __attribute__((always_inline)) {
-          if constexpr (G >= 64) {
-            return __builtin_amdgcn_mfma_i32_16x16x64_i8(av, bv, c, 0, 0, 0);
-          } else {
-            typedef int i32x2 __attribute__((ext_vector_type(2)));
-            return __builtin_amdgcn_mfma_i32_16x16x32_i8(__builtin_bit_cast(int64_t, (i32x2{av.x, av.y})),
-                                                         __builtin_bit_cast(int64_t, (i32x2{bv.x, bv.y})), c, 0, 0, 0);
-          }
-        };
-        i32x4 xo[S];
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-          xo[s] = ordered<SB>(x[u][m][s]);
-          t = product(xo[s], hi[s], t);
+        const uint8_t* at = mine + F::kXAt + (m * kB + r % kB) * F::kXStride + p * G + piece * CL + 16 * s;
+        if (P > 1 && r / kB != p) at = mine + F::kZeroAt + 16 * s;
+        i32x4 x;
+        if constexpr (CL >= 16) {
+          x = *reinterpret_cast<const i32x4*>(at);
+        } else {
+          const int2 half = *reinterpret_cast<const int2*>(at);
+          x = i32x4{half.x, half.y, 0, 0};
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) t[i] <<= 8;
-#pragma unroll
-        for (int s = 0; s < S; ++s) t = product(xo[s], lo[s], t);
-        // A norm of zero (a run's end, a zero group) adds nothing, whatever
-        // the sum; integers are finite.
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[m][i] = __builtin_fmaf(w, static_cast<float>(t[i]), acc[m][i]);
+        ch[m] = product(x, hi, ch[m]);
+        cl[m] = product(x, lo, cl[m]);
       }
     }
+    // A weight of zero (a group past the row) adds nothing: the sums are finite.
+    const float w = P == 1 || g * P + p < ng ? half_value(nb) : 0.0f;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        acc[m][i] = __builtin_fmaf(w, static_cast<float>((ch[m][i] << 8) + cl[m][i]), acc[m][i]);
+    asm volatile("" ::: "memory");  // the next unit is stored after this one's reads
   }
-  // Result layout: register i of lane l is batch row 4 (l / 16) + i, output l % 16.
+  // Register i of lane (j, r) is activation row 4 j + i, output r.
+  float* const sums = reinterpret_cast<float*>(mine);
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) part[wave][m * 256 + (4 * j + i) * 16 + r] = acc[m][i];
+    for (int i = 0; i < 4; ++i) sums[(m * 4 + i) * kWave + lane] = acc[m][i];
   wait_lds_writes();
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int i = 0; i < 4; ++i) hold_value(acc[m][i]);
   __syncthreads();
-  for (int e = threadIdx.x; e < MT * 256; e += kFewBlock) {
-    float v = part[0][e];
+  for (int e = threadIdx.x; e < MT * kB * 16; e += W * kWave) {
+    const int b = e / 16, c = e % 16;
+    const int64_t o = n0 + c;
+    if (b >= batch || o >= a.n_out) continue;
+    float v = 0.0f;
 #pragma unroll
-    for (int w = 1; w < kFewWaves; ++w) v += part[w][e];
-    const int64_t b = b0 + e / 16, o = n0 + e % 16;
-    if (b >= a.batch || o >= a.n_out) continue;
-    v *= unit * a.scale[b];
+    for (int pp = 0; pp < P; ++pp) {
+      const int row = pp * kB + b % kB, at = (b / kB * 4 + row % 4) * kWave + row / 4 * 16 + c;
+#pragma unroll
+      for (int w = 0; w < W; ++w) v += reinterpret_cast<const float*>(stage + w * kWaveBytes)[at];
+    }
+    v *= unit * (e == static_cast<int>(threadIdx.x) ? s_first : a.scale[b]);
     if (a.y_bf16)
       store_elem<true>(a.y, b * a.n_out + o, v);
     else
@@ -300,7 +437,7 @@ gemm_q8_kernel(GemmQ8Args a, Q8Levels lv, float unit, float* part, int ksplit, i
       for (int s = 0; s < S; ++s)
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
-          const uint32_t sel = selectors<SB, CB>(cur[i], 4 * s + d);
+          const uint32_t sel = selectors<SB, false, CB>(cur[i], 4 * s + d);
           hi[s][d] = static_cast<int>(pick<SB>(lv.hi, sel));
           lo[s][d] = static_cast<int>(pick<SB>(lv.lo, sel));
         }
@@ -312,7 +449,7 @@ gemm_q8_kernel(GemmQ8Args a, Q8Levels lv, float unit, float* part, int ksplit, i
 #pragma unroll
         for (int s = 0; s < S; ++s) {
           const int c = i * (G / 16) + h * (G / 32) + s;
-          xo[s] = ordered<SB>(*reinterpret_cast<const i32x4*>(x + (r * CH + (c ^ (r & 7))) * 16));
+          xo[s] = ordered<SB, false>(*reinterpret_cast<const i32x4*>(x + (r * CH + (c ^ (r & 7))) * 16));
         }
         i32x16 t = {};
 #pragma unroll
@@ -396,6 +533,25 @@ hipError_t launch_join(const GemmQ8Args& a, const float* part, int ksplit, float
   return hipGetLastError();
 }
 
+// Turns 16 bytes (entry i at byte i) into the two tables of pick<4>().
+// first[i] = entry[i] ^ answer(second, i ^ 8) and second[i] = entry[8 + i] ^
+// answer(first, 8 + i), where answer(t, 8 .. 11) is the sign of t's byte 1,
+// 3, 5, 7 as a byte, answer(t, 12) = 0 and answer(t, 13 .. 15) = 255.  Bytes 5
+// and 7 depend on no sign, 3 on byte 7's, 1 on byte 3's, the others on these.
+void xor_tables(uint32_t (&table)[4]) {
+  uint8_t entry[16], t[2][8];
+  __builtin_memcpy(entry, table, 16);
+  auto answer = [&](int which, int sel) -> uint8_t {
+    if (sel >= 13) return 255;
+    if (sel == 12) return 0;
+    return t[which][2 * (sel - 8) + 1] & 0x80 ? 255 : 0;
+  };
+  for (const int i : {7, 5, 3, 1, 0, 2, 4, 6})
+    for (int which = 0; which < 2; ++which)
+      t[which][i] = static_cast<uint8_t>(entry[8 * which + i] ^ answer(1 - which, 8 + i));
+  __builtin_memcpy(table, t, 16);
+}
+
 // How a call is cut up; the same for the workspace size and the launch.
 struct Plan {
   int few;     // row tiles of 16 of the few-rows kernel, 0: the tiled kernel
@@ -409,7 +565,7 @@ constexpr int kCus = 256;
 Plan plan_for(int64_t n_out, int64_t k, int64_t batch, int group_size) {
   Plan p{};
   p.ksplit = 1;
-  if (batch <= kFewRows) {
+  if (batch <= (group_size > 128 ? kFewRows / 2 : kFewRows)) {
     p.few = static_cast<int>((batch + 15) / 16);
     return p;
   }
@@ -426,20 +582,23 @@ Plan plan_for(int64_t n_out, int64_t k, int64_t batch, int group_size) {
   return p;
 }
 
+template <int SB, int G, int MT, int P>
+hipError_t launch_few(const GemmQ8Args& a, const Q8Levels& lv, float unit, hipStream_t s) {
+  const dim3 grid(static_cast<uint32_t>((a.n_out + 15) / 16));
+  few_kernel<SB, G, MT, P, kFewWaves><<<grid, dim3(kFewWaves * kWave), 0, s>>>(a, lv, unit);
+  return hipGetLastError();
+}
+
 template <int SB, int G>
 hipError_t launch_for(const GemmQ8Args& a, const Q8Levels& lv, const Plan& p, float unit, float* ws, hipStream_t s) {
   if (p.few) {
-    const dim3 grid(static_cast<uint32_t>((a.n_out + 15) / 16), 1), block(kFewBlock);
-    constexpr int U = G >= 128 ? 2 : 4;
-    if (p.few == 1)
-      few_kernel<SB, G, 1, 2 * U><<<grid, block, 0, s>>>(a, lv, unit);
-    else if (p.few == 2)
-      few_kernel<SB, G, 2, U><<<grid, block, 0, s>>>(a, lv, unit);
-    else if (p.few == 3)
-      few_kernel<SB, G, 3, U><<<grid, block, 0, s>>>(a, lv, unit);
-    else
-      few_kernel<SB, G, 4, U><<<grid, block, 0, s>>>(a, lv, unit);
-    return hipGetLastError();
+    if (a.batch <= 8) return launch_few<SB, G, 1, 2>(a, lv, unit, s);
+    if (a.batch <= 16) return launch_few<SB, G, 2, 2>(a, lv, unit, s);
+    if (a.batch <= 32) return launch_few<SB, G, 2, 1>(a, lv, unit, s);
+    if constexpr (G <= 128) {
+      if (a.batch <= 48) return launch_few<SB, G, 3, 1>(a, lv, unit, s);
+      return launch_few<SB, G, 4, 1>(a, lv, unit, s);
+    }
   }
   const int64_t tiles = (a.n_out + kGemmCols - 1) / kGemmCols * ((a.batch + 32 * p.tm - 1) / (32 * p.tm));
   float* part = p.ksplit > 1 ? ws : nullptr;
@@ -470,8 +629,11 @@ hipError_t launch_gemm_q8_empty(const GemmQ8Args& a, hipStream_t s) {
   return launch_join(a, nullptr, 0, 0.0f, s);
 }
 
-hipError_t launch_gemm_q8(const GemmQ8Args& a, int sbits, int group_size, const Q8Levels& lv, float* ws,
-                          hipStream_t s) {
+hipError_t launch_gemm_q8(const GemmQ8Args& a, int sbits, int group_size, Q8Levels lv, float* ws, hipStream_t s) {
+  if (sbits == 4) {
+    xor_tables(lv.hi);
+    xor_tables(lv.lo);
+  }
   const Plan p = plan_for(a.n_out, a.k, a.batch, group_size);
   const float unit = lv.scale / __builtin_sqrtf(static_cast<float>(group_size));
   if (sbits == 2) return launch_bits<2>(a, group_size, lv, p, unit, ws, s);
