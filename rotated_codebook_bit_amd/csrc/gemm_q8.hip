@@ -15,6 +15,8 @@
 // two thirds of what split-bf16 activations and levels cost on the same
 // cores at half their rate each, and the activations are a quarter of the
 // bytes of float32.
+#include <type_traits>
+
 #include "lanes.h"
 
 namespace cq {
@@ -190,6 +192,9 @@ few_kernel(GemmQ8Args a, Q8Levels lv, float unit) {
   const int b_first = threadIdx.x / 16 % (MT * kB);
   const float s_first = a.scale[b_first < batch ? b_first : batch - 1];
 
+  // With up to 4 batch rows at P = 2 the later half of the loads holds none of
+  // them: not loaded, its activation rows only meet sums that are not stored.
+  const bool half = P == 2 && MT == 1 && F::kXLoads % 2 == 0 && batch <= kB / 2;
   // The pieces of a unit this lane moves.
   constexpr int kPer = F::kCodeRow / F::kCodePiece, kPerX = F::kXRow / 16;  // per output, per batch row
   CodePiece<F::kCodePiece> c_reg[F::kCodeLoads];
@@ -203,20 +208,20 @@ few_kernel(GemmQ8Args a, Q8Levels lv, float unit) {
       __builtin_memcpy(c_reg[i].w, tile + static_cast<int64_t>(row) * row_bytes + at, F::kCodePiece);
     }
 #if defined(__HIP_DEVICE_COMPILE__)
-    // Batch rows past the batch are outside the buffer (or, where a whole
-    // load is past it, not loaded: they only meet sums that are not stored).
+    // Batch rows past the batch are outside the buffer (read as zero).
     // Columns past k are the next row's, or outside; they are scaled by zero.
     const auto src = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(a.q), 0, static_cast<int>(batch * a.k), 0x00020000);
 #pragma unroll
     for (int i = 0; i < F::kXLoads; ++i) {
-      if (i * kWave / kPerX >= batch) break;
+      if (half && i >= F::kXLoads / 2) break;
       const int e = lane + i * kWave, b = e / kPerX;
       const uint32_t off = b < batch ? static_cast<uint32_t>(b * a.k + e % kPerX * 16) : 0x80000000u;
       x_reg[i] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(src, off, g * F::kXRow, 0));
     }
 #endif
   };
-  auto put = [&]() __attribute__((always_inline)) {
+  auto put_loads = [&](auto loads) __attribute__((always_inline)) {
+    constexpr int kLoads = decltype(loads)::value;
 #pragma unroll
     for (int i = 0; i < F::kCodeLoads; ++i) {
       const int e = lane + i * kWave;
@@ -224,13 +229,13 @@ few_kernel(GemmQ8Args a, Q8Levels lv, float unit) {
         __builtin_memcpy(__builtin_assume_aligned(mine + e / kPer * F::kCodeStride + e % kPer * F::kCodePiece, F::kCodePiece),
                          c_reg[i].w, F::kCodePiece);
     }
+    i32x4 x[kLoads];
 #pragma unroll
-    for (int i = 0; i < F::kXLoads; ++i) {
-      if (i * kWave / kPerX >= batch) break;
+    for (int i = 0; i < kLoads; ++i) {
       const int e = lane + i * kWave;
-      x_reg[i] = ordered<SB, SHUFFLE>(x_reg[i]);
+      x[i] = ordered<SB, SHUFFLE>(x_reg[i]);
       if (MT * kB * kPerX % kWave == 0 || e < MT * kB * kPerX)
-        *reinterpret_cast<i32x4*>(mine + F::kXAt + e / kPerX * F::kXStride + e % kPerX * 16) = x_reg[i];
+        *reinterpret_cast<i32x4*>(mine + F::kXAt + e / kPerX * F::kXStride + e % kPerX * 16) = x[i];
     }
     wait_lds_writes();
 #pragma unroll
@@ -238,7 +243,13 @@ few_kernel(GemmQ8Args a, Q8Levels lv, float unit) {
 #pragma unroll
       for (int d = 0; d < F::kCodePiece / 4; ++d) hold_value(c_reg[i].w[d]);
 #pragma unroll
-    for (int i = 0; i < F::kXLoads; ++i) hold_values(x_reg[i].x, x_reg[i].y, x_reg[i].z, x_reg[i].w);
+    for (int i = 0; i < kLoads; ++i) hold_values(x[i].x, x[i].y, x[i].z, x[i].w);
+  };
+  auto put = [&]() __attribute__((always_inline)) {
+    if (half)
+      put_loads(std::integral_constant<int, (F::kXLoads + 1) / 2>{});
+    else
+      put_loads(std::integral_constant<int, F::kXLoads>{});
   };
   if constexpr (F::kZeros > 0) {
     const i32x4 zero = {0, 0, 0, 0};
