@@ -372,11 +372,13 @@ few_kernel(GemmQ8Args a, Q8Levels lv, float unit) {
 // group; a wave decodes its outputs' codes once per group for all TM row
 // tiles.  The activations' next tile moves by direct-to-LDS loads into the
 // other buffer while this one is multiplied; 16-byte chunk c of row r lies at
-// slot c ^ (r & 7), so the operand reads (8 rows of one chunk) cover all
-// banks.
+// slot c ^ chunk_key(r), so that the operand reads, 16 rows of one chunk at a
+// time, cover all 64 banks.
 constexpr int kGemmWaves = 4;
 constexpr int kGemmBlock = kGemmWaves * kWave;
 constexpr int kGemmCols = 32 * kGemmWaves;
+constexpr uint32_t kBand = 8;
+__device__ __forceinline__ int chunk_key(int row) { return (row >> 1) & 7; }
 
 template <int SB, int G, int TM>
 __global__ void __launch_bounds__(kGemmBlock, 2)
@@ -392,11 +394,16 @@ gemm_q8_kernel(GemmQ8Args a, Q8Levels lv, float unit, float* part, int ksplit, i
   const int lane = threadIdx.x & (kWave - 1), c32 = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
 
-  // Consecutive logical blocks run on one XCD and share a weight tile.
+  // Consecutive logical blocks run on one XCD.  They go over bands of kBand
+  // output tiles, row tile by row tile: the 64 blocks that an XCD runs
+  // together share kBand weight tiles and 64 / kBand row tiles, which its L2
+  // holds for the whole of k.
   const uint32_t mt = static_cast<uint32_t>((a.batch + BM - 1) / BM);
   const uint32_t lb = xcd_block(blockIdx.x, gridDim.x);
   const uint32_t ks = lb % ksplit, tile = lb / ksplit;
-  const uint32_t ntile = tile / mt, mtile = tile - ntile * mt;
+  const uint32_t nt = static_cast<uint32_t>((a.n_out + kGemmCols - 1) / kGemmCols), band = tile / (kBand * mt);
+  const uint32_t wide = nt - band * kBand < kBand ? nt - band * kBand : kBand, in_band = tile - band * kBand * mt;
+  const uint32_t mtile = in_band / wide, ntile = band * kBand + in_band - mtile * wide;
   const int64_t m0 = static_cast<int64_t>(mtile) * BM;
   const int64_t n = static_cast<int64_t>(ntile) * kGemmCols + 32 * wave + c32;
   const int64_t nc = n < a.n_out ? n : a.n_out - 1;
@@ -406,21 +413,26 @@ gemm_q8_kernel(GemmQ8Args a, Q8Levels lv, float unit, float* part, int ksplit, i
   const uint8_t* const codes = a.packed + nc * ng * (G * SB / 8) + h * CB;
   const uint16_t* const norms = a.norms + nc * ng;
 
+  // Where this lane's pieces of a tile lie, from the tile's first column.
+  // Rows past the batch lie outside the buffer (they read zero), columns past
+  // k (the last tile at G < 128) are the next row's, or outside: they only
+  // meet weights of zero.
+  constexpr int kDma = BM * CH / kGemmBlock;
+  uint32_t x_off[kDma];
+#pragma unroll
+  for (int i = 0; i < kDma; ++i) {
+    const int slot = (i * kGemmWaves + wave) * kWave + lane, r = slot / CH, c = (slot % CH) ^ chunk_key(r);
+    x_off[i] = m0 + r < a.batch ? static_cast<uint32_t>(r * a.k + 16 * c) : 0x80000000u;
+  }
   auto issue = [&](int t, uint8_t* dst) __attribute__((always_inline)) {
 #if defined(__HIP_DEVICE_COMPILE__)
     const int rows = a.batch - m0 < BM ? static_cast<int>(a.batch - m0) : BM;
-    const int k = static_cast<int>(a.k);
-    const auto src = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(a.q + m0 * a.k), 0, rows * k, 0x00020000);
+    const auto src = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(a.q + m0 * a.k), 0, rows * static_cast<int>(a.k),
+                                                       0x00020000);
 #pragma unroll
-    for (int i = 0; i < BM * CH / kGemmBlock; ++i) {
-      const int slot0 = (i * kGemmWaves + wave) * kWave, slot = slot0 + lane;
-      const int r = slot / CH, c = (slot % CH) ^ (r & 7);
-      // Rows past the batch and columns past k are fetched from outside the
-      // buffer: they read zero.
-      const int col = t * KT + 16 * c;
-      const uint32_t off = r < rows && col < k ? static_cast<uint32_t>(r * k + col) : 0x80000000u;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (lds_ptr_t)(dst + 16 * slot0), 16, off, 0, 0, 0);
-    }
+    for (int i = 0; i < kDma; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (lds_ptr_t)(dst + 16 * ((i * kGemmWaves + wave) * kWave)), 16, x_off[i],
+                                               t * KT, 0, 0);
 #endif
   };
   // Groups past k (the last tile at G < 128): the last group's codes, scaled by zero.
@@ -453,25 +465,28 @@ gemm_q8_kernel(GemmQ8Args a, Q8Levels lv, float unit, float* part, int ksplit, i
           lo[s][d] = static_cast<int>(pick<SB>(lv.lo, sel));
         }
       const float w = half_value(ncur[i]);
+      // Row tile m's products are issued before row tile m - 1's sums are
+      // scaled, so that the vector operations run beside the matrix cores'.
+      i32x16 ch[2], cl[2];
+      auto finish = [&](int m) __attribute__((always_inline)) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          acc[m][e] = __builtin_fmaf(w, static_cast<float>((ch[m & 1][e] << 8) + cl[m & 1][e]), acc[m][e]);
+      };
 #pragma unroll
       for (int m = 0; m < TM; ++m) {
         const int r = 32 * m + c32;
-        i32x4 xo[S];
+        ch[m & 1] = cl[m & 1] = i32x16{};
 #pragma unroll
         for (int s = 0; s < S; ++s) {
           const int c = i * (G / 16) + h * (G / 32) + s;
-          xo[s] = ordered<SB, false>(*reinterpret_cast<const i32x4*>(x + (r * CH + (c ^ (r & 7))) * 16));
+          const i32x4 xo = ordered<SB, false>(*reinterpret_cast<const i32x4*>(x + (r * CH + (c ^ chunk_key(r))) * 16));
+          ch[m & 1] = __builtin_amdgcn_mfma_i32_32x32x32_i8(xo, hi[s], ch[m & 1], 0, 0, 0);
+          cl[m & 1] = __builtin_amdgcn_mfma_i32_32x32x32_i8(xo, lo[s], cl[m & 1], 0, 0, 0);
         }
-        i32x16 t = {};
-#pragma unroll
-        for (int s = 0; s < S; ++s) t = __builtin_amdgcn_mfma_i32_32x32x32_i8(xo[s], hi[s], t, 0, 0, 0);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) t[e] <<= 8;
-#pragma unroll
-        for (int s = 0; s < S; ++s) t = __builtin_amdgcn_mfma_i32_32x32x32_i8(xo[s], lo[s], t, 0, 0, 0);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) acc[m][e] = __builtin_fmaf(w, static_cast<float>(t[e]), acc[m][e]);
+        if (m > 0) finish(m - 1);
       }
+      finish(TM - 1);
     }
   };
   auto step = [&](int t, const uint8_t* x, uint8_t* other) __attribute__((always_inline)) {
@@ -500,24 +515,62 @@ gemm_q8_kernel(GemmQ8Args a, Q8Levels lv, float unit, float* part, int ksplit, i
     if (t + 1 < t_end) step(t + 1, xt1, xt0);
   }
 
-  // Result layout: register e of lane l is batch row 8 (e / 4) + 4 (l / 32) + e % 4, output l % 32.
-  if (n >= a.n_out) return;
+  // Result layout: register e of lane l is batch row 8 (e / 4) + 4 (l / 32) +
+  // e % 4 of its row tile, output l % 32.  The rows' scales go through LDS
+  // once; every address is a uniform row plus the lane's own offset.
+  float* const sc = reinterpret_cast<float*>(xt0);  // all waves are past their last tile
+  if (!part) {
+    float v = 0.0f;
+    if (threadIdx.x < BM) {
+      v = m0 + threadIdx.x < a.batch ? unit * a.scale[m0 + threadIdx.x] : 0.0f;
+      sc[threadIdx.x] = v;
+    }
+    wait_lds_writes();
+    hold_value(v);
+    __syncthreads();
+  }
+  const bool inside = m0 + BM <= a.batch && static_cast<int64_t>(ntile + 1) * kGemmCols <= a.n_out;  // the whole block tile
+  auto uniform_row = [](int m, int e) { return 32 * m + 8 * (e / 4) + e % 4; };
+  const uint32_t lane_at = static_cast<uint32_t>(4 * h * a.n_out + n);  // n_out <= 2^27
+  float* const to_part = part + (static_cast<int64_t>(ks) * a.batch + m0) * a.n_out;
+  uint8_t* const to_y = a.y + m0 * a.n_out * (a.y_bf16 ? 2 : 4);
 #pragma unroll
-  for (int m = 0; m < TM; ++m)
+  for (int m = 0; m < TM; ++m) {
+    float4 s4[4];
+    if (!part) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s4[i] = *reinterpret_cast<const float4*>(sc + 32 * m + 8 * i + 4 * h);
+    }
+    auto value = [&](int e) __attribute__((always_inline)) {
+      const float4& q4 = s4[e / 4];
+      return acc[m][e] * (e % 4 == 0 ? q4.x : e % 4 == 1 ? q4.y : e % 4 == 2 ? q4.z : q4.w);
+    };
+    if (inside && !part && a.y_bf16 && a.n_out % 2 == 0) {
+      // Two columns per store: the even lane of a pair stores row e, the odd
+      // one row e + 1, each with its neighbour's value.
+      const bool odd = lane & 1;
+      const uint32_t pair_at = lane_at - odd + (odd ? static_cast<uint32_t>(a.n_out) : 0u);
+#pragma unroll
+      for (int e = 0; e < 16; e += 2) {
+        const float v0 = value(e), v1 = value(e + 1);
+        const float mine = odd ? v1 : v0, other = dpp_move<0xB1>(odd ? v0 : v1);
+        uint16_t* row = reinterpret_cast<uint16_t*>(to_y) + static_cast<int64_t>(uniform_row(m, e)) * a.n_out;
+        *reinterpret_cast<uint32_t*>(row + pair_at) = odd ? pack_bf16(other, mine) : pack_bf16(mine, other);
+      }
+      continue;
+    }
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      const int64_t b = m0 + 32 * m + 8 * (e / 4) + 4 * h + e % 4;
-      if (b >= a.batch) continue;
-      if (part) {
-        part[(static_cast<int64_t>(ks) * a.batch + b) * a.n_out + n] = acc[m][e];
-        continue;
-      }
-      const float v = acc[m][e] * (unit * a.scale[b]);
-      if (a.y_bf16)
-        store_elem<true>(a.y, b * a.n_out + n, v);
+      const int row = uniform_row(m, e);
+      if (!inside && (n >= a.n_out || m0 + row + 4 * h >= a.batch)) continue;
+      if (part)
+        (to_part + static_cast<int64_t>(row) * a.n_out)[lane_at] = acc[m][e];
+      else if (a.y_bf16)
+        (reinterpret_cast<uint16_t*>(to_y) + static_cast<int64_t>(row) * a.n_out)[lane_at] = one_bf16(value(e));
       else
-        store_elem<false>(a.y, b * a.n_out + n, v);
+        (reinterpret_cast<float*>(to_y) + static_cast<int64_t>(row) * a.n_out)[lane_at] = value(e);
     }
+  }
 }
 
 // y from the ksplit partial sums, added in order; zeros from none.
