@@ -12,10 +12,18 @@
 //
 // Gradient: grad[v] = scale * sum of dout[i] over the positions i with
 // token i = v, added in position order.  The positions are sorted by token
-// (a stable radix sort), so that every table row is written once, by one
-// wave per 256 columns, with no atomics and no order that changes between
-// runs.  Tokens that occur more than kSegment times are cut into pieces of
-// the sorted list, whose sums are added in order afterwards.
+// (a stable radix sort); then the sorted list is cut into pieces of 64
+// positions, and a wave streams the rows of dout of one piece over 256
+// columns, writing a table row where a token's run ends: no atomics, and no
+// order that changes between runs.  Runs longer than a piece leave one sum
+// per piece, which are added in order afterwards.  The rows of absent tokens,
+// most of the bytes at training sizes, are cleared by a plain fill that runs
+// beside the sort.
+// 16384 bf16 rows of 4096 into 32000 rows of float32 (0.66 GB): 95 us for the
+// fill with the sort (36 us alone) beside it, 55 for the sums, 9 to join long
+// runs, 4.1 TB/s over all; a block per table row that searched the sorted list
+// for its run, zeros included, took 250.  With cached instead of streaming
+// stores the fill takes 75 us and the sums, behind its write-backs, 76.
 #include <utility>
 
 #include "lanes.h"
@@ -174,7 +182,6 @@ embed_packed_kernel(EmbedArgs a, LevelTable lv, int64_t units, uint32_t per_row)
 // ---- Gradient: sorting the positions by token --------------------------------------------
 
 constexpr int kDigit = 256;       // 8-bit digits, least significant first
-constexpr int kSortTile = 4096;   // keys per block of the many-block sort
 constexpr int kSortOne = 16384;   // keys that one block sorts by itself
 
 // Sort key: the token, or vocab (past every row) where it is outside the table.
@@ -238,17 +245,42 @@ __device__ __forceinline__ uint32_t digit_scan(uint32_t v, uint32_t* part) {
   return before + x - v;
 }
 
+// Zeros over the gradient by block `block` of `blocks`, in contiguous pieces
+// of 64 bytes per thread.
+constexpr int kClearBytes = 64;
+constexpr int64_t kMaxClear = int64_t(1) << 30;
+__device__ __forceinline__ void clear_grad(const EmbedGradArgs& a, int64_t block, int64_t blocks) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  const int64_t bytes = a.vocab * a.dim * (a.grad_bf16 ? 2 : 4), whole = bytes / 16, each = blockDim.x * (kClearBytes / 16);
+  u32x4* const to = reinterpret_cast<u32x4*>(a.grad);
+  for (int64_t first = block * each; first < whole; first += blocks * each) {
+#pragma unroll
+    for (int k = 0; k < kClearBytes / 16; ++k) {
+      const int64_t i = first + k * static_cast<int64_t>(blockDim.x) + threadIdx.x;
+      if (i < whole) __builtin_nontemporal_store(u32x4{0, 0, 0, 0}, to + i);
+    }
+  }
+  if (block == 0 && threadIdx.x < bytes % 16 / 2) reinterpret_cast<uint16_t*>(to + whole)[threadIdx.x] = 0;
+}
+// Blocks of `threads` threads that clear all of it, at most `most` (none when
+// accumulating).
+uint32_t clear_blocks(const EmbedGradArgs& a, int threads, int64_t most) {
+  const int64_t bytes = a.accumulate ? 0 : a.vocab * a.dim * (a.grad_bf16 ? 2 : 4), each = threads * kClearBytes;
+  const int64_t want = (bytes + each - 1) / each;
+  return static_cast<uint32_t>(want < most ? want : most);
+}
+
 // The whole sort in one block of 16 waves: wave w holds the keys
 // 64 IPT w .. of the current order, IPT per lane.  Positions past n carry the
-// largest key and stay last.
+// largest key and stay last.  The launch's other blocks clear the gradient.
 constexpr int kOneThreads = 1024, kOneWaves = kOneThreads / kWave;
 template <int IPT>
 __global__ void __launch_bounds__(kOneThreads)
 sort_one_kernel(EmbedGradArgs a, int passes, uint32_t* __restrict__ keys, uint32_t* __restrict__ order) {
   __shared__ uint32_t hist[kOneWaves][kDigit];
   __shared__ uint32_t part[kDigit / kWave];
-  __shared__ uint32_t xkey[kOneThreads * IPT];
-  __shared__ uint32_t xpos[kOneThreads * IPT];
+  __shared__ uint32_t moved[kOneThreads * IPT];  // the keys, then the positions, on their way
+  if (blockIdx.x > 0) return clear_grad(a, blockIdx.x - 1, gridDim.x - 1);
   const int t = threadIdx.x, lane = t & (kWave - 1), wave = t / kWave;
   const int first = wave * kWave * IPT + lane;
   const int n = static_cast<int>(a.n);
@@ -290,20 +322,20 @@ sort_one_kernel(EmbedGradArgs a, int passes, uint32_t* __restrict__ keys, uint32
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < IPT; ++i) {
-      const uint32_t to = rank[i] + hist[wave][(key[i] >> (8 * pass)) & (kDigit - 1)];
-      xkey[to] = key[i];
-      xpos[to] = pos[i];
-    }
-    wait_lds_writes();
+    for (int i = 0; i < IPT; ++i) rank[i] += hist[wave][(key[i] >> (8 * pass)) & (kDigit - 1)];
+    auto move = [&](uint32_t (&v)[IPT]) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < IPT; ++i) hold_values(key[i], pos[i]);
-    __syncthreads();
+      for (int i = 0; i < IPT; ++i) moved[rank[i]] = v[i];
+      wait_lds_writes();
 #pragma unroll
-    for (int i = 0; i < IPT; ++i) {
-      key[i] = xkey[first + i * kWave];
-      pos[i] = xpos[first + i * kWave];
-    }
+      for (int i = 0; i < IPT; ++i) hold_value(v[i]);
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < IPT; ++i) v[i] = moved[first + i * kWave];
+      __syncthreads();
+    };
+    move(key);
+    move(pos);
   }
 #pragma unroll
   for (int i = 0; i < IPT; ++i) {
@@ -319,7 +351,7 @@ sort_one_kernel(EmbedGradArgs a, int passes, uint32_t* __restrict__ keys, uint32
 // counts in counts[tile][256]; scatter_kernel adds the counts of smaller
 // digits and of earlier tiles itself (tiles * 1 KiB from the L2, a fraction
 // of a tile's own keys up to thousands of tiles) and moves its tile's keys.
-constexpr int kTileIpt = kSortTile / kBlock;
+constexpr int kTileIpt = 8, kSortTile = kTileIpt * kBlock;  // 2048 keys per block
 
 __device__ __forceinline__ void tile_keys(const EmbedGradArgs& a, const uint32_t* keys, const uint32_t* order,
                                           uint32_t (&key)[kTileIpt], uint32_t (&pos)[kTileIpt]) {
@@ -336,8 +368,9 @@ __device__ __forceinline__ void tile_keys(const EmbedGradArgs& a, const uint32_t
 }
 
 __global__ void __launch_bounds__(kBlock)
-count_kernel(EmbedGradArgs a, int shift, const uint32_t* __restrict__ keys, uint32_t* __restrict__ counts) {
+count_kernel(EmbedGradArgs a, int shift, const uint32_t* __restrict__ keys, uint32_t* __restrict__ counts, uint32_t tiles) {
   __shared__ uint32_t hist[kDigit];
+  if (blockIdx.x >= tiles) return clear_grad(a, blockIdx.x - tiles, gridDim.x - tiles);
   const uint32_t zero = 0;
   hist[threadIdx.x] = zero;
   wait_lds_writes();
@@ -404,9 +437,7 @@ scatter_kernel(EmbedGradArgs a, int shift, const uint32_t* __restrict__ counts, 
 
 // ---- Gradient: the sums -------------------------------------------------------------
 
-constexpr int kSegment = 64;   // longest run of one token that one wave adds by itself
 constexpr int kSlice = 256;    // columns per wave: four per lane
-constexpr int kRowsMax = 32;   // table rows per block
 
 // First sorted index whose key is at least v.
 __device__ __forceinline__ uint32_t lower_bound(const uint32_t* __restrict__ keys, uint32_t n, uint32_t v) {
@@ -418,6 +449,42 @@ __device__ __forceinline__ uint32_t lower_bound(const uint32_t* __restrict__ key
     len = right ? len - half - 1 : half;
   }
   return lo;
+}
+
+// The runs of equal keys that meet piece c, positions lo .. lo + count - 1.
+template <int PIECE>
+struct Runs {
+  uint32_t lo, count, key;  // key: of position lo + lane
+  uint64_t starts;          // bit l: a run starts at position lo + l
+  uint32_t head;            // positions of a run that began in an earlier piece
+  bool head_long;           // that run is longer than a piece
+  uint32_t last;            // where the last run that starts here starts (PIECE: none starts here)
+  uint32_t beyond;          // its positions past the piece, at most PIECE
+  bool last_long;           // it is longer than a piece
+};
+template <int PIECE>
+__device__ __forceinline__ Runs<PIECE> find_runs(const uint32_t* __restrict__ keys, uint32_t n, uint32_t c, int lane) {
+  Runs<PIECE> r;
+  r.lo = c * PIECE;
+  r.count = n - r.lo < PIECE ? n - r.lo : PIECE;
+  const uint32_t none = 0xFFFFFFFFu;  // no key
+  const bool here = lane < static_cast<int>(r.count);
+  r.key = keys[here ? r.lo + lane : r.lo];
+  const uint32_t before = c > 0 && lane < PIECE ? keys[r.lo - PIECE + lane] : none;  // a piece back
+  const uint32_t after = lane < PIECE && r.lo + PIECE + lane < n ? keys[r.lo + PIECE + lane] : none;
+  const uint32_t left = __shfl_up(r.key, 1, kWave), edge = __builtin_amdgcn_readlane(before, PIECE - 1);
+  r.starts = __ballot(here && r.key != (lane == 0 ? edge : left));
+  const uint32_t first = r.starts ? static_cast<uint32_t>(__builtin_ctzll(r.starts)) : r.count;
+  r.head = first;
+  // A run that began earlier and whose last position here is l is longer than
+  // a piece if the position PIECE before l is its own too.
+  r.head_long = first > 0 && __builtin_amdgcn_readlane(before, first - 1) == __builtin_amdgcn_readlane(r.key, first - 1);
+  r.last = r.starts ? 63 - static_cast<uint32_t>(__builtin_clzll(r.starts)) : PIECE;
+  const uint32_t tail = __builtin_amdgcn_readlane(r.key, r.count - 1);
+  const uint64_t differs = __ballot(after != tail);  // lanes past the piece hold no key: set where PIECE < 64
+  r.beyond = differs ? static_cast<uint32_t>(__builtin_ctzll(differs)) : 64;
+  r.last_long = r.starts && r.count - r.last + r.beyond > PIECE;
+  return r;
 }
 
 // Four columns of lane `lane` in slice s: consecutive (WIDE), or 64 apart.
@@ -476,31 +543,6 @@ __device__ __forceinline__ void store_four(uint8_t* row, bool bf16, int64_t s, i
   }
 }
 
-// Sum of dout rows order[lo .. hi) over one slice, in order.
-template <bool BF16, bool WIDE>
-__device__ __forceinline__ void add_rows(const EmbedGradArgs& a, const uint32_t* __restrict__ order, uint32_t lo,
-                                         uint32_t hi, int64_t s, int lane, float (&acc)[4]) {
-#pragma unroll
-  for (int k = 0; k < 4; ++k) acc[k] = 0.0f;
-  const int64_t bytes = a.dim * Piece<BF16>::kBytes;
-  uint32_t j = lo;
-  for (; j + 4 <= hi; j += 4) {
-    float v[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) load_four<BF16, WIDE>(a.dout + order[j + i] * bytes, s, lane, a.dim, v[i]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) acc[k] += v[i][k];
-  }
-  for (; j < hi; ++j) {
-    float v[4];
-    load_four<BF16, WIDE>(a.dout + order[j] * bytes, s, lane, a.dim, v);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) acc[k] += v[k];
-  }
-}
-
 // Scaled sum into grad row v (added to it when accumulating).
 template <bool WIDE>
 __device__ __forceinline__ void put_row(const EmbedGradArgs& a, int64_t v, int64_t s, int lane, float (&acc)[4]) {
@@ -517,68 +559,70 @@ __device__ __forceinline__ void put_row(const EmbedGradArgs& a, int64_t v, int64
   store_four<WIDE>(row, a.grad_bf16, s, lane, a.dim, acc);
 }
 
-// Blocks [0, piece_blocks): piece c of kSegment sorted positions, 1024
-// columns.  A run longer than kSegment that meets the piece holds its first or
-// its last position; the sum of the run's part goes to slot 2c (the run of
-// the first position) or 2c + 1 (a later run, the last position's).
-// The other blocks: `rows` table rows each, all columns; runs of up to
-// kSegment positions are added and every absent row is cleared.
-template <bool BF16, bool WIDE>
+// Piece c over 1024 columns, 256 per wave: the rows of dout in sorted order,
+// eight in flight, added into acc; where a run ends, its sum goes to its row,
+// or for a run longer than a piece to partial slot 2c (a run that goes on
+// from an earlier piece, or fills this one) or 2c + 1.
+template <bool BF16, bool WIDE, int PIECE>
 __global__ void __launch_bounds__(kBlock)
 embed_grad_kernel(EmbedGradArgs a, const uint32_t* __restrict__ keys, const uint32_t* __restrict__ order,
-                  float* __restrict__ partial, uint32_t piece_blocks, int rows) {
-  __shared__ uint32_t start[kRowsMax + 1];
+                  float* __restrict__ partial) {
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const uint32_t n = static_cast<uint32_t>(a.n);
   const int64_t slices = (a.dim + kSlice - 1) / kSlice;
-  if (blockIdx.x < piece_blocks) {
-    const uint32_t per = static_cast<uint32_t>((slices + kWaves - 1) / kWaves);
-    const uint32_t c = blockIdx.x / per;
-    const int64_t s = static_cast<int64_t>(blockIdx.x - c * per) * kWaves + wave;
-    if (s >= slices) return;
-    const uint32_t lo = c * kSegment, hi = lo + kSegment < n ? lo + kSegment : n;
-    const uint32_t k0 = keys[lo], k1 = keys[hi - 1];
-    // Lanes 0 .. 3: where the runs of k0 and k1 begin and end.
-    const uint32_t b = lower_bound(keys, n, (lane & 2 ? k1 : k0) + (lane & 1));
-    const uint32_t s0 = __builtin_amdgcn_readlane(b, 0), e0 = __builtin_amdgcn_readlane(b, 1);
-    const uint32_t s1 = __builtin_amdgcn_readlane(b, 2), e1 = __builtin_amdgcn_readlane(b, 3);
-    float acc[4];
-    if (k0 < a.vocab && e0 - s0 > kSegment) {
-      add_rows<BF16, WIDE>(a, order, lo, e0 < hi ? e0 : hi, s, lane, acc);
-      store_four<WIDE>(reinterpret_cast<uint8_t*>(partial + 2 * static_cast<int64_t>(c) * a.dim), false, s, lane, a.dim, acc);
+  const uint32_t per = static_cast<uint32_t>((slices + kWaves - 1) / kWaves);
+  const uint32_t c = blockIdx.x / per;
+  const int64_t s = static_cast<int64_t>(blockIdx.x - c * per) * kWaves + wave;
+  if (s >= slices) return;
+  const Runs<PIECE> r = find_runs<PIECE>(keys, n, c, lane);
+  // Positions from the piece's first that this wave adds, all of them or from
+  // the first run that starts here, to the piece's end or that of its last run.
+  const uint32_t from = r.head_long ? 0 : r.head;
+  const uint32_t to = r.last < PIECE && !r.last_long ? r.count + r.beyond : r.count;
+  const uint32_t o0 = lane < static_cast<int>(r.count) ? order[r.lo + lane] : 0;
+  const uint32_t o1 = r.lo + PIECE + lane < n ? order[r.lo + PIECE + lane] : 0;
+  const int64_t bytes = a.dim * Piece<BF16>::kBytes;
+  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  const uint64_t ends = r.starts >> 1;  // bit l: position l is a run's last
+  constexpr int kAhead = 8;
+  for (uint32_t l0 = from; l0 < to; l0 += kAhead) {
+    float v[kAhead][4];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const uint32_t l = l0 + i < to ? l0 + i : to - 1;
+      const uint32_t row = l < PIECE ? __builtin_amdgcn_readlane(o0, l) : __builtin_amdgcn_readlane(o1, l - PIECE);
+      load_four<BF16, WIDE>(a.dout + row * bytes, s, lane, a.dim, v[i]);
     }
-    if (k1 != k0 && k1 < a.vocab && e1 - s1 > kSegment) {
-      add_rows<BF16, WIDE>(a, order, s1, hi, s, lane, acc);
-      store_four<WIDE>(reinterpret_cast<uint8_t*>(partial + (2 * static_cast<int64_t>(c) + 1) * a.dim), false, s, lane, a.dim, acc);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const uint32_t l = l0 + i;
+      if (l >= to) break;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[k] += v[i][k];
+      const bool end = l + 1 == to || (l < PIECE && ((ends >> l) & 1));
+      if (!end) continue;
+      const uint32_t at = l < r.count ? l : r.count - 1;  // the run's key is the piece's last key past its end
+      const uint32_t key = __builtin_amdgcn_readlane(r.key, at);
+      if (key < a.vocab) {
+        const bool head = at < r.head, whole = head ? r.head_long : at >= r.last && r.last_long;
+        if (whole) {
+          const int64_t slot = 2 * static_cast<int64_t>(c) + (head || r.last == 0 ? 0 : 1);
+          store_four<WIDE>(reinterpret_cast<uint8_t*>(partial + slot * a.dim), false, s, lane, a.dim, acc);
+        } else {
+          put_row<WIDE>(a, key, s, lane, acc);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[k] = 0.0f;
     }
-    return;
-  }
-  const int64_t v0 = static_cast<int64_t>(blockIdx.x - piece_blocks) * rows;
-  const int here = a.vocab - v0 < rows ? static_cast<int>(a.vocab - v0) : rows;
-  if (threadIdx.x <= here) {
-    const uint32_t b = lower_bound(keys, n, static_cast<uint32_t>(v0 + threadIdx.x));
-    start[threadIdx.x] = b;
-    wait_lds_writes();
-    hold_value(b);
-  }
-  __syncthreads();
-  const int64_t units = here * slices;
-  for (int64_t u = wave; u < units; u += kWaves) {
-    const int r = static_cast<int>(u / slices);
-    const int64_t s = u - r * slices;
-    const uint32_t lo = __builtin_amdgcn_readfirstlane(start[r]), hi = __builtin_amdgcn_readfirstlane(start[r + 1]);
-    if (hi - lo > kSegment || (hi == lo && a.accumulate)) continue;
-    float acc[4];
-    add_rows<BF16, WIDE>(a, order, lo, hi, s, lane, acc);
-    put_row<WIDE>(a, v0 + r, s, lane, acc);
   }
 }
 
-// Rows of runs longer than kSegment: block (c, slice) serves the run that
+// Rows of runs longer than a piece: block (c, slice) serves the run that
 // begins in piece c, if any; its waves add a quarter of the pieces each, the
 // quarters are added in order.
-template <bool WIDE>
+template <bool WIDE, int PIECE>
 __global__ void __launch_bounds__(kBlock)
 embed_grad_join_kernel(EmbedGradArgs a, const uint32_t* __restrict__ keys, const float* __restrict__ partial) {
   __shared__ float sums[kWaves][kSlice];
@@ -588,17 +632,16 @@ embed_grad_join_kernel(EmbedGradArgs a, const uint32_t* __restrict__ keys, const
   const int64_t slices = (a.dim + kSlice - 1) / kSlice;
   const uint32_t c = static_cast<uint32_t>(blockIdx.x / slices);
   const int64_t s = blockIdx.x - c * slices;
-  const uint32_t lo = c * kSegment, hi = lo + kSegment < n ? lo + kSegment : n;
-  const uint32_t key = keys[hi - 1];
-  const uint32_t b = lower_bound(keys, n, key + (lane & 1));
-  const uint32_t first = __builtin_amdgcn_readlane(b, 0), end = __builtin_amdgcn_readlane(b, 1);
-  if (key >= a.vocab || first < lo || end - first <= kSegment) return;  // the whole block
-  const uint32_t pieces = (end - 1) / kSegment - c + 1, quarter = (pieces + kWaves - 1) / kWaves;
+  const Runs<PIECE> r = find_runs<PIECE>(keys, n, c, lane);
+  const uint32_t key = __builtin_amdgcn_readlane(r.key, r.count - 1);
+  if (!r.last_long || key >= a.vocab) return;  // the whole block
+  const uint32_t end = __builtin_amdgcn_readfirstlane(lower_bound(keys, n, key + 1));
+  const uint32_t pieces = (end - 1) / PIECE - c + 1, quarter = (pieces + kWaves - 1) / kWaves;
   const uint32_t p0 = wave * quarter, p1 = p0 + quarter < pieces ? p0 + quarter : pieces;
   float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
   for (uint32_t p = p0; p < p1; ++p) {
-    const int64_t slot = p == 0 && first != lo ? 2 * static_cast<int64_t>(c) + 1 : 2 * static_cast<int64_t>(c + p);
+    const int64_t slot = p == 0 && r.last != 0 ? 2 * static_cast<int64_t>(c) + 1 : 2 * static_cast<int64_t>(c + p);
     float v[4];
     load_four<false, WIDE>(reinterpret_cast<const uint8_t*>(partial + slot * a.dim), s, lane, a.dim, v);
 #pragma unroll
@@ -621,7 +664,12 @@ embed_grad_join_kernel(EmbedGradArgs a, const uint32_t* __restrict__ keys, const
 uint32_t blocks_of(int64_t waves) { return static_cast<uint32_t>((waves + kWaves - 1) / kWaves); }
 
 int64_t align256(int64_t b) { return (b + 255) & ~int64_t(255); }
-int64_t pieces_of(int64_t n) { return (n + kSegment - 1) / kSegment; }
+// Positions per piece: short lists in small pieces, so that enough waves
+// stream them (777 float32 rows of 1000: 8.0 us in pieces
+// of 16, 12.6 of 32, 21.2 of 64; 16384 bf16 rows of 4096 51.0, 54.9, 56.3, and
+// 14.4, 8.9, 6.2 us to join the longer runs).
+int piece_of(int64_t n) { return n <= 8192 ? 16 : n <= 65536 ? 32 : 64; }
+int64_t pieces_of(int64_t n) { return (n + piece_of(n) - 1) / piece_of(n); }
 
 // Workspace: sorted keys and positions (twice in the many-block sort), the
 // tiles' digit counts, the pieces' sums.
@@ -633,7 +681,7 @@ GradSpace grad_space(int64_t n, int64_t dim) {
   g.list = align256(4 * n);
   const bool many = n > kSortOne;
   g.counts = many ? align256((n + kSortTile - 1) / kSortTile * kDigit * 4) : 0;
-  g.partial = n > kSegment ? align256(2 * pieces_of(n) * dim * 4) : 0;
+  g.partial = n > piece_of(n) ? align256(2 * pieces_of(n) * dim * 4) : 0;
   g.total = g.list * (many ? 4 : 2) + g.counts + g.partial;
   return g;
 }
@@ -671,25 +719,17 @@ hipError_t launch_embed_at(const EmbedArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <bool WIDE>
+template <bool WIDE, int PIECE>
 hipError_t launch_grad_sums(const EmbedGradArgs& a, const uint32_t* keys, const uint32_t* order, float* partial,
                             hipStream_t s) {
   const int64_t slices = (a.dim + kSlice - 1) / kSlice;
-  const bool runs = a.n > kSegment;  // a longer run than kSegment may exist
-  const int64_t pb = runs ? pieces_of(a.n) * ((slices + kWaves - 1) / kWaves) : 0;
-  // Rows per block: about 8 blocks per CU, so that the blocks' searches for
-  // their rows' runs hide behind other blocks' stores.
-  int64_t rows = a.vocab / (8 * static_cast<int64_t>(device_cu_count()));
-  rows = rows < 1 ? 1 : rows > kRowsMax ? kRowsMax : rows;
-  const int64_t blocks = pb + (a.vocab + rows - 1) / rows;
+  const dim3 grid(static_cast<uint32_t>(pieces_of(a.n) * ((slices + kWaves - 1) / kWaves)));
   if (a.dout_bf16)
-    embed_grad_kernel<true, WIDE><<<dim3(static_cast<uint32_t>(blocks)), dim3(kBlock), 0, s>>>(
-        a, keys, order, partial, static_cast<uint32_t>(pb), static_cast<int>(rows));
+    embed_grad_kernel<true, WIDE, PIECE><<<grid, dim3(kBlock), 0, s>>>(a, keys, order, partial);
   else
-    embed_grad_kernel<false, WIDE><<<dim3(static_cast<uint32_t>(blocks)), dim3(kBlock), 0, s>>>(
-        a, keys, order, partial, static_cast<uint32_t>(pb), static_cast<int>(rows));
-  if (runs)
-    embed_grad_join_kernel<WIDE><<<dim3(static_cast<uint32_t>(pieces_of(a.n) * slices)), dim3(kBlock), 0, s>>>(
+    embed_grad_kernel<false, WIDE, PIECE><<<grid, dim3(kBlock), 0, s>>>(a, keys, order, partial);
+  if (a.n > PIECE)  // a run may be longer than a piece
+    embed_grad_join_kernel<WIDE, PIECE><<<dim3(static_cast<uint32_t>(pieces_of(a.n) * slices)), dim3(kBlock), 0, s>>>(
         a, keys, partial);
   return hipGetLastError();
 }
@@ -722,19 +762,22 @@ hipError_t launch_embed_grad(const EmbedGradArgs& a, uint8_t* ws, hipStream_t s)
   while (passes < 4 && (a.vocab >> (8 * passes))) ++passes;
   if (a.n <= kSortOne) {
     partial = reinterpret_cast<float*>(at(2 * g.list));
+    // Beside the sort's LDS two blocks fit a CU: that many, looping.
+    const dim3 grid(1 + clear_blocks(a, kOneThreads, 2 * static_cast<int64_t>(device_cu_count()))), block(kOneThreads);
     if (a.n > 4 * kOneThreads)
-      sort_one_kernel<16><<<dim3(1), dim3(kOneThreads), 0, s>>>(a, passes, keys, order);
+      sort_one_kernel<16><<<grid, block, 0, s>>>(a, passes, keys, order);
     else if (a.n > kOneThreads)
-      sort_one_kernel<4><<<dim3(1), dim3(kOneThreads), 0, s>>>(a, passes, keys, order);
-    else if (a.n > 0)
-      sort_one_kernel<1><<<dim3(1), dim3(kOneThreads), 0, s>>>(a, passes, keys, order);
+      sort_one_kernel<4><<<grid, block, 0, s>>>(a, passes, keys, order);
+    else
+      sort_one_kernel<1><<<grid, block, 0, s>>>(a, passes, keys, order);
   } else {
     uint32_t *keys2 = at(2 * g.list), *order2 = at(3 * g.list), *counts = at(4 * g.list);
     partial = reinterpret_cast<float*>(at(4 * g.list + g.counts));
-    const dim3 grid(static_cast<uint32_t>((a.n + kSortTile - 1) / kSortTile)), block(kBlock);
+    const uint32_t tiles = static_cast<uint32_t>((a.n + kSortTile - 1) / kSortTile);
+    const dim3 grid(tiles), block(kBlock);
     const uint32_t *in_keys = nullptr, *in_order = nullptr;  // the first pass reads the tokens
     for (int p = 0; p < passes; ++p) {
-      count_kernel<<<grid, block, 0, s>>>(a, 8 * p, in_keys, counts);
+      count_kernel<<<dim3(tiles + (p == 0 ? clear_blocks(a, kBlock, kMaxClear) : 0)), block, 0, s>>>(a, 8 * p, in_keys, counts, tiles);
       scatter_kernel<<<grid, block, 0, s>>>(a, 8 * p, counts, in_keys, in_order, keys2, order2);
       in_keys = keys2;
       in_order = order2;
@@ -743,10 +786,15 @@ hipError_t launch_embed_grad(const EmbedGradArgs& a, uint8_t* ws, hipStream_t s)
     }
     // The last pass wrote what the swap made `keys` and `order`.
   }
+  if (a.n == 0) return hipGetLastError();
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  return a.dim % 4 == 0 ? launch_grad_sums<true>(a, keys, order, partial, s)
-                        : launch_grad_sums<false>(a, keys, order, partial, s);
+  const bool wide = a.dim % 4 == 0;
+  if (piece_of(a.n) == 16)
+    return wide ? launch_grad_sums<true, 16>(a, keys, order, partial, s) : launch_grad_sums<false, 16>(a, keys, order, partial, s);
+  if (piece_of(a.n) == 32)
+    return wide ? launch_grad_sums<true, 32>(a, keys, order, partial, s) : launch_grad_sums<false, 32>(a, keys, order, partial, s);
+  return wide ? launch_grad_sums<true, 64>(a, keys, order, partial, s) : launch_grad_sums<false, 64>(a, keys, order, partial, s);
 }
 
 }  // namespace cq
