@@ -38,16 +38,28 @@ __device__ __forceinline__ int64_t token_at(const void* tokens, int bytes, int64
   return bytes == 8 ? static_cast<const int64_t*>(tokens)[i] : static_cast<const int32_t*>(tokens)[i];
 }
 
+// Lookups of 4 MiB and more leave with streaming stores: 8192 rows of 4096 to
+// bf16 from 4 bits 19.2 us instead of 21.6, to float32 from 2 bits 22.6 (25.4),
+// dense bf16 16.3 (17.2).  Smaller ones stay in the caches for what reads them.
+constexpr int64_t kStreamBytes = int64_t(4) << 20;
+
 // E consecutive output columns from column c of a row of dim columns; WIDE:
 // rows start on and hold whole 16-byte pieces.
-template <bool BF16, int E, bool WIDE>
+template <bool BF16, int E, bool WIDE, bool STREAM>
 __device__ __forceinline__ void store_columns(uint8_t* row, int64_t c, int64_t dim, const float (&v)[E]) {
   if constexpr (WIDE) {
     if (c >= dim) return;
     constexpr int V = Piece<BF16>::kElems;
-    uint4* o = reinterpret_cast<uint4*>(row + c * Piece<BF16>::kBytes);
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    u32x4* o = reinterpret_cast<u32x4*>(row + c * Piece<BF16>::kBytes);
 #pragma unroll
-    for (int i = 0; i < E / V; ++i) o[i] = pack_piece<BF16>(v + i * V);
+    for (int i = 0; i < E / V; ++i) {
+      const u32x4 u = __builtin_bit_cast(u32x4, pack_piece<BF16>(v + i * V));
+      if constexpr (STREAM)
+        __builtin_nontemporal_store(u, o + i);
+      else
+        o[i] = u;
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < E; ++i)
@@ -59,16 +71,15 @@ __device__ __forceinline__ void store_columns(uint8_t* row, int64_t c, int64_t d
 
 // One wave per unit: 64 E columns of one token's row, E = 8 when either type
 // is bf16, else 4.
-template <bool IN16, bool OUT16, bool WIDE>
+template <bool IN16, bool OUT16, bool WIDE, bool STREAM>
 __global__ void __launch_bounds__(kBlock)
-embed_kernel(EmbedArgs a, int64_t units, uint32_t per_row) {
+embed_kernel(EmbedArgs a, uint32_t units, uint32_t per_row) {
   constexpr int E = IN16 || OUT16 ? 8 : 4, V = Piece<IN16>::kElems;
   const int lane = threadIdx.x & (kWave - 1);
-  const int64_t u = static_cast<int64_t>(blockIdx.x) * kWaves +
-                    __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const uint32_t u = blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   if (u >= units) return;
-  const int64_t i = u / per_row;
-  const int64_t c = ((u - i * per_row) * kWave + lane) * E;
+  const uint32_t i = u / per_row;
+  const int64_t c = static_cast<int64_t>((u - i * per_row) * kWave + lane) * E;
   const int64_t tok = token_at(a.tokens, a.token_bytes, i);
   const bool in = tok >= 0 && tok < a.vocab;
   float v[E];
@@ -89,7 +100,7 @@ embed_kernel(EmbedArgs a, int64_t units, uint32_t per_row) {
 #pragma unroll
     for (int k = 0; k < E; ++k) v[k] = 0.0f;
   }
-  store_columns<OUT16, E, WIDE>(a.out + i * a.dim * Piece<OUT16>::kBytes, c, a.dim, v);
+  store_columns<OUT16, E, WIDE, STREAM>(a.out + i * a.dim * Piece<OUT16>::kBytes, c, a.dim, v);
 }
 
 // ---- Lookup from CQ storage ----------------------------------------------------------
@@ -115,10 +126,11 @@ __device__ __forceinline__ uint32_t load_codes(const uint8_t* p, int within, int
   }
 }
 
-// P units of 64 E columns per wave, their loads issued together.
+// P units of 64 E columns of one row per wave, their loads issued together
+// (P = 4 for large lookups: 2 and 8 were no faster); per_row: waves per row.
 template <int SB, bool OUT16, bool WIDE, int P>
 __global__ void __launch_bounds__(kBlock)
-embed_packed_kernel(EmbedArgs a, LevelTable lv, int64_t units, uint32_t per_row) {
+embed_packed_kernel(EmbedArgs a, LevelTable lv, uint32_t waves, uint32_t per_row) {
   constexpr int E = OUT16 ? 8 : 4;
   constexpr int FB = SB == kTritStorage ? 2 : SB;
   __shared__ float tab[kMaxLevels];  // 16 banks: any mix of codes reads without conflict
@@ -137,32 +149,31 @@ embed_packed_kernel(EmbedArgs a, LevelTable lv, int64_t units, uint32_t per_row)
   }
   __syncthreads();
   const int lane = threadIdx.x & (kWave - 1), label = lane_label(lane);
-  const int64_t u0 = (static_cast<int64_t>(blockIdx.x) * kWaves +
-                      __builtin_amdgcn_readfirstlane(threadIdx.x / kWave)) * P;
+  const uint32_t w = blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  if (w >= waves) return;
+  const uint32_t i = w / per_row;
+  const int64_t first = static_cast<int64_t>(w - i * per_row) * (P * kWave * E) + label * E;  // this lane's columns
+  const int64_t tok = token_at(a.tokens, a.token_bytes, i);
+  const bool in = tok >= 0 && tok < a.vocab;
   const int shift = __builtin_ctz(a.group);
-  const int64_t ngr = (a.dim + a.group - 1) >> shift, row_bytes = ngr * a.gbytes;
+  const int64_t ngr = (a.dim + a.group - 1) >> shift;
+  const uint8_t* const packed = a.packed + (in ? tok : 0) * ngr * a.gbytes;
+  const uint16_t* const norms = a.norms + (in ? tok : 0) * ngr;
   uint32_t raw[P];
   float f[P];
-  int64_t col[P], tok_i[P];
 #pragma unroll
   for (int j = 0; j < P; ++j) {
-    const int64_t u = u0 + j < units ? u0 + j : units - 1;
-    const int64_t i = u / per_row;
-    const int64_t c = ((u - i * per_row) * kWave + label) * E;
-    const int64_t tok = token_at(a.tokens, a.token_bytes, i);
-    tok_i[j] = i;
-    col[j] = c;
     raw[j] = 0;
     f[j] = 0.0f;
-    if (tok >= 0 && tok < a.vocab) {
-      int64_t g = c >> shift;
-      const int within = g < ngr ? static_cast<int>(c & (a.group - 1)) : 0;
-      g = g < ngr ? g : 0;
-      raw[j] = load_codes<SB, E>(a.packed + tok * row_bytes + g * a.gbytes, within, a.gbytes, trits);
-      f[j] = static_cast<float>(__builtin_bit_cast(_Float16, a.norms[tok * ngr + g]));
+    if (in) {  // a token outside the table has norms of zero
+      const int64_t c = first + j * (kWave * E), g = c >> shift;
+      const int64_t gc = g < ngr ? g : 0;
+      raw[j] = load_codes<SB, E>(packed + gc * a.gbytes, static_cast<int>(c & (a.group - 1)), a.gbytes, trits);
+      f[j] = static_cast<float>(__builtin_bit_cast(_Float16, norms[gc]));
     }
   }
-  const float unit = a.scale / static_cast<float>(a.group);
+  const float unit = label_sign(label, a.group / E) * a.scale / static_cast<float>(a.group);
+  uint8_t* const out = a.out + i * a.dim * Piece<OUT16>::kBytes;
 #pragma unroll
   for (int j = 0; j < P; ++j) {
     float y[E];
@@ -171,11 +182,9 @@ embed_packed_kernel(EmbedArgs a, LevelTable lv, int64_t units, uint32_t per_row)
     lane_butterfly(y);
     label_butterfly(y, label, a.group / E);
     const float s = f[j] * unit;
-    // A token outside the table has a zero row, whatever its codes decode to.
 #pragma unroll
-    for (int k = 0; k < E; ++k) y[k] = s == 0.0f ? 0.0f : y[k] * s;
-    if (u0 + j < units)
-      store_columns<OUT16, E, WIDE>(a.out + tok_i[j] * a.dim * Piece<OUT16>::kBytes, col[j], a.dim, y);
+    for (int k = 0; k < E; ++k) y[k] *= s;
+    store_columns<OUT16, E, WIDE, (P > 1)>(out, first + j * (kWave * E), a.dim, y);
   }
 }
 
@@ -686,18 +695,21 @@ GradSpace grad_space(int64_t n, int64_t dim) {
   return g;
 }
 
+template <int SB, bool OUT16, bool WIDE, int P>
+hipError_t launch_packed_units(const EmbedArgs& a, const LevelTable& lv, int64_t units, hipStream_t s) {
+  const int64_t per_row = (units + P - 1) / P, waves = a.n * per_row;
+  embed_packed_kernel<SB, OUT16, WIDE, P><<<dim3(blocks_of(waves)), dim3(kBlock), 0, s>>>(
+      a, lv, static_cast<uint32_t>(waves), static_cast<uint32_t>(per_row));
+  return hipGetLastError();
+}
+
 template <int SB, bool OUT16, bool WIDE>
 hipError_t launch_packed_at(const EmbedArgs& a, const LevelTable& lv, hipStream_t s) {
-  const int64_t per_row = (a.dim + kWave * (OUT16 ? 8 : 4) - 1) / (kWave * (OUT16 ? 8 : 4));
-  const int64_t units = a.n * per_row;
-  // Few units: one per wave, to spread over the CUs.
-  if (units < 16 * static_cast<int64_t>(device_cu_count()))
-    embed_packed_kernel<SB, OUT16, WIDE, 1><<<dim3(blocks_of(units)), dim3(kBlock), 0, s>>>(
-        a, lv, units, static_cast<uint32_t>(per_row));
-  else
-    embed_packed_kernel<SB, OUT16, WIDE, 4><<<dim3(blocks_of((units + 3) / 4)), dim3(kBlock), 0, s>>>(
-        a, lv, units, static_cast<uint32_t>(per_row));
-  return hipGetLastError();
+  const int64_t units = (a.dim + kWave * (OUT16 ? 8 : 4) - 1) / (kWave * (OUT16 ? 8 : 4));  // per row
+  // Few units in all: one per wave, to spread over the CUs.
+  if (a.n * a.dim * (OUT16 ? 2 : 4) < kStreamBytes)
+    return launch_packed_units<SB, OUT16, WIDE, 1>(a, lv, units, s);
+  return launch_packed_units<SB, OUT16, WIDE, 4>(a, lv, units, s);
 }
 
 template <int SB>
@@ -710,12 +722,16 @@ hipError_t launch_packed_for(const EmbedArgs& a, const LevelTable& lv, hipStream
 template <bool IN16, bool OUT16>
 hipError_t launch_embed_at(const EmbedArgs& a, hipStream_t s) {
   constexpr int E = IN16 || OUT16 ? 8 : 4;
-  const int64_t per_row = (a.dim + kWave * E - 1) / (kWave * E), units = a.n * per_row;
+  const int64_t per_row = (a.dim + kWave * E - 1) / (kWave * E);
+  const uint32_t units = static_cast<uint32_t>(a.n * per_row);
   const dim3 grid(blocks_of(units)), block(kBlock);
-  if (a.dim % E == 0)
-    embed_kernel<IN16, OUT16, true><<<grid, block, 0, s>>>(a, units, static_cast<uint32_t>(per_row));
+  const bool wide = a.dim % E == 0, stream = a.n * a.dim * (OUT16 ? 2 : 4) >= kStreamBytes;
+  if (wide && stream)
+    embed_kernel<IN16, OUT16, true, true><<<grid, block, 0, s>>>(a, units, static_cast<uint32_t>(per_row));
+  else if (wide)
+    embed_kernel<IN16, OUT16, true, false><<<grid, block, 0, s>>>(a, units, static_cast<uint32_t>(per_row));
   else
-    embed_kernel<IN16, OUT16, false><<<grid, block, 0, s>>>(a, units, static_cast<uint32_t>(per_row));
+    embed_kernel<IN16, OUT16, false, false><<<grid, block, 0, s>>>(a, units, static_cast<uint32_t>(per_row));
   return hipGetLastError();
 }
 

@@ -33,16 +33,17 @@ __device__ __forceinline__ float dpp_move(float v) {
 // lane_label(l); within 8 lanes only the upper four are reversed.
 __device__ __forceinline__ int lane_label(int lane) { return lane ^ ((lane & 4) ? 3 : 0); }
 
-// One butterfly stage over label bit BIT: the lane whose bit is clear holds a
-// and takes a + b, its partner holds b and takes a - b (the rounded fma).
-// `label` is this lane's label.
+// One butterfly stage over label bit BIT; `label` is this lane's label.  Bits
+// 0 to 3: the lane whose bit is clear holds a and takes b + a, its partner
+// holds b and takes b - a, the negated difference; both lanes of a later pair
+// are negated alike, so label_sign() puts all signs right at the end.
 template <int BIT, int N>
 __device__ __forceinline__ void label_stage(float (&y)[N], int label) {
   const float sgn = ((label >> BIT) & 1) ? -1.0f : 1.0f;
   if constexpr (BIT < 4) {
     constexpr int kCtrl = BIT == 0 ? 0xB1 : BIT == 1 ? 0x4E : BIT == 2 ? 0x141 : 0x128;
 #pragma unroll
-    for (int i = 0; i < N; ++i) y[i] = __builtin_fmaf(sgn, y[i], dpp_move<kCtrl>(y[i]));
+    for (int i = 0; i < N; ++i) y[i] = __builtin_fmaf(dpp_move<kCtrl>(y[i]), sgn, y[i]);
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -57,7 +58,8 @@ __device__ __forceinline__ void label_stage(float (&y)[N], int label) {
   }
 }
 
-// Butterfly over LABELS lanes (a power of two, run time, 1 .. 64).
+// Butterfly over `labels` lanes (a power of two, run time, 1 .. 64), times
+// label_sign(label, labels).
 template <int N>
 __device__ __forceinline__ void label_butterfly(float (&y)[N], int label, int labels) {
   if (labels > 1) label_stage<0>(y, label);
@@ -66,6 +68,9 @@ __device__ __forceinline__ void label_butterfly(float (&y)[N], int label, int la
   if (labels > 8) label_stage<3>(y, label);
   if (labels > 16) label_stage<4>(y, label);
   if (labels > 32) label_stage<5>(y, label);
+}
+__device__ __forceinline__ float label_sign(int label, int labels) {
+  return __popc(label & (labels - 1) & 15) & 1 ? -1.0f : 1.0f;
 }
 
 // Butterfly stages of pair distances 1 .. N/2 inside a lane.

@@ -1000,8 +1000,8 @@ int check_lookup(const void* tokens, int token_bytes, int64_t n, int64_t vocab, 
   if (!std::isfinite(scale)) return fail(CQ_ERR_ARG, "scale is not finite");
   if (n > kMaxIndex || vocab > kMaxIndex || dim > kMaxIndex || !fits(n, dim, 4) || !fits(vocab, dim, 4))
     return fail(CQ_ERR_UNSUPPORTED, "n, vocab and dim must be at most 2^31 - 2");
-  // One block of four waves, each at least 256 columns.
-  if (n && ceil_div(dim, 256) > (int64_t(1) << 32) / n)
+  // Waves of 256 columns are counted in 32 bits.
+  if (n && ceil_div(dim, 256) > ((int64_t(1) << 32) - 4) / n)
     return fail(CQ_ERR_UNSUPPORTED, "n * dim is past this call's grid");
   if (n && dim && !tokens) return fail(CQ_ERR_NULL, "tokens is NULL");
   if (!aligned(tokens, token_bytes)) return fail(CQ_ERR_ALIGN, "tokens need %d-byte alignment", token_bytes);

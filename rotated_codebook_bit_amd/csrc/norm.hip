@@ -236,6 +236,7 @@ norm_kernel(NormArgs a) {
     const bool finite = top < 0x7F800000u;
     // Below 2^-118 the reciprocal would leave float32: such a row is zero.
     const float inv = finite && amax >= 0x1.0p-118f ? 127.0f / amax : 0.0f;
+    const float signed_inv = label_sign(label, a.labels) * inv;
     if (t == 0) a.scale[row] = !finite ? __builtin_nanf("") : inv == 0.0f ? 0.0f : amax * a.unit;
     int8_t* const q = a.q + first;
 #pragma unroll
@@ -247,7 +248,7 @@ norm_kernel(NormArgs a) {
       uint32_t b[V];
 #pragma unroll
       for (int k = 0; k < V; ++k)
-        b[k] = inv == 0.0f ? 0u : __builtin_bit_cast(uint32_t, __builtin_fmaf(h[c * V + k], inv, 12582912.0f));
+        b[k] = inv == 0.0f ? 0u : __builtin_bit_cast(uint32_t, __builtin_fmaf(h[c * V + k], signed_inv, 12582912.0f));
       uint32_t u[V / 4];
 #pragma unroll
       for (int k = 0; k < V / 4; ++k) {
