@@ -72,6 +72,13 @@ def lib() -> ctypes.CDLL:
     if _lib is None:
         if not os.path.exists(LIB_PATH):
             raise ImportError(f"{LIB_PATH} is missing: run `python -m rotated_codebook_bit_amd.build`")
+        # PyTorch brings a HIP runtime of its own.  Loaded after libcq it would
+        # be a second one in the process, and streams and memory of one mean
+        # nothing to the other: calls failed and the process crashed.
+        try:
+            import torch  # noqa: F401
+        except ImportError:
+            pass  # the host-only calls work without it
         L = ctypes.CDLL(LIB_PATH)
         i64, i32, vp = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p
         L.cq_layout.argtypes = [i64, i64, i32, i32, ctypes.POINTER(i64), ctypes.POINTER(i64)]

@@ -215,8 +215,8 @@ few_kernel(GemmQ8Args a, Q8Levels lv, float unit) {
     for (int i = 0; i < F::kXLoads; ++i) {
       if (half && i >= F::kXLoads / 2) break;
       const int e = lane + i * kWave, b = e / kPerX;
-      const uint32_t off = b < batch ? static_cast<uint32_t>(b * a.k + e % kPerX * 16) : 0x80000000u;
-      x_reg[i] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(src, off, g * F::kXRow, 0));
+      const uint32_t off = b < batch ? static_cast<uint32_t>(b * a.k + e % kPerX * 16 + g * F::kXRow) : 0x80000000u;
+      x_reg[i] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(src, off, 0, 0));
     }
 #endif
   };
@@ -431,8 +431,8 @@ gemm_q8_kernel(GemmQ8Args a, Q8Levels lv, float unit, float* part, int ksplit, i
                                                        0x00020000);
 #pragma unroll
     for (int i = 0; i < kDma; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (lds_ptr_t)(dst + 16 * ((i * kGemmWaves + wave) * kWave)), 16, x_off[i],
-                                               t * KT, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (lds_ptr_t)(dst + 16 * ((i * kGemmWaves + wave) * kWave)), 16,
+                                               x_off[i] + t * KT, 0, 0, 0);
 #endif
   };
   // Groups past k (the last tile at G < 128): the last group's codes, scaled by zero.

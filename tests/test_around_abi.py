@@ -4,6 +4,8 @@ anything is enqueued, so no GPU is needed."""
 
 import ctypes
 import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -142,6 +144,17 @@ def test_q8_levels_of_odd_tables():
         cq.q8_levels(2, [1, 2, 3, nan])
     with pytest.raises(cq.CQError):
         cq.q8_levels(9)
+
+
+def test_one_hip_runtime_whatever_is_imported_first():
+    """A process that calls the library before it imports torch still has
+    torch's HIP runtime only: two of them do not share streams or memory."""
+    pytest.importorskip("torch")
+    code = ("import rotated_codebook_bit_amd as cq; cq.q8_levels(2); import torch; "
+            "print(len({l.split()[-1] for l in open('/proc/self/maps') if 'libamdhip64' in l}))")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, check=True).stdout
+    assert int(out) <= 1
 
 
 def test_binding_refuses_host_tensors():
