@@ -220,7 +220,10 @@ matvec_pair_rot_kernel(MatvecArgs a, LevelTable lv, int log2g, int rows_per_bloc
     }
     // 3. Pair tables: thread (w, lane) builds pairs 4 w .. 4 w + 3 of the
     //    lane's 64 columns (columns 64 lane + 8 w .. 64 lane + 8 w + 7).
-    if (active) {
+    //    Lanes without columns build theirs too, from the zeros stored above:
+    //    step 4 looks them up, and what the LDS held before may be a NaN,
+    //    which a norm of 0 does not take out of a sum.
+    {
       const float* src = xs + xpad(64 * lane + 8 * w);
       const float4 p = *reinterpret_cast<const float4*>(src);
       const float4 q = *reinterpret_cast<const float4*>(src + 4);
@@ -266,7 +269,8 @@ matvec_pair_rot_kernel(MatvecArgs a, LevelTable lv, int log2g, int rows_per_bloc
           part[d >> 1] = (d & 1) || qq ? part[d >> 1] + v : v;
         }
       }
-      // Lanes without columns in the pass read codes 0 and norms 0: they add 0.
+      // Lanes without columns in the pass read codes 0 and norms 0, and their
+      // table entries are products of zeros: they add 0.
       const float n_lo = static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(nrm[r])));
       if constexpr (TWO_NORMS) {
         const float n_hi = static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(nrm[r] >> 16)));
