@@ -275,9 +275,6 @@ norm_grad_kernel(NormGradArgs a) {
   constexpr int V = Piece<BF16>::kElems, EB = Piece<BF16>::kBytes, N = C * V;
   constexpr int kTeams = NT < 256 ? 256 / NT : 1, kWaves = NT / kWave;
   constexpr int R = WIDE ? C : N;  // loads of one array per row
-  // The widest rows have no registers left for the weights and the next row:
-  // LEAN reads weights and dsum where they are used, and nothing ahead.
-  constexpr bool LEAN = N >= 32 || (!WIDE && N >= 16);
   typedef typename std::conditional<WIDE, uint4, uint32_t>::type Raw;
   __shared__ float red[2][2 * kWaves];
   __shared__ float team_dw[kTeams > 1 ? kTeams * NT * N : 1];
@@ -286,21 +283,16 @@ norm_grad_kernel(NormGradArgs a) {
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kTeams;
 
   constexpr int M = WIDE ? V : 1;  // elements of one load
-  float w[LEAN ? 1 : N], dw[N];
+  float w[N], dw[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) dw[i] = 0.0f;
-  // Weights of load i.
-  const void* weight = a.weight;
-  auto weights = [&](int i, float* v) __attribute__((always_inline)) {
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
     const int p = i * NT + t;
     if constexpr (WIDE)
-      load_weights<V>(weight, a.w_bf16, static_cast<int64_t>(p < np ? p : 0) * V, v);
+      load_weights<V>(a.weight, a.w_bf16, static_cast<int64_t>(p < np ? p : 0) * V, w + i * V);
     else
-      v[0] = load_weight(weight, a.w_bf16, p < cols ? p : 0);
-  };
-  if constexpr (!LEAN) {
-#pragma unroll
-    for (int i = 0; i < R; ++i) weights(i, w + i * M);
+      w[i] = load_weight(a.weight, a.w_bf16, p < cols ? p : 0);
   }
 
   auto load = [&](const uint8_t* base, int64_t row, Raw (&v)[R]) __attribute__((always_inline)) {
@@ -339,44 +331,29 @@ norm_grad_kernel(NormGradArgs a) {
     return WIDE ? (i / V) * NT + t < np : i * NT + t < cols;
   };
 
-  constexpr int RD = LEAN ? 1 : R;
-  Raw h[R], dy[R], ds[RD];
+  Raw h[R], dy[R], ds[R];
   int64_t row = static_cast<int64_t>(blockIdx.x) * kTeams + team;
   int turn = 0;
-  if constexpr (!LEAN) {
-    if (row < a.rows) {
-      load(a.sum, row, h);
-      load(a.dout, row, dy);
-      if (a.dsum) load(a.dsum, row, ds);
-    }
+  if (row < a.rows) {
+    load(a.sum, row, h);
+    load(a.dout, row, dy);
+    if (a.dsum) load(a.dsum, row, ds);
   }
   while (row < a.rows) {
     const int64_t next = row + stride;
-    Raw h2[RD], dy2[RD], ds2[RD];
-    if constexpr (LEAN) {
-#if defined(__HIP_DEVICE_COMPILE__)
-      asm volatile("" : "+s"(weight));  // keeps the loads in the loop: hoisted, they would take N registers
-#endif
-      load(a.sum, row, h);
-      load(a.dout, row, dy);
-    } else if (next < a.rows) {
+    Raw h2[R], dy2[R], ds2[R];
+    if (next < a.rows) {
       load(a.sum, next, h2);
       load(a.dout, next, dy2);
       if (a.dsum) load(a.dsum, next, ds2);
     }
     float ss = 0.0f, dot = 0.0f;
 #pragma unroll
-    for (int l = 0; l < R; ++l) {
-      float wl[M];
-      if constexpr (LEAN) weights(l, wl);
-#pragma unroll
-      for (int j = 0; j < M; ++j) {
-        const int i = l * M + j;
-        const float hv = inside(i) ? value(h, i) : 0.0f;
-        const float u = (LEAN ? wl[j] : w[LEAN ? 0 : i]) * value(dy, i);
-        ss = __builtin_fmaf(hv, hv, ss);
-        dot = inside(i) ? __builtin_fmaf(u, hv, dot) : dot;
-      }
+    for (int i = 0; i < N; ++i) {
+      const float hv = inside(i) ? value(h, i) : 0.0f;
+      const float u = w[i] * value(dy, i);
+      ss = __builtin_fmaf(hv, hv, ss);
+      dot = inside(i) ? __builtin_fmaf(u, hv, dot) : dot;
     }
     ss = wave_sum(ss);
     dot = wave_sum(dot);
@@ -405,29 +382,13 @@ norm_grad_kernel(NormGradArgs a) {
 #pragma unroll
     for (int l = 0; l < R; ++l) {
       const int p = l * NT + t;
-      float wl[M], dl[M], d[M];
-      if constexpr (LEAN) {
-        weights(l, wl);
-        if (a.dsum) {
-          const uint8_t* p0 = a.dsum + row * a.cols * EB;
-          if constexpr (WIDE)
-            unpack_piece<BF16>(reinterpret_cast<const uint4*>(p0)[p < np ? p : 0], dl);
-          else
-            dl[0] = load_elem<BF16>(p0, p < cols ? p : 0);
-        }
-      }
+      float d[M];
 #pragma unroll
       for (int j = 0; j < M; ++j) {
         const int i = l * M + j;
         const float hv = value(h, i), g = value(dy, i);
-        float v = __builtin_fmaf(-hv, k, r * ((LEAN ? wl[j] : w[LEAN ? 0 : i]) * g));
-        if (a.dsum) {
-          if constexpr (LEAN)
-            v += dl[j];
-          else
-            v += value(ds, i);
-        }
-        d[j] = v;
+        d[j] = __builtin_fmaf(-hv, k, r * (w[i] * g));
+        if (a.dsum) d[j] += value(ds, i);
         if (inside(i)) dw[i] = __builtin_fmaf(g, hv * r, dw[i]);
       }
       if constexpr (WIDE) {
@@ -436,13 +397,11 @@ norm_grad_kernel(NormGradArgs a) {
         if (p < cols) store_elem<BF16>(out, p, d[0]);
       }
     }
-    if constexpr (!LEAN) {
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
-        h[i] = h2[i];
-        dy[i] = dy2[i];
-        ds[i] = ds2[i];
-      }
+    for (int i = 0; i < R; ++i) {
+      h[i] = h2[i];
+      dy[i] = dy2[i];
+      ds[i] = ds2[i];
     }
     row = next;
   }
@@ -473,10 +432,10 @@ norm_grad_kernel(NormGradArgs a) {
   }
 }
 
-// Gradient of rows past 1024 pieces.  Such a row does not fit the registers
-// beside its share of dw: the block reads it twice (the second time from the
-// L2, a row is at most 128 KiB) and keeps dw in LDS, each column with the
-// thread that owns it.
+// Gradient of wide rows.  Such a row does not fit the registers beside its
+// share of dw: the block reads it twice (the second time from the L2, a row is
+// at most 128 KiB) and keeps dw in LDS, each column with the thread that owns
+// it.
 constexpr int kWideThreads = 1024;
 template <bool BF16, bool WIDE, int COLS>
 __global__ void __launch_bounds__(kWideThreads)
@@ -605,37 +564,38 @@ hipError_t launch_norm_at(const NormArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <bool BF16, int NT, int C>
+template <bool BF16, bool WIDE, int NT, int C>
 hipError_t launch_norm_grad_at(const NormGradArgs& a, int blocks, hipStream_t s) {
-  const dim3 grid(blocks), block(NT < 256 ? 256 : NT);
-  if (a.cols % Piece<BF16>::kElems == 0)
-    norm_grad_kernel<BF16, NT, C, true><<<grid, block, 0, s>>>(a);
-  else
-    norm_grad_kernel<BF16, NT, C, false><<<grid, block, 0, s>>>(a);
+  norm_grad_kernel<BF16, NT, C, WIDE><<<dim3(blocks), dim3(NT < 256 ? 256 : NT), 0, s>>>(a);
   return hipGetLastError();
 }
 
-template <bool BF16, int COLS>
+template <bool BF16, bool WIDE>
 hipError_t launch_norm_grad_wide(const NormGradArgs& a, int blocks, hipStream_t s) {
-  if (a.cols % Piece<BF16>::kElems == 0)
-    norm_grad_wide_kernel<BF16, true, COLS><<<dim3(blocks), dim3(kWideThreads), 0, s>>>(a);
+  const dim3 grid(blocks), block(kWideThreads);
+  if (a.cols <= kNormMaxCols / 2)
+    norm_grad_wide_kernel<BF16, WIDE, kNormMaxCols / 2><<<grid, block, 0, s>>>(a);
   else
-    norm_grad_wide_kernel<BF16, false, COLS><<<dim3(blocks), dim3(kWideThreads), 0, s>>>(a);
+    norm_grad_wide_kernel<BF16, WIDE, kNormMaxCols><<<grid, block, 0, s>>>(a);
   return hipGetLastError();
 }
 
-// A row's pieces: 64-element units (8 bf16 or 16 float32 pieces) decide the
-// team.  Rows of up to 64 C pieces go to one wave (no barrier), wider ones to
-// 4 and 16 waves.
+// The row's pieces of 16 bytes decide its team: one wave (no barrier) up to 64
+// pieces, 4 waves up to 1024, then 16.  From 65 to 128 pieces one wave is the
+// faster one with many rows: bf16 rows of 1024, one wave and four, 512 rows
+// 3.2 and 3.0 us, 4096 rows 7.2 and 6.2, 8192 rows 10.6 and 11.8; to 8 bits,
+// where each lane does more, 512 rows 3.8 and 3.2, 2048 rows 4.8 and 5.8, 4096
+// rows 6.6 and 9.2.  From 513 to 1024 pieces 16 waves are with few: rows of
+// 8192, 4 waves and 16, one row 2.9 and 2.0 us (to 8 bits 4.3 and 2.9), 512
+// rows 6.4 and 6.6 (7.8 and 6.7), 1024 rows 10.9 and 12.0 (12.2 and 12.7).
 template <bool BF16>
 hipError_t launch_norm_for(const NormArgs& a, hipStream_t s) {
-  const int64_t np = (a.cols + Piece<BF16>::kElems - 1) / Piece<BF16>::kElems;
-  const bool few = a.rows < 4 * static_cast<int64_t>(device_cu_count());
+  const int64_t np = (a.cols + Piece<BF16>::kElems - 1) / Piece<BF16>::kElems, cus = device_cu_count();
   if (np <= 64) return launch_norm_at<BF16, 64, 1>(a, s);
-  if (np <= 128 && !few) return launch_norm_at<BF16, 64, 2>(a, s);
-  if (np <= 256 && !few) return launch_norm_at<BF16, 64, 4>(a, s);
+  if (np <= 128 && a.rows >= (a.q ? 8 : 32) * cus) return launch_norm_at<BF16, 64, 2>(a, s);
   if (np <= 256) return launch_norm_at<BF16, 256, 1>(a, s);
   if (np <= 512) return launch_norm_at<BF16, 256, 2>(a, s);
+  if (np <= 1024 && a.rows <= 2 * cus) return launch_norm_at<BF16, 1024, 1>(a, s);
   if (np <= 1024) return launch_norm_at<BF16, 256, 4>(a, s);
   if (np <= 2048) return launch_norm_at<BF16, 1024, 2>(a, s);
   if (np <= 4096) return launch_norm_at<BF16, 1024, 4>(a, s);
@@ -643,16 +603,36 @@ hipError_t launch_norm_for(const NormArgs& a, hipStream_t s) {
   return hipErrorInvalidValue;
 }
 
-template <bool BF16>
+// Rows that one wave takes, 4 of them to a block; others take the block.
+bool norm_grad_one_wave(int64_t cols, bool bf16) {
+  const int64_t v = bf16 ? 8 : 4, np = (cols + v - 1) / v;
+  return np <= 64 || (np <= 128 && (cols % v == 0 || !bf16));
+}
+
+// Up to 8 elements per lane the row, the next one and dw stay in registers
+// (one element per load) and up to 16 in whole pieces.  Rows beyond that go to
+// the wide kernel: bf16, 8192 columns, 256 rows 7.1 us (11.1 from registers,
+// 32 elements per lane), 4096 rows 67.3 (73.3); 4001 columns, 4096 rows 38.5
+// (81.0, 16 single elements).  So do up to four rows per CU of 16 elements per
+// lane: bf16, 4096 columns, 300 rows 5.9 us (8.0), 1024 rows 10.8 (11.8), 4096
+// rows 34.9 (26.6); float32 7.0 (7.0), 13.4 (14.5), 48.2 (44.2).
+template <bool BF16, bool WIDE>
 hipError_t launch_norm_grad_for(const NormGradArgs& a, int blocks, hipStream_t s) {
   const int64_t np = (a.cols + Piece<BF16>::kElems - 1) / Piece<BF16>::kElems;
-  if (np <= 64) return launch_norm_grad_at<BF16, 64, 1>(a, blocks, s);
-  if (np <= 128) return launch_norm_grad_at<BF16, 64, 2>(a, blocks, s);
-  if (np <= 256) return launch_norm_grad_at<BF16, 256, 1>(a, blocks, s);
-  if (np <= 512) return launch_norm_grad_at<BF16, 256, 2>(a, blocks, s);
-  if (np <= 1024) return launch_norm_grad_at<BF16, 256, 4>(a, blocks, s);
-  if (a.cols <= kNormMaxCols / 2) return launch_norm_grad_wide<BF16, kNormMaxCols / 2>(a, blocks, s);
-  return launch_norm_grad_wide<BF16, kNormMaxCols>(a, blocks, s);
+  if (np <= 64) return launch_norm_grad_at<BF16, WIDE, 64, 1>(a, blocks, s);
+  if constexpr (WIDE || !BF16) {
+    if (np <= 128) return launch_norm_grad_at<BF16, WIDE, 64, 2>(a, blocks, s);
+  }
+  if (np <= 256) return launch_norm_grad_at<BF16, WIDE, 256, 1>(a, blocks, s);
+  if constexpr (!BF16) {
+    if (np <= 512) return launch_norm_grad_at<BF16, WIDE, 256, 2>(a, blocks, s);
+  }
+  if constexpr (WIDE) {
+    constexpr int kPieces = BF16 ? 2 : 4;
+    if (np <= 256 * kPieces && a.rows > 4 * static_cast<int64_t>(device_cu_count()))
+      return launch_norm_grad_at<BF16, WIDE, 256, kPieces>(a, blocks, s);
+  }
+  return launch_norm_grad_wide<BF16, WIDE>(a, blocks, s);
 }
 
 }  // namespace
@@ -664,15 +644,16 @@ hipError_t launch_norm(const NormArgs& a, bool bf16, hipStream_t s) {
 // Blocks of the gradient: as many as there are rows, up to two per CU of the
 // MI355X; each leaves one share of dw.
 int norm_grad_blocks(int64_t rows, int64_t cols, bool bf16) {
-  const int64_t np = (cols + (bf16 ? 7 : 3)) / (bf16 ? 8 : 4), teams = np <= 128 ? 4 : 1;
-  const int64_t want = (rows + teams - 1) / teams;
+  const int64_t teams = norm_grad_one_wave(cols, bf16) ? 4 : 1, want = (rows + teams - 1) / teams;
   return static_cast<int>(want < kNormGradBlocks ? want : kNormGradBlocks);
 }
 
 hipError_t launch_norm_grad(NormGradArgs a, bool bf16, float* dweight, float* ws, hipStream_t s) {
   const int blocks = norm_grad_blocks(a.rows, a.cols, bf16);
   a.part = !dweight ? nullptr : blocks == 1 ? dweight : ws;
-  const hipError_t e = bf16 ? launch_norm_grad_for<true>(a, blocks, s) : launch_norm_grad_for<false>(a, blocks, s);
+  const bool wide = a.cols % (bf16 ? 8 : 4) == 0;
+  const hipError_t e = bf16 ? (wide ? launch_norm_grad_for<true, true>(a, blocks, s) : launch_norm_grad_for<true, false>(a, blocks, s))
+                            : (wide ? launch_norm_grad_for<false, true>(a, blocks, s) : launch_norm_grad_for<false, false>(a, blocks, s));
   if (e != hipSuccess || !dweight || blocks == 1) return e;
   weight_grad_kernel<<<dim3(static_cast<uint32_t>((a.cols + kWave - 1) / kWave)), dim3(kSumWaves * kWave), 0, s>>>(
       a.part, blocks, a.cols, dweight);

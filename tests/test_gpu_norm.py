@@ -266,3 +266,36 @@ def test_norm_other_stream_and_graph():
         q, sc, h = cq.add_rms_norm_q8(x, r, w)
         d, dw = cq.rms_norm_grad(dy, x, w, dsum=r)
         assert torch.equal(q, q1) and torch.equal(sc, s1) and torch.equal(h, h1) and torch.equal(d, d1) and torch.equal(dw, w1)
+
+
+@pytest.mark.parametrize("rows,cols,kind", [(8195, 512, "f32"), (8195, 507, "f32"), (8195, 1016, "bf16"), (2050, 1024, "bf16"),
+                                            (512, 8192, "bf16"), (515, 8192, "bf16"), (515, 4093, "f32")])
+def test_norm_teams(rows, cols, kind):
+    """Both sides of every choice of a row's team, by rows and by width."""
+    x, r, w = inputs(rows + cols, rows, cols, kind)
+    say(f"norm teams rows={rows} cols={cols} {kind}")
+    y, s = cq.add_rms_norm(x, r, w, out_dtype=torch.float32)
+    _, _, ref = reference(x, r, w, 1e-6)
+    assert np.all(np.abs(host64(y) - ref) <= TOL * np.abs(ref))
+    assert torch.equal(s, (x.float() + r.float()).to(TYPES[kind]))
+
+
+@pytest.mark.parametrize("rows,cols,kind", [(2047, 1024, "bf16"), (2048, 1024, "bf16"), (512, 8192, "bf16"), (513, 8192, "bf16"),
+                                            (2051, 512, "f32")])
+def test_norm_q8_teams(rows, cols, kind):
+    x, r, w = inputs(rows + cols, rows, cols, kind)
+    say(f"norm_q8 teams rows={rows} cols={cols} {kind}")
+    q, s, _ = cq.add_rms_norm_q8(x, r, w, 1e-6, group_size=128)
+    _, _, y = reference(x, r, w, 1e-6)
+    v = (y.reshape(rows, -1, 128) @ hadamard(128)).reshape(rows, cols) / np.sqrt(128)
+    mass = np.repeat(np.abs(y).reshape(rows, -1, 128).sum(2), 128, axis=1) / np.sqrt(128)
+    tol = (7 + 3) * EPS * mass + TOL * mass
+    s64 = host64(s)
+    assert np.all(np.abs(host64(q) * s64[:, None] - v) <= s64[:, None] * (0.5 + 127 * 4 * EPS) + tol)
+
+
+@pytest.mark.parametrize("rows,cols,kind", [(1024, 4096, "f32"), (1025, 4096, "f32"), (1025, 3604, "f32"), (1024, 4096, "bf16"),
+                                            (1025, 3608, "bf16"), (1025, 3601, "bf16"), (1025, 801, "bf16"), (90, 3601, "f32"),
+                                            (600, 6001, "bf16")])
+def test_norm_grad_teams(rows, cols, kind):
+    check_grad(rows, cols, kind, "f32", True, seed=5)
