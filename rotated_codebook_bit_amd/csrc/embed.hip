@@ -38,10 +38,13 @@ __device__ __forceinline__ int64_t token_at(const void* tokens, int bytes, int64
   return bytes == 8 ? static_cast<const int64_t*>(tokens)[i] : static_cast<const int32_t*>(tokens)[i];
 }
 
-// Lookups of 4 MiB and more leave with streaming stores: 8192 rows of 4096 to
-// bf16 from 4 bits 19.2 us instead of 21.6, to float32 from 2 bits 22.6 (25.4),
-// dense bf16 16.3 (17.2).  Smaller ones stay in the caches for what reads them.
-constexpr int64_t kStreamBytes = int64_t(4) << 20;
+// Lookups of 16 MiB and more leave with streaming stores (and from CQ storage
+// several units to a wave).  Rows of 4096, cached and streaming, us: from 2
+// bits to bf16 8 MiB 5.7 and 6.2, 16 MiB 9.0 and 8.4, 64 MiB 22.6 and 16.2; to
+// float32 8 MiB 5.3 and 5.4, 16 MiB 8.1 and 7.4, 64 MiB 20.8 and 13.2; bf16
+// rows 8 MiB 4.0 and 4.0, 16 MiB 5.8 and 4.9, 32 MiB 11.6 and 10.3.  Smaller
+// ones stay in the caches for what reads them.
+constexpr int64_t kStreamBytes = int64_t(16) << 20;
 
 // E consecutive output columns from column c of a row of dim columns; WIDE:
 // rows start on and hold whole 16-byte pieces.
@@ -780,8 +783,10 @@ hipError_t launch_embed_grad(const EmbedGradArgs& a, uint8_t* ws, hipStream_t s)
     partial = reinterpret_cast<float*>(at(2 * g.list));
     // Beside the sort's LDS two blocks fit a CU: that many, looping.
     const dim3 grid(1 + clear_blocks(a, kOneThreads, 2 * static_cast<int64_t>(device_cu_count()))), block(kOneThreads);
-    if (a.n > 4 * kOneThreads)
+    if (a.n > 8 * kOneThreads)
       sort_one_kernel<16><<<grid, block, 0, s>>>(a, passes, keys, order);
+    else if (a.n > 4 * kOneThreads)
+      sort_one_kernel<8><<<grid, block, 0, s>>>(a, passes, keys, order);
     else if (a.n > kOneThreads)
       sort_one_kernel<4><<<grid, block, 0, s>>>(a, passes, keys, order);
     else

@@ -248,3 +248,39 @@ def test_embed_other_stream_and_graph(levels32):
         torch.cuda.synchronize()
         assert torch.equal(buf, cq.embed_packed(tok, packed, norms, 64, 512, 4, levels32[4]))
         assert torch.equal(gbuf, cq.embed_grad(tok, d, 64))
+
+
+@pytest.mark.parametrize("n", [5000, 8192, 8193])
+def test_embed_grad_one_block_sorts(n):
+    grad_case(n, n, 300, 68, "f32", "f32", 64, False)
+
+
+@pytest.mark.parametrize("bits", [0, O.TERNARY, cq.TERNARY_TRITS, 2, 3, 4])
+@pytest.mark.parametrize("dim,dst", [(1000, "f32"), (1030, "f32"), (1032, "bf16"), (2051, "bf16")])
+def test_embed_large_lookups(bits, dim, dst, levels32):
+    """Lookups past 16 MiB (streaming stores, several units to a wave) equal
+    the dequantized or dense rows."""
+    say(f"embed large bits={bits} dim={dim} {dst}")
+    rng = np.random.default_rng(dim + bits)
+    n, vocab, group, scale = 8200, 60, 128, 2.5
+    t, tok = tokens_for(rng, n, vocab, 64)
+    w = torch.from_numpy((rng.standard_normal((vocab, dim)) * 0.02).astype(np.float32)).to(DEV)
+    inside = torch.from_numpy((t >= 0) & (t < vocab)).to(DEV)
+    at = torch.where(inside, tok, 0)
+    if bits == 0:
+        out = cq.embed(tok, w.to(TYPES[dst]), scale)
+        ref = (w.to(TYPES[dst]).float()[at] * np.float32(scale) * inside[:, None]).to(TYPES[dst])
+        assert torch.equal(out, ref)
+        return
+    lv = levels32[O.TERNARY if bits == cq.TERNARY_TRITS else bits]
+    packed, norms = cq.quantize(w, bits, lv, group_size=group)
+    rows = cq.dequantize(packed, norms, vocab, dim, bits, lv, group_size=group).double()
+    ref = rows[at] * scale * inside[:, None]
+    nm = norms.double().repeat_interleave(group, 1)[:, :dim][at] * inside[:, None]
+    tol = 2 * (np.log2(group) + 4) * EPS * scale * float(np.abs(lv).max()) * nm
+    out = cq.embed_packed(tok, packed, norms, vocab, dim, bits, lv, scale, out_dtype=TYPES[dst], group_size=group)
+    if dst == "bf16":
+        full = cq.embed_packed(tok, packed, norms, vocab, dim, bits, lv, scale, group_size=group)
+        assert torch.equal(out, full.to(torch.bfloat16))
+        out = full
+    assert bool(((out.double() - ref).abs() <= tol).all())
