@@ -618,31 +618,46 @@ void xor_tables(uint32_t (&table)[4]) {
 
 // How a call is cut up; the same for the workspace size and the launch.
 struct Plan {
-  int few;     // row tiles of 16 of the few-rows kernel, 0: the tiled kernel
-  int tm;      // row tiles of 32
+  bool few;    // the few-rows kernel
   int ksplit;  // ranges of k
   int per;     // tiles per range
 };
+// 64 rows: 2-bit 11008 x 4096 18.5 us here and 29.5 tiled, 4-bit 4096 x 11008
+// 17.4 and 28.6 (G = 128).  At G = 256 the registers hold 32 rows.
 constexpr int64_t kFewRows = 64;
+constexpr int kRowTiles = 4;  // row tiles of 32 of the tiled kernel
 constexpr int kCus = 256;
 
+// The ranges of k that an estimate finds fastest: rounds of one block per CU,
+// 1.6 us per tile and block (1.1 to 1.6 measured), two blocks on a CU at 1.7
+// times one; then 3 us and 8 bytes per partial sum at 4 TB/s to join them.  Measured (us, ranges
+// 1 / 2 / 4 / 8): 2-bit 11008 x 4096 at 128 rows 35.8 / 32.5 / 33.6 / 36.7, at
+// 256 37.8 / 46.1 / 47.8 / 67.6; 4-bit 4096 x 11008 at 128 rows 111.7 / 66.7 /
+// 42.0 / 30.9, at 256 114.1 / 70.1 / 46.7 / 45.3, at 512 118.8 / 76.6 / 72.4 / 82.6.
 Plan plan_for(int64_t n_out, int64_t k, int64_t batch, int group_size) {
   Plan p{};
   p.ksplit = 1;
   if (batch <= (group_size > 128 ? kFewRows / 2 : kFewRows)) {
-    p.few = static_cast<int>((batch + 15) / 16);
+    p.few = true;
     return p;
   }
-  p.tm = batch <= 64 ? 2 : 4;
   const int kt = group_size > 128 ? group_size : 128;
   const int64_t tiles = (k + kt - 1) / kt;
-  const int64_t blocks = (n_out + kGemmCols - 1) / kGemmCols * ((batch + 32 * p.tm - 1) / (32 * p.tm));
-  // Fewer blocks than two per CU: ranges of k, at least 8 tiles each.
-  int64_t split = blocks < 2 * kCus ? 2 * kCus / blocks : 1;
-  if (split > tiles / 8) split = tiles / 8;
-  if (split < 1) split = 1;
-  p.per = static_cast<int>((tiles + split - 1) / split);
-  p.ksplit = static_cast<int>((tiles + p.per - 1) / p.per);
+  const int64_t blocks = (n_out + kGemmCols - 1) / kGemmCols * ((batch + 32 * kRowTiles - 1) / (32 * kRowTiles));
+  p.per = static_cast<int>(tiles);
+  double best = 0.0;
+  // Ranges of 4 tiles or more, and no more than two blocks per CU.
+  for (int64_t want = 1; want == 1 || (want <= tiles / 4 && blocks * want <= 2 * kCus); ++want) {
+    const int64_t per = (tiles + want - 1) / want, split = (tiles + per - 1) / per;
+    const int64_t rounds = (blocks * split + kCus - 1) / kCus;
+    const double us = (0.85 * static_cast<double>(rounds / 2 * 2) + static_cast<double>(rounds % 2)) * 1.6 * static_cast<double>(per) +
+                      (split > 1 ? 3.0 + static_cast<double>(split) * static_cast<double>(batch * n_out) * 8.0 / 4e6 : 0.0);
+    if (want == 1 || us < best) {
+      best = us;
+      p.per = static_cast<int>(per);
+      p.ksplit = static_cast<int>(split);
+    }
+  }
   return p;
 }
 
@@ -664,9 +679,9 @@ hipError_t launch_for(const GemmQ8Args& a, const Q8Levels& lv, const Plan& p, fl
       return launch_few<SB, G, 4, 1>(a, lv, unit, s);
     }
   }
-  const int64_t tiles = (a.n_out + kGemmCols - 1) / kGemmCols * ((a.batch + 32 * p.tm - 1) / (32 * p.tm));
+  const int64_t tiles = (a.n_out + kGemmCols - 1) / kGemmCols * ((a.batch + 32 * kRowTiles - 1) / (32 * kRowTiles));
   float* part = p.ksplit > 1 ? ws : nullptr;
-  gemm_q8_kernel<SB, G, 4><<<dim3(static_cast<uint32_t>(tiles * p.ksplit)), dim3(kGemmBlock), 0, s>>>(
+  gemm_q8_kernel<SB, G, kRowTiles><<<dim3(static_cast<uint32_t>(tiles * p.ksplit)), dim3(kGemmBlock), 0, s>>>(
       a, lv, unit, part, p.ksplit, p.per);
   const hipError_t e = hipGetLastError();
   return e == hipSuccess && part ? launch_join(a, part, p.ksplit, unit, s) : e;
