@@ -20,7 +20,7 @@
 // most of the bytes at training sizes, are cleared by a plain fill that runs
 // beside the sort.
 // 16384 bf16 rows of 4096 into 32000 rows of float32 (0.66 GB): 95 us for the
-// fill with the sort (36 us alone) beside it, 55 for the sums, 9 to join long
+// fill with the sort (31 us alone) beside it, 55 for the sums, 9 to join long
 // runs, 4.1 TB/s over all; a block per table row that searched the sorted list
 // for its run, zeros included, took 250.  With cached instead of streaming
 // stores the fill takes 75 us and the sums, behind its write-backs, 76.
@@ -194,7 +194,11 @@ embed_packed_kernel(EmbedArgs a, LevelTable lv, uint32_t waves, uint32_t per_row
 // ---- Gradient: sorting the positions by token --------------------------------------------
 
 constexpr int kDigit = 256;       // 8-bit digits, least significant first
-constexpr int kSortOne = 16384;   // keys that one block sorts by itself
+// Keys that one block sorts by itself, the fill running beside all of it.  The
+// sort alone, in one block and in four launches: 1024 tokens 5.3 and 17.2 us,
+// 4096 10.8 and 20.9, 8192 17.7 and 22.9, 16384 31.3 and 24.4 with three gaps
+// between launches and the fill beside only the first.
+constexpr int kSortOne = 16384;
 
 // Sort key: the token, or vocab (past every row) where it is outside the table.
 __device__ __forceinline__ uint32_t token_key(const EmbedGradArgs& a, int64_t i) {

@@ -11,10 +11,9 @@
 // every sum within a group is an exact integer: two v_mfma_i32 per product,
 // the hi products' sum shifted up by 8 as the lo products' starting value
 // (|sum| <= 256 * 128 * 32768 = 2^30 at the largest group).  Only the step
-// between groups, one fma with the group's norm, rounds.  The two terms cost
-// two thirds of what split-bf16 activations and levels cost on the same
-// cores at half their rate each, and the activations are a quarter of the
-// bytes of float32.
+// between groups, one fma with the group's norm, rounds.  Two integer terms
+// take the matrix cores as long as one bf16 product of the same shape would,
+// and the activations are a quarter of the bytes of float32.
 #include <type_traits>
 
 #include "lanes.h"
@@ -127,10 +126,10 @@ __device__ __forceinline__ i32x4 ordered(i32x4 q) {
 // 29.8 us.  So a wave loads a unit's codes and activations in memory order
 // (whole lines), one unit ahead, passes them through its own piece of LDS
 // (rows an odd number of 16 bytes apart, so that 8 rows of one column fall on
-// different banks) and reads the operands there: 14.4 and 17.3 us.  What is
+// different banks) and reads the operands there: 14.4 and 18.5 us.  What is
 // left at one batch row is mostly the decoding, about a vector operation and
-// a half per 2-bit code (11008 x 4096: 6.8 us, 4096 x 4096: 4.1, 32000 x 4096:
-// 12.8).
+// a half per 2-bit code (11008 x 4096: 6.4 us, 1.9 TB/s of its bytes; 4096 x
+// 4096: 4.1, 32000 x 4096: 12.8).
 
 // What a wave stages per unit: 16 rows of codes, MT 16 / P rows of
 // activations and, for activation rows of the other group, a run of zeros.
@@ -373,7 +372,20 @@ few_kernel(GemmQ8Args a, Q8Levels lv, float unit) {
 // tiles.  The activations' next tile moves by direct-to-LDS loads into the
 // other buffer while this one is multiplied; 16-byte chunk c of row r lies at
 // slot c ^ chunk_key(r), so that the operand reads, 16 rows of one chunk at a
-// time, cover all 64 banks.
+// time, cover all 64 banks (no conflicts, by the counters).
+//
+// 4096 rows, 2-bit 11008 x 4096 (3.7e11 operations, twice that in the two
+// terms): 361 to 404 us by the clock the card grants, 1.8 to 2.0 POP/s of
+// integer operations; a large int8 library product reaches 2.07, the bare
+// instruction on random data 3.76.  It took 492 us with the sums scaled before
+// the next products instead of beside them, with conflicting chunk slots and
+// the blocks in plain order; the bands of output tiles (below) took the L2's
+// misses from 1.19e7 to 2.5e6.  What bounds it now are vector operations: a
+// wave issues about 320 per step (decoding its outputs' codes, then turning
+// each row tile's sums to float32 and scaling them) beside 32 products; they
+// keep the vector units busy 65% of the time and the matrix cores 50%.  192
+// and 256 rows per block spill registers (432 to 462 us), 256 columns per tile
+// took 455.
 constexpr int kGemmWaves = 4;
 constexpr int kGemmBlock = kGemmWaves * kWave;
 constexpr int kGemmCols = 32 * kGemmWaves;
