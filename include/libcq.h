@@ -472,7 +472,7 @@ int cq_q8_levels(int bits, const float* levels, int n_levels, cq_q8_table* table
  * y is batch x n_out, y_dtype CQ_F32 or CQ_BF16.  One batch row (a decode
  * step) to many.  The sums within a group are exact integers on the table's
  * 16-bit levels, the sum over groups float32.  k a multiple of G, at most
- * 2^22, n_out at most 2^27; trit storage is converted with cq_repack first.  table: host.
+ * 2^22, n_out below 2^27; trit storage is converted with cq_repack first.  table: host.
  * workspace: cq_dequant_gemm_q8_workspace bytes (0 for many calls: NULL). */
 int cq_dequant_gemm_q8_workspace(int64_t n_out, int64_t k, int64_t batch, int group_size, int64_t* bytes);
 int cq_dequant_gemm_q8(const uint8_t* packed, const uint16_t* norms, int64_t n_out, int64_t k, int bits,

@@ -622,6 +622,9 @@ hipError_t launch_gemm(const GemmDesc* table, const int64_t* bstart, int n, int6
 
 // ---- Norm (norm.hip) ------------------------------------------------------------
 
+// A launch counts its threads in 32 bits: more blocks than this take several.
+constexpr int64_t most_blocks(int threads) { return 0xFFFFFFFFll / threads; }
+
 constexpr int64_t kNormMaxCols = 32768;  // a row stays in the registers of at most 16 waves
 constexpr int kNormGradBlocks = 512;     // two per CU: shares of the weight gradient
 
@@ -693,6 +696,7 @@ struct EmbedGradArgs {
   int accumulate;
 };
 int64_t embed_grad_workspace(int64_t n, int64_t vocab, int64_t dim);
+int64_t embed_grad_blocks(int64_t n, int64_t dim);  // of the largest launch, 256 threads each
 hipError_t launch_embed_grad(const EmbedGradArgs& a, uint8_t* ws, hipStream_t stream);
 
 // ---- Product of 8-bit activations (gemm_q8.hip) ---------------------------------------

@@ -264,7 +264,7 @@ __device__ __forceinline__ uint32_t digit_scan(uint32_t v, uint32_t* part) {
 // Zeros over the gradient by block `block` of `blocks`, in contiguous pieces
 // of 64 bytes per thread.
 constexpr int kClearBytes = 64;
-constexpr int64_t kMaxClear = int64_t(1) << 30;
+constexpr int64_t kMaxClear = int64_t(1) << 23;  // blocks; more bytes than they hold take turns
 __device__ __forceinline__ void clear_grad(const EmbedGradArgs& a, int64_t block, int64_t blocks) {
   typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
   const int64_t bytes = a.vocab * a.dim * (a.grad_bf16 ? 2 : 4), whole = bytes / 16, each = blockDim.x * (kClearBytes / 16);
@@ -702,12 +702,29 @@ GradSpace grad_space(int64_t n, int64_t dim) {
   return g;
 }
 
+// launch(args, waves) for all of a lookup's tokens, per_row waves each.
+template <typename F>
+hipError_t launch_rows(EmbedArgs a, int64_t per_row, F launch) {
+  const int64_t most = most_blocks(kBlock) * kWaves / per_row;
+  const int64_t row = a.dim * (a.out_bf16 ? 2 : 4);
+  for (int64_t left = a.n; left > 0; left -= a.n) {
+    a.n = left < most ? left : most;
+    launch(a, static_cast<uint32_t>(a.n * per_row));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    a.tokens = static_cast<const uint8_t*>(a.tokens) + a.n * a.token_bytes;
+    a.out += a.n * row;
+  }
+  return hipSuccess;
+}
+
 template <int SB, bool OUT16, bool WIDE, int P>
-hipError_t launch_packed_units(const EmbedArgs& a, const LevelTable& lv, int64_t units, hipStream_t s) {
-  const int64_t per_row = (units + P - 1) / P, waves = a.n * per_row;
-  embed_packed_kernel<SB, OUT16, WIDE, P><<<dim3(blocks_of(waves)), dim3(kBlock), 0, s>>>(
-      a, lv, static_cast<uint32_t>(waves), static_cast<uint32_t>(per_row));
-  return hipGetLastError();
+hipError_t launch_packed_units(const EmbedArgs& all, const LevelTable& lv, int64_t units, hipStream_t s) {
+  const int64_t per_row = (units + P - 1) / P;
+  return launch_rows(all, per_row, [&](const EmbedArgs& a, uint32_t waves) {
+    embed_packed_kernel<SB, OUT16, WIDE, P><<<dim3(blocks_of(waves)), dim3(kBlock), 0, s>>>(
+        a, lv, waves, static_cast<uint32_t>(per_row));
+  });
 }
 
 template <int SB, bool OUT16, bool WIDE>
@@ -727,19 +744,20 @@ hipError_t launch_packed_for(const EmbedArgs& a, const LevelTable& lv, hipStream
 }
 
 template <bool IN16, bool OUT16>
-hipError_t launch_embed_at(const EmbedArgs& a, hipStream_t s) {
+hipError_t launch_embed_at(const EmbedArgs& all, hipStream_t s) {
   constexpr int E = IN16 || OUT16 ? 8 : 4;
-  const int64_t per_row = (a.dim + kWave * E - 1) / (kWave * E);
-  const uint32_t units = static_cast<uint32_t>(a.n * per_row);
-  const dim3 grid(blocks_of(units)), block(kBlock);
-  const bool wide = a.dim % E == 0, stream = a.n * a.dim * (OUT16 ? 2 : 4) >= kStreamBytes;
-  if (wide && stream)
-    embed_kernel<IN16, OUT16, true, true><<<grid, block, 0, s>>>(a, units, static_cast<uint32_t>(per_row));
-  else if (wide)
-    embed_kernel<IN16, OUT16, true, false><<<grid, block, 0, s>>>(a, units, static_cast<uint32_t>(per_row));
-  else
-    embed_kernel<IN16, OUT16, false, false><<<grid, block, 0, s>>>(a, units, static_cast<uint32_t>(per_row));
-  return hipGetLastError();
+  const int64_t per_row = (all.dim + kWave * E - 1) / (kWave * E);
+  const bool wide = all.dim % E == 0, stream = all.n * all.dim * (OUT16 ? 2 : 4) >= kStreamBytes;
+  return launch_rows(all, per_row, [&](const EmbedArgs& a, uint32_t units) {
+    const dim3 grid(blocks_of(units)), block(kBlock);
+    const uint32_t per = static_cast<uint32_t>(per_row);
+    if (wide && stream)
+      embed_kernel<IN16, OUT16, true, true><<<grid, block, 0, s>>>(a, units, per);
+    else if (wide)
+      embed_kernel<IN16, OUT16, true, false><<<grid, block, 0, s>>>(a, units, per);
+    else
+      embed_kernel<IN16, OUT16, false, false><<<grid, block, 0, s>>>(a, units, per);
+  });
 }
 
 template <bool WIDE, int PIECE>
@@ -775,6 +793,8 @@ int64_t embed_grad_workspace(int64_t n, int64_t vocab, int64_t dim) {
   (void)vocab;
   return grad_space(n, dim).total;
 }
+
+int64_t embed_grad_blocks(int64_t n, int64_t dim) { return pieces_of(n) * ((dim + kSlice - 1) / kSlice); }
 
 hipError_t launch_embed_grad(const EmbedGradArgs& a, uint8_t* ws, hipStream_t s) {
   const GradSpace g = grad_space(a.n, a.dim);

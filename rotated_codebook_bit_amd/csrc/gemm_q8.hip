@@ -589,23 +589,24 @@ gemm_q8_kernel(GemmQ8Args a, Q8Levels lv, float unit, float* part, int ksplit, i
 __global__ void __launch_bounds__(256)
 gemm_q8_join_kernel(GemmQ8Args a, const float* __restrict__ part, int ksplit, float unit) {
   const int64_t total = a.batch * a.n_out;
-  const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (e >= total) return;
-  float v = 0.0f;
-  if (ksplit) {
-    v = part[e];
-    for (int s = 1; s < ksplit; ++s) v += part[s * total + e];
-    v *= unit * a.scale[e / a.n_out];
+  for (int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; e < total; e += static_cast<int64_t>(gridDim.x) * 256) {
+    float v = 0.0f;
+    if (ksplit) {
+      v = part[e];
+      for (int s = 1; s < ksplit; ++s) v += part[s * total + e];
+      v *= unit * a.scale[e / a.n_out];
+    }
+    if (a.y_bf16)
+      store_elem<true>(a.y, e, v);
+    else
+      store_elem<false>(a.y, e, v);
   }
-  if (a.y_bf16)
-    store_elem<true>(a.y, e, v);
-  else
-    store_elem<false>(a.y, e, v);
 }
 
 hipError_t launch_join(const GemmQ8Args& a, const float* part, int ksplit, float unit, hipStream_t s) {
-  gemm_q8_join_kernel<<<dim3(static_cast<uint32_t>((a.batch * a.n_out + 255) / 256)), dim3(256), 0, s>>>(a, part, ksplit,
-                                                                                                         unit);
+  const int64_t blocks = (a.batch * a.n_out + 255) / 256;
+  gemm_q8_join_kernel<<<dim3(static_cast<uint32_t>(blocks < most_blocks(256) ? blocks : most_blocks(256))), dim3(256), 0, s>>>(
+      a, part, ksplit, unit);
   return hipGetLastError();
 }
 

@@ -1127,6 +1127,8 @@ int cq_embed_grad(const void* tokens, int token_bytes, int64_t n, const void* do
   if (vocab == 0 || dim == 0 || (n == 0 && accumulate)) return CQ_OK;
   if (!grad || (n && !dout)) return fail(CQ_ERR_NULL, "dout/grad is NULL");
   if (!aligned(grad, 16) || !aligned(dout, 16)) return fail(CQ_ERR_ALIGN, "dout and grad need 16-byte alignment");
+  if (cq::embed_grad_blocks(n, dim) > cq::most_blocks(256))
+    return fail(CQ_ERR_UNSUPPORTED, "n * dim is past this call's grid");
   const int64_t need = cq::embed_grad_workspace(n, vocab, dim);
   if (int rc = check_workspace(workspace, workspace_bytes, need)) return rc;
   const int64_t gbytes = vocab * dim * dtype_bytes(grad_dtype), dbytes = n * dim * dtype_bytes(dout_dtype);
@@ -1304,7 +1306,7 @@ static int check_q8_sizes(int64_t n_out, int64_t k, int64_t batch, int group_siz
   if (batch < 1) return fail(CQ_ERR_ARG, "batch must be >= 1");
   if (k % group_size) return fail(CQ_ERR_UNSUPPORTED, "k=%lld is not a multiple of %d", (long long)k, group_size);
   if (k > cq::kQ8MaxK) return fail(CQ_ERR_UNSUPPORTED, "k=%lld: this product takes k <= 2^22", (long long)k);
-  if (n_out > (int64_t(1) << 27) || batch > kMaxIndex || !fits(n_out, std::max(k, batch), 4) || !fits(batch, k, 4) ||
+  if (n_out >= (int64_t(1) << 27) || batch > kMaxIndex || !fits(n_out, std::max(k, batch), 4) || !fits(batch, k, 4) ||
       ceil_div(n_out, 128) > kMaxIndex / ceil_div(batch, 128) / 8 || ceil_div(batch, 8) > kMaxIndex * 16 / std::max<int64_t>(n_out, 1))
     return fail(CQ_ERR_UNSUPPORTED, "batch * n_out is past this call's grid");
   return CQ_OK;

@@ -559,17 +559,32 @@ weight_grad_kernel(const float* __restrict__ part, int blocks, int64_t cols, flo
 }
 
 template <bool BF16, int NT, int C>
-hipError_t launch_norm_at(const NormArgs& a, hipStream_t s) {
-  constexpr int teams = NT < 256 ? 256 / NT : 1;
-  const dim3 grid(static_cast<uint32_t>((a.rows + teams - 1) / teams)), block(NT < 256 ? 256 : NT);
+hipError_t launch_norm_at(NormArgs a, hipStream_t s) {
+  constexpr int teams = NT < 256 ? 256 / NT : 1, threads = NT * teams;
   const bool wide = a.cols % Piece<BF16>::kElems == 0;
-  if (a.q)
-    norm_kernel<BF16, NT, C, true, true><<<grid, block, 0, s>>>(a);
-  else if (wide)
-    norm_kernel<BF16, NT, C, true, false><<<grid, block, 0, s>>>(a);
-  else
-    norm_kernel<BF16, NT, C, false, false><<<grid, block, 0, s>>>(a);
-  return hipGetLastError();
+  for (int64_t left = a.rows; left > 0; left -= a.rows) {
+    a.rows = left < most_blocks(threads) * teams ? left : most_blocks(threads) * teams;
+    const dim3 grid(static_cast<uint32_t>((a.rows + teams - 1) / teams)), block(threads);
+    if (a.q)
+      norm_kernel<BF16, NT, C, true, true><<<grid, block, 0, s>>>(a);
+    else if (wide)
+      norm_kernel<BF16, NT, C, true, false><<<grid, block, 0, s>>>(a);
+    else
+      norm_kernel<BF16, NT, C, false, false><<<grid, block, 0, s>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int64_t done = a.rows * a.cols, bytes = done * Piece<BF16>::kBytes;
+    a.x += bytes;
+    if (a.residual) a.residual += bytes;
+    if (a.sum) a.sum += bytes;
+    if (a.q) {
+      a.q += done;
+      a.scale += a.rows;
+    } else {
+      a.out += done * (a.out_bf16 ? 2 : 4);
+    }
+  }
+  return hipSuccess;
 }
 
 template <bool BF16, bool WIDE, int NT, int C>
