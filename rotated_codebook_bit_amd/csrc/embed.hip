@@ -18,7 +18,8 @@
 // order that changes between runs.  Runs longer than a piece leave one sum
 // per piece, which are added in order afterwards.  The rows of absent tokens,
 // most of the bytes at training sizes, are cleared by a plain fill that runs
-// beside the sort.
+// beside the sort.  Short lists are not sorted: one launch compares every
+// position with all others (below).
 // 16384 bf16 rows of 4096 into 32000 rows of float32 (0.66 GB): 95 us for the
 // fill with the sort (31 us alone) beside it, 55 for the sums, 9 to join long
 // runs, 4.1 TB/s over all; a block per table row that searched the sorted list
@@ -677,6 +678,137 @@ embed_grad_join_kernel(EmbedGradArgs a, const uint32_t* __restrict__ keys, const
   put_row<WIDE>(a, key, s, lane, acc);
 }
 
+// ---- Gradient of short lists, in one launch ---------------------------------------------
+
+// No sort: block (i, slice) looks at all tokens, stops unless position i is
+// the first of its token, and adds that token's rows, each wave those among its
+// quarter of the positions, eight in flight; the quarters are added in order.
+// The launch's other blocks clear the rows whose tokens are absent, kScanRows
+// (fewer for long rows) each, found the same way.
+//
+// It is bound by latency (tokens, rows, the store) and, past some thousand
+// blocks, by the n * n comparisons per slice: up to 2^23 of them in all it is
+// faster than the sort with its three launches.  Scan and sort, us, float32
+// rows into 8192 rows: 8 of 96 4.8 and 9.6, 256 of 1000 8.1 and 19.3, 777 of
+// 1000 11.2 and 20.3, 2048 of 500 (2^23) 12.9 and 23.6, 1024 of 2048 (2^23)
+// 22.9 and 25.2, 1024 of 4096 (2^24) 42.5 and 37.0, 2048 of 2048 (2^25) 41.7
+// and 26.5.
+constexpr int64_t kScanCompares = int64_t(1) << 23;
+constexpr int64_t kScanMost = 2896;  // tokens: the square root of that
+constexpr int kScanList = (kScanMost + kBlock - 1) / kBlock * kWave;
+constexpr int kScanRows = 64;
+constexpr int64_t kScanBytes = 64 << 10;  // of table rows per clearing block
+
+// A constant in a register of its own, so that hold_value() holds that one.
+__device__ __forceinline__ uint32_t in_register(uint32_t v) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("" : "+v"(v));
+#endif
+  return v;
+}
+
+template <bool BF16, bool WIDE>
+__global__ void __launch_bounds__(kBlock)
+embed_grad_scan_kernel(EmbedGradArgs a, uint32_t sum_blocks, uint32_t slices, uint32_t rows) {
+  __shared__ uint32_t found[kWaves][kScanList];
+  __shared__ uint32_t count[kWaves], early[kWaves];
+  __shared__ float sums[kWaves][kSlice];
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const uint32_t n = static_cast<uint32_t>(a.n);
+  if (blockIdx.x >= sum_blocks) {  // the same for the block
+    uint32_t* const present = found[0];
+    const uint32_t zero = in_register(0), one = in_register(1);
+    if (threadIdx.x < kScanRows) present[threadIdx.x] = zero;
+    wait_lds_writes();
+    hold_value(zero);
+    __syncthreads();
+    const int64_t first = static_cast<int64_t>(blockIdx.x - sum_blocks) * rows;
+    const uint32_t here = static_cast<uint32_t>(a.vocab - first < rows ? a.vocab - first : rows);
+    for (uint32_t p = threadIdx.x; p < n; p += kBlock) {
+      const int64_t at = token_at(a.tokens, a.token_bytes, p) - first;
+      if (at >= 0 && at < here) present[at] = one;
+      wait_lds_writes();
+      hold_value(one);
+    }
+    __syncthreads();
+    const float none[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (uint32_t r = wave; r < here; r += kWaves) {
+      if (__builtin_amdgcn_readfirstlane(present[r])) continue;
+      uint8_t* const row = a.grad + (first + r) * a.dim * (a.grad_bf16 ? 2 : 4);
+      for (uint32_t s = 0; s < slices; ++s) store_four<WIDE>(row, a.grad_bf16, s, lane, a.dim, none);
+    }
+    return;
+  }
+  const uint32_t i = blockIdx.x / slices, s = blockIdx.x - i * slices;
+  const int64_t tok = token_at(a.tokens, a.token_bytes, i);
+  if (tok < 0 || tok >= a.vocab) return;
+  const uint32_t quarter = (n + kBlock - 1) / kBlock * kWave, begin = wave * quarter;
+  uint32_t mine = 0, before = 0;
+  for (uint32_t p0 = begin; p0 < begin + quarter && p0 < n; p0 += kWave) {
+    const uint32_t p = p0 + lane;
+    const bool hit = p < n && token_at(a.tokens, a.token_bytes, p < n ? p : i) == tok;
+    const uint64_t hits = __ballot(hit);
+    if (hit) found[wave][mine + __popcll(hits & ((uint64_t(1) << lane) - 1))] = p;
+    wait_lds_writes();
+    hold_value(p);
+    if (p0 < i) before |= static_cast<uint32_t>(i - p0 >= kWave ? hits != 0 : (hits & ((uint64_t(1) << (i - p0)) - 1)) != 0);
+    mine += __popcll(hits);
+  }
+  if (lane == 0) {
+    count[wave] = mine;
+    early[wave] = before;
+  }
+  wait_lds_writes();
+  hold_values(mine, before);
+  __syncthreads();
+  uint32_t total = 0, any = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    total += count[w];
+    any |= early[w];
+  }
+  if (__builtin_amdgcn_readfirstlane(any)) return;  // an earlier position's block serves this token
+  const bool alone = __builtin_amdgcn_readfirstlane(total) == 1;
+  if (alone && mine == 0) return;
+  const int64_t bytes = a.dim * Piece<BF16>::kBytes;
+  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  constexpr int kAhead = 8;
+  for (uint32_t l0 = 0; l0 < mine; l0 += kAhead) {
+    float v[kAhead][4];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const uint32_t row = __builtin_amdgcn_readfirstlane(found[wave][l0 + k < mine ? l0 + k : mine - 1]);
+      load_four<BF16, WIDE>(a.dout + row * bytes, s, lane, a.dim, v[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {  // all loads are issued before the first sum
+      const bool in = l0 + k < mine;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float t = acc[e] + v[k][e];
+        acc[e] = in ? t : acc[e];
+      }
+    }
+  }
+  if (alone) {
+    put_row<WIDE>(a, tok, s, lane, acc);
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) sums[wave][k * kWave + lane] = acc[k];
+  wait_lds_writes();
+#pragma unroll
+  for (int k = 0; k < 4; ++k) hold_value(acc[k]);
+  __syncthreads();
+  if (wave != 0) return;
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k] += sums[w][k * kWave + lane];
+  put_row<WIDE>(a, tok, s, lane, acc);
+}
+
 uint32_t blocks_of(int64_t waves) { return static_cast<uint32_t>((waves + kWaves - 1) / kWaves); }
 
 int64_t align256(int64_t b) { return (b + 255) & ~int64_t(255); }
@@ -687,7 +819,11 @@ int64_t align256(int64_t b) { return (b + 255) & ~int64_t(255); }
 int piece_of(int64_t n) { return n <= 8192 ? 16 : n <= 65536 ? 32 : 64; }
 int64_t pieces_of(int64_t n) { return (n + piece_of(n) - 1) / piece_of(n); }
 
-// Workspace: sorted keys and positions (twice in the many-block sort), the
+bool scans(int64_t n, int64_t dim) {
+  return n > 0 && n <= kScanMost && (dim + kSlice - 1) / kSlice <= kScanCompares / (n * n);
+}
+
+// Workspace of the sort: sorted keys and positions (twice in the many-block sort), the
 // tiles' digit counts, the pieces' sums.
 struct GradSpace {
   int64_t list, counts, partial, total;
@@ -760,6 +896,20 @@ hipError_t launch_embed_at(const EmbedArgs& all, hipStream_t s) {
   });
 }
 
+template <bool BF16>
+hipError_t launch_grad_scan(const EmbedGradArgs& a, hipStream_t s) {
+  const int64_t slices = (a.dim + kSlice - 1) / kSlice, sums = a.n * slices;
+  const int64_t fit = kScanBytes / (a.dim * (a.grad_bf16 ? 2 : 4)), rows = fit < 1 ? 1 : fit < kScanRows ? fit : kScanRows;
+  const int64_t clear = a.accumulate ? 0 : (a.vocab + rows - 1) / rows;
+  const dim3 grid(static_cast<uint32_t>(sums + clear)), block(kBlock);
+  const uint32_t n_sums = static_cast<uint32_t>(sums), n_slices = static_cast<uint32_t>(slices);
+  if (a.dim % 4 == 0)
+    embed_grad_scan_kernel<BF16, true><<<grid, block, 0, s>>>(a, n_sums, n_slices, static_cast<uint32_t>(rows));
+  else
+    embed_grad_scan_kernel<BF16, false><<<grid, block, 0, s>>>(a, n_sums, n_slices, static_cast<uint32_t>(rows));
+  return hipGetLastError();
+}
+
 template <bool WIDE, int PIECE>
 hipError_t launch_grad_sums(const EmbedGradArgs& a, const uint32_t* keys, const uint32_t* order, float* partial,
                             hipStream_t s) {
@@ -791,12 +941,13 @@ hipError_t launch_embed_packed(const EmbedArgs& a, int storage, const LevelTable
 
 int64_t embed_grad_workspace(int64_t n, int64_t vocab, int64_t dim) {
   (void)vocab;
-  return grad_space(n, dim).total;
+  return grad_space(n, dim).total;  // also of a list that is scanned: one contract for all lengths
 }
 
 int64_t embed_grad_blocks(int64_t n, int64_t dim) { return pieces_of(n) * ((dim + kSlice - 1) / kSlice); }
 
 hipError_t launch_embed_grad(const EmbedGradArgs& a, uint8_t* ws, hipStream_t s) {
+  if (scans(a.n, a.dim)) return a.dout_bf16 ? launch_grad_scan<true>(a, s) : launch_grad_scan<false>(a, s);
   const GradSpace g = grad_space(a.n, a.dim);
   auto at = [&](int64_t off) { return reinterpret_cast<uint32_t*>(ws + off); };
   uint32_t *keys = at(0), *order = at(g.list);

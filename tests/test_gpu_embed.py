@@ -284,3 +284,23 @@ def test_embed_large_lookups(bits, dim, dst, levels32):
         assert torch.equal(out, full.to(torch.bfloat16))
         out = full
     assert bool(((out.double() - ref).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("n,dim", [(2896, 256), (2897, 256), (2048, 512), (2049, 512), (1000, 4096), (724, 4096), (725, 4096),
+                                   (90, 4099), (8, 33000), (3000, 33)])
+@pytest.mark.parametrize("kind,out,accumulate", [("f32", "f32", False), ("bf16", "bf16", True)])
+def test_embed_grad_scan_or_sort(n, dim, kind, out, accumulate):
+    """Both sides of the choice between comparing all tokens and sorting them,
+    tokens of one run to many (and a vocabulary past a clearing block's rows)."""
+    def skewed(rng):
+        t = np.minimum(rng.geometric(0.02, n) - 1, 129)
+        t[0], t[n // 2] = -1, 131
+        return t
+
+    grad_case(n + dim, n, 131, dim, kind, out, 64, accumulate, tokens=skewed)
+
+
+@pytest.mark.parametrize("n", [2900, 4097, 9000])
+@pytest.mark.parametrize("distinct", [1, 2, 40])
+def test_embed_grad_long_runs_sorted(n, distinct):
+    grad_case(n, n, 50, 36, "f32", "f32", 32, False, tokens=lambda rng: rng.integers(0, distinct, n))
