@@ -195,11 +195,17 @@ embed_packed_kernel(EmbedArgs a, LevelTable lv, uint32_t waves, uint32_t per_row
 // ---- Gradient: sorting the positions by token --------------------------------------------
 
 constexpr int kDigit = 256;       // 8-bit digits, least significant first
-// Keys that one block sorts by itself, the fill running beside all of it.  The
-// sort alone, in one block and in four launches: 1024 tokens 5.3 and 17.2 us,
-// 4096 10.8 and 20.9, 8192 17.7 and 22.9, 16384 31.3 and 24.4 with three gaps
-// between launches and the fill beside only the first.
-constexpr int kSortOne = 16384;
+// Tokens and vocabulary that one launch sorts, the fill running beside it.
+constexpr int64_t kSortOne = 16384, kSortVocab = int64_t(1) << 20;
+bool one_launch_sorts(int64_t n, int64_t vocab) { return n <= kSortOne && vocab <= kSortVocab; }
+
+// A constant in a register of its own, so that hold_value() holds that one.
+__device__ __forceinline__ uint32_t in_register(uint32_t v) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("" : "+v"(v));
+#endif
+  return v;
+}
 
 // Sort key: the token, or vocab (past every row) where it is outside the table.
 __device__ __forceinline__ uint32_t token_key(const EmbedGradArgs& a, int64_t i) {
@@ -287,80 +293,105 @@ uint32_t clear_blocks(const EmbedGradArgs& a, int threads, int64_t most) {
   return static_cast<uint32_t>(want < most ? want : most);
 }
 
-// The whole sort in one block of 16 waves: wave w holds the keys
-// 64 IPT w .. of the current order, IPT per lane.  Positions past n carry the
-// largest key and stay last.  The launch's other blocks clear the gradient.
+// The whole sort in one launch: block b takes the keys 256 b .. 256 b + 255
+// out of all n, which tells it where they go (the smaller keys' number) and
+// their order of position, and sorts them by their last digit: counts per wave,
+// then ranks.  The launch's other blocks clear the gradient.  IPT: tokens per
+// lane, a wave's 64 IPT consecutive.
 constexpr int kOneThreads = 1024, kOneWaves = kOneThreads / kWave;
 template <int IPT>
 __global__ void __launch_bounds__(kOneThreads)
-sort_one_kernel(EmbedGradArgs a, int passes, uint32_t* __restrict__ keys, uint32_t* __restrict__ order) {
+sort_ranges_kernel(EmbedGradArgs a, uint32_t ranges, uint32_t* __restrict__ keys, uint32_t* __restrict__ order) {
   __shared__ uint32_t hist[kOneWaves][kDigit];
   __shared__ uint32_t part[kDigit / kWave];
-  __shared__ uint32_t moved[kOneThreads * IPT];  // the keys, then the positions, on their way
-  if (blockIdx.x > 0) return clear_grad(a, blockIdx.x - 1, gridDim.x - 1);
-  const int t = threadIdx.x, lane = t & (kWave - 1), wave = t / kWave;
-  const int first = wave * kWave * IPT + lane;
-  const int n = static_cast<int>(a.n);
-  uint32_t key[IPT], pos[IPT], rank[IPT];
+  __shared__ uint32_t smaller[kOneWaves], inside[kOneWaves];
+  __shared__ uint32_t list[kOneThreads * IPT];  // digit and position of the range's keys, by position
+  if (blockIdx.x >= ranges) return clear_grad(a, blockIdx.x - ranges, gridDim.x - ranges);
+  const int t = threadIdx.x, lane = t & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(t / kWave);
+  const uint32_t n = static_cast<uint32_t>(a.n), lo = blockIdx.x * kDigit;
+  const uint32_t first = wave * kWave * IPT + lane;
+  uint32_t key[IPT];
 #pragma unroll
   for (int i = 0; i < IPT; ++i) {
-    const int p = first + i * kWave;
-    pos[i] = p;
+    const uint32_t p = first + i * kWave;
     key[i] = p < n ? token_key(a, p) : 0xFFFFFFFFu;
   }
-  const uint32_t zero = 0;
-  for (int pass = 0; pass < passes; ++pass) {
-    for (int i = t; i < kOneWaves * kDigit; i += kOneThreads) hist[i / kDigit][i % kDigit] = zero;
-    wait_lds_writes();
-    hold_value(zero);
-    __syncthreads();
-    rank_keys<IPT>(key, 8 * pass, hist[wave], rank);
-    __syncthreads();
-    uint32_t total = 0;
-    if (t < kDigit) {
-#pragma unroll
-      for (int w = 0; w < kOneWaves; ++w) total += hist[w][t];
-    }
-    uint32_t run = digit_scan(total, part);
-    if (t < kDigit) {
-#pragma unroll 1
-      for (int w = 0; w < kOneWaves; w += 4) {  // four at a time: registers
-        uint32_t at[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          at[i] = run;
-          run += hist[w + i][t];
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) hist[w + i][t] = at[i];
-        wait_lds_writes();
-        hold_values(at[0], at[1], at[2], at[3]);
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < IPT; ++i) rank[i] += hist[wave][(key[i] >> (8 * pass)) & (kDigit - 1)];
-    auto move = [&](uint32_t (&v)[IPT]) __attribute__((always_inline)) {
-#pragma unroll
-      for (int i = 0; i < IPT; ++i) moved[rank[i]] = v[i];
-      wait_lds_writes();
-#pragma unroll
-      for (int i = 0; i < IPT; ++i) hold_value(v[i]);
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < IPT; ++i) v[i] = moved[first + i * kWave];
-      __syncthreads();
-    };
-    move(key);
-    move(pos);
-  }
+  uint32_t under = 0, mine = 0;
 #pragma unroll
   for (int i = 0; i < IPT; ++i) {
-    const int p = first + i * kWave;
-    if (p < n) {
-      keys[p] = key[i];
-      order[p] = pos[i];
+    under += __popcll(__ballot(key[i] < lo));
+    mine += __popcll(__ballot(key[i] - lo < kDigit));
+  }
+  const uint32_t zero = in_register(0);
+  for (int i = t; i < kOneWaves * kDigit; i += kOneThreads) hist[i / kDigit][i % kDigit] = zero;
+  const uint32_t u = in_register(under), v = in_register(mine);
+  if (lane == 0) {
+    smaller[wave] = u;
+    inside[wave] = v;
+  }
+  wait_lds_writes();
+  hold_values(zero, u, v);
+  __syncthreads();
+  uint32_t base = 0, at = 0, count = 0;
+  for (int w = 0; w < kOneWaves; ++w) {
+    base += smaller[w];
+    at += w < wave ? inside[w] : 0;
+    count += inside[w];
+  }
+  if (count == 0) return;  // the same for the block
+#pragma unroll
+  for (int i = 0; i < IPT; ++i) {
+    const bool in = key[i] - lo < kDigit;
+    const uint64_t m = __ballot(in);
+    const uint32_t item = (key[i] - lo) << 16 | (first + i * kWave);
+    if (in) list[at + __popcll(m & ((1ull << lane) - 1ull))] = item;
+    wait_lds_writes();
+    hold_value(item);
+    at += __popcll(m);
+  }
+  __syncthreads();
+  // A wave ranks consecutive items.
+  const uint32_t share = (count + kOneThreads - 1) / kOneThreads * kWave, begin = wave * share;
+  volatile uint32_t* const mine_of = hist[wave];  // volatile: other lanes change it between steps
+  for (uint32_t p0 = begin; p0 < begin + share && p0 < count; p0 += kWave) {
+    const bool in = p0 + lane < count;
+    const uint32_t d = list[in ? p0 + lane : p0] >> 16;
+    const uint64_t m = same_digit(d) & __ballot(in);
+    const uint32_t next = mine_of[d] + static_cast<uint32_t>(__popcll(m));
+    if (in && (m & ((1ull << lane) - 1ull)) == 0) mine_of[d] = next;
+    wait_lds_writes();
+    hold_value(next);
+  }
+  __syncthreads();
+  uint32_t total = 0;
+  if (t < kDigit) {
+    for (int w = 0; w < kOneWaves; ++w) total += hist[w][t];
+  }
+  uint32_t run = base + digit_scan(total, part);
+  if (t < kDigit) {
+    for (int w = 0; w < kOneWaves; ++w) {
+      const uint32_t here = run;
+      run += hist[w][t];
+      hist[w][t] = here;
+      wait_lds_writes();
+      hold_value(here);
     }
+  }
+  __syncthreads();
+  for (uint32_t p0 = begin; p0 < begin + share && p0 < count; p0 += kWave) {
+    const bool in = p0 + lane < count;
+    const uint32_t item = list[in ? p0 + lane : p0], d = item >> 16;
+    const uint64_t m = same_digit(d) & __ballot(in);
+    const uint32_t below = __popcll(m & ((1ull << lane) - 1ull));
+    const uint32_t from = mine_of[d], next = from + static_cast<uint32_t>(__popcll(m));
+    if (in) {
+      if (below == 0) mine_of[d] = next;
+      keys[from + below] = lo + d;
+      order[from + below] = item & 0xFFFFu;
+    }
+    wait_lds_writes();
+    hold_value(next);
   }
 }
 
@@ -699,14 +730,6 @@ constexpr int kScanList = (kScanMost + kBlock - 1) / kBlock * kWave;
 constexpr int kScanRows = 64;
 constexpr int64_t kScanBytes = 64 << 10;  // of table rows per clearing block
 
-// A constant in a register of its own, so that hold_value() holds that one.
-__device__ __forceinline__ uint32_t in_register(uint32_t v) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  asm volatile("" : "+v"(v));
-#endif
-  return v;
-}
-
 template <bool BF16, bool WIDE>
 __global__ void __launch_bounds__(kBlock)
 embed_grad_scan_kernel(EmbedGradArgs a, uint32_t sum_blocks, uint32_t slices, uint32_t rows) {
@@ -828,10 +851,10 @@ bool scans(int64_t n, int64_t dim) {
 struct GradSpace {
   int64_t list, counts, partial, total;
 };
-GradSpace grad_space(int64_t n, int64_t dim) {
+GradSpace grad_space(int64_t n, int64_t vocab, int64_t dim) {
   GradSpace g;
   g.list = align256(4 * n);
-  const bool many = n > kSortOne;
+  const bool many = !one_launch_sorts(n, vocab);
   g.counts = many ? align256((n + kSortTile - 1) / kSortTile * kDigit * 4) : 0;
   g.partial = n > piece_of(n) ? align256(2 * pieces_of(n) * dim * 4) : 0;
   g.total = g.list * (many ? 4 : 2) + g.counts + g.partial;
@@ -940,37 +963,35 @@ hipError_t launch_embed_packed(const EmbedArgs& a, int storage, const LevelTable
 }
 
 int64_t embed_grad_workspace(int64_t n, int64_t vocab, int64_t dim) {
-  (void)vocab;
-  return grad_space(n, dim).total;  // also of a list that is scanned: one contract for all lengths
+  return grad_space(n, vocab, dim).total;  // also of a list that is scanned: one contract for all lengths
 }
 
 int64_t embed_grad_blocks(int64_t n, int64_t dim) { return pieces_of(n) * ((dim + kSlice - 1) / kSlice); }
 
 hipError_t launch_embed_grad(const EmbedGradArgs& a, uint8_t* ws, hipStream_t s) {
   if (scans(a.n, a.dim)) return a.dout_bf16 ? launch_grad_scan<true>(a, s) : launch_grad_scan<false>(a, s);
-  const GradSpace g = grad_space(a.n, a.dim);
+  const GradSpace g = grad_space(a.n, a.vocab, a.dim);
   auto at = [&](int64_t off) { return reinterpret_cast<uint32_t*>(ws + off); };
   uint32_t *keys = at(0), *order = at(g.list);
   float* partial;
-  int passes = 1;  // keys run from 0 to vocab
-  while (passes < 4 && (a.vocab >> (8 * passes))) ++passes;
-  if (a.n <= kSortOne) {
+  if (one_launch_sorts(a.n, a.vocab)) {
     partial = reinterpret_cast<float*>(at(2 * g.list));
-    // Beside the sort's LDS two blocks fit a CU: that many, looping.
-    const dim3 grid(1 + clear_blocks(a, kOneThreads, 2 * static_cast<int64_t>(device_cu_count()))), block(kOneThreads);
+    // Beside the sort's LDS two blocks fit a CU: that many clear, looping.
+    const uint32_t ranges = static_cast<uint32_t>(a.vocab / kDigit + 1);
+    const dim3 grid(ranges + clear_blocks(a, kOneThreads, 2 * static_cast<int64_t>(device_cu_count()))), block(kOneThreads);
     if (a.n > 8 * kOneThreads)
-      sort_one_kernel<16><<<grid, block, 0, s>>>(a, passes, keys, order);
+      sort_ranges_kernel<16><<<grid, block, 0, s>>>(a, ranges, keys, order);
     else if (a.n > 4 * kOneThreads)
-      sort_one_kernel<8><<<grid, block, 0, s>>>(a, passes, keys, order);
-    else if (a.n > kOneThreads)
-      sort_one_kernel<4><<<grid, block, 0, s>>>(a, passes, keys, order);
+      sort_ranges_kernel<8><<<grid, block, 0, s>>>(a, ranges, keys, order);
     else
-      sort_one_kernel<1><<<grid, block, 0, s>>>(a, passes, keys, order);
+      sort_ranges_kernel<4><<<grid, block, 0, s>>>(a, ranges, keys, order);
   } else {
     uint32_t *keys2 = at(2 * g.list), *order2 = at(3 * g.list), *counts = at(4 * g.list);
     partial = reinterpret_cast<float*>(at(4 * g.list + g.counts));
     const uint32_t tiles = static_cast<uint32_t>((a.n + kSortTile - 1) / kSortTile);
     const dim3 grid(tiles), block(kBlock);
+    int passes = 1;  // keys run from 0 to vocab
+    while (passes < 4 && (a.vocab >> (8 * passes))) ++passes;
     const uint32_t *in_keys = nullptr, *in_order = nullptr;  // the first pass reads the tokens
     for (int p = 0; p < passes; ++p) {
       count_kernel<<<dim3(tiles + (p == 0 ? clear_blocks(a, kBlock, kMaxClear) : 0)), block, 0, s>>>(a, 8 * p, in_keys, counts, tiles);

@@ -304,3 +304,10 @@ def test_embed_grad_scan_or_sort(n, dim, kind, out, accumulate):
 @pytest.mark.parametrize("distinct", [1, 2, 40])
 def test_embed_grad_long_runs_sorted(n, distinct):
     grad_case(n, n, 50, 36, "f32", "f32", 32, False, tokens=lambda rng: rng.integers(0, distinct, n))
+
+
+@pytest.mark.parametrize("vocab", [1 << 20, (1 << 20) + 1, 255, 511, 512])
+@pytest.mark.parametrize("n", [3000, 5000, 12000])
+def test_embed_grad_sorts_by_vocabulary(vocab, n):
+    """Vocabularies at and past what one launch sorts, and at the ends of its ranges."""
+    grad_case(n, n, vocab, 4, "f32", "f32", 64, False)
