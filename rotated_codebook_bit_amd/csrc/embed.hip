@@ -20,11 +20,11 @@
 // most of the bytes at training sizes, are cleared by a plain fill that runs
 // beside the sort.  Short lists are not sorted: one launch compares every
 // position with all others (below).
-// 16384 bf16 rows of 4096 into 32000 rows of float32 (0.66 GB): 95 us for the
-// fill with the sort (31 us alone) beside it, 55 for the sums, 9 to join long
-// runs, 4.1 TB/s over all; a block per table row that searched the sorted list
-// for its run, zeros included, took 250.  With cached instead of streaming
-// stores the fill takes 75 us and the sums, behind its write-backs, 76.
+// 16384 bf16 rows of 4096 into 32000 rows of float32 (0.66 GB): 92 us for the
+// fill with the sort beside it, 55 for the sums, 9 to join long runs, 4.2 TB/s
+// over all; a block per table row that searched the sorted list for its run,
+// zeros included, took 250.  With cached instead of streaming stores the fill
+// takes 75 us and the sums, behind its write-backs, 76.
 #include <utility>
 
 #include "lanes.h"
@@ -195,7 +195,10 @@ embed_packed_kernel(EmbedArgs a, LevelTable lv, uint32_t waves, uint32_t per_row
 // ---- Gradient: sorting the positions by token --------------------------------------------
 
 constexpr int kDigit = 256;       // 8-bit digits, least significant first
-// Tokens and vocabulary that one launch sorts, the fill running beside it.
+// Tokens and vocabulary that one launch sorts, the fill running beside it: two
+// passes in one block took 32.6 us for 12000 tokens of 1000, four launches over
+// tiles 24 and their gaps, ranges take 17.1 (6000 of 4000: 18.4, 23 and 9.7).
+// Past it every range's look at all tokens would cost more than tiles do.
 constexpr int64_t kSortOne = 16384, kSortVocab = int64_t(1) << 20;
 bool one_launch_sorts(int64_t n, int64_t vocab) { return n <= kSortOne && vocab <= kSortVocab; }
 
@@ -976,9 +979,11 @@ hipError_t launch_embed_grad(const EmbedGradArgs& a, uint8_t* ws, hipStream_t s)
   float* partial;
   if (one_launch_sorts(a.n, a.vocab)) {
     partial = reinterpret_cast<float*>(at(2 * g.list));
-    // Beside the sort's LDS two blocks fit a CU: that many clear, looping.
+    // Beside the sort's LDS two blocks fit a CU: that many in all, the clearing
+    // ones looping (at least one per CU).
     const uint32_t ranges = static_cast<uint32_t>(a.vocab / kDigit + 1);
-    const dim3 grid(ranges + clear_blocks(a, kOneThreads, 2 * static_cast<int64_t>(device_cu_count()))), block(kOneThreads);
+    const int64_t cus = device_cu_count(), beside = ranges < cus ? 2 * cus - ranges : cus;
+    const dim3 grid(ranges + clear_blocks(a, kOneThreads, beside)), block(kOneThreads);
     if (a.n > 8 * kOneThreads)
       sort_ranges_kernel<16><<<grid, block, 0, s>>>(a, ranges, keys, order);
     else if (a.n > 4 * kOneThreads)
