@@ -20,7 +20,7 @@
 // most of the bytes at training sizes, are cleared by a plain fill that runs
 // beside the sort.  Short lists are not sorted: one launch compares every
 // position with all others (below).
-// 16384 bf16 rows of 4096 into 32000 rows of float32 (0.66 GB): 92 us for the
+// 16384 bf16 rows of 4096 into 32000 rows of float32 (0.66 GB): 94 us for the
 // fill with the sort beside it, 55 for the sums, 9 to join long runs, 4.2 TB/s
 // over all; a block per table row that searched the sorted list for its run,
 // zeros included, took 250.  With cached instead of streaming stores the fill
