@@ -972,6 +972,10 @@ int64_t embed_grad_workspace(int64_t n, int64_t vocab, int64_t dim) {
 int64_t embed_grad_blocks(int64_t n, int64_t dim) { return pieces_of(n) * ((dim + kSlice - 1) / kSlice); }
 
 hipError_t launch_embed_grad(const EmbedGradArgs& a, uint8_t* ws, hipStream_t s) {
+  if (a.n == 0) {  // no tiles: the launch is the fill alone (accumulating calls end before)
+    count_kernel<<<dim3(clear_blocks(a, kBlock, kMaxClear)), dim3(kBlock), 0, s>>>(a, 0, nullptr, nullptr, 0);
+    return hipGetLastError();
+  }
   if (scans(a.n, a.dim)) return a.dout_bf16 ? launch_grad_scan<true>(a, s) : launch_grad_scan<false>(a, s);
   const GradSpace g = grad_space(a.n, a.vocab, a.dim);
   auto at = [&](int64_t off) { return reinterpret_cast<uint32_t*>(ws + off); };
@@ -1008,7 +1012,6 @@ hipError_t launch_embed_grad(const EmbedGradArgs& a, uint8_t* ws, hipStream_t s)
     }
     // The last pass wrote what the swap made `keys` and `order`.
   }
-  if (a.n == 0) return hipGetLastError();
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const bool wide = a.dim % 4 == 0;
