@@ -15,7 +15,9 @@
 // spread each group's outliers.
 //
 // Gradient, with u = w * dy, r = rsqrt(mean(h^2) + eps):
-//   dx = dsum + r u - h r^3 mean(u h),   dw = sum over rows of dy h r.
+//   dx = dsum + r (u - h r (r mean(u h))),   dw = sum over rows of dy h r.
+// In these factors: h r and r mean(u h) are about 1 and u whatever the row's
+// magnitude, while r^3 would leave float32 for rows below 1e-13 or above 1e15.
 //
 // Memory bounds all three at many rows, so nothing is read or written twice
 // and every load and store is 16 bytes per lane.  bf16 8192 x 4096 to 8 bits
@@ -385,7 +387,7 @@ norm_grad_kernel(NormGradArgs a) {
     }
     const float n = static_cast<float>(cols);
     const float r = rsqrtf(ss / n + a.eps);
-    const float k = r * r * r * (dot / n);
+    const float k = r * (dot / n);
     uint8_t* const out = a.dx + row * a.cols * EB;
 #pragma unroll
     for (int l = 0; l < R; ++l) {
@@ -394,10 +396,10 @@ norm_grad_kernel(NormGradArgs a) {
 #pragma unroll
       for (int j = 0; j < M; ++j) {
         const int i = l * M + j;
-        const float hv = value(h, i), g = value(dy, i);
-        d[j] = __builtin_fmaf(-hv, k, r * (w[i] * g));
+        const float hn = value(h, i) * r, g = value(dy, i);
+        d[j] = r * __builtin_fmaf(-hn, k, w[i] * g);
         if (a.dsum) d[j] += value(ds, i);
-        if (inside(i)) dw[i] = __builtin_fmaf(g, hv * r, dw[i]);
+        if (inside(i)) dw[i] = __builtin_fmaf(g, hn, dw[i]);
       }
       if constexpr (WIDE) {
         if (p < np) reinterpret_cast<uint4*>(out)[p] = pack_piece<BF16>(d);
@@ -505,7 +507,7 @@ norm_grad_wide_kernel(NormGradArgs a) {
     turn ^= 1;
     const float n = static_cast<float>(a.cols);
     const float r = rsqrtf(ss / n + a.eps);
-    const float k = r * r * r * (dot / n);
+    const float k = r * (dot / n);
     for (int i = t; i < np; i += kWideThreads) {
       float h[V], g[V], w[V], d[V], s[V];
       load(a.sum + first, i, h);
@@ -514,9 +516,9 @@ norm_grad_wide_kernel(NormGradArgs a) {
       if (a.dsum) load(a.dsum + first, i, d);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const float v = __builtin_fmaf(-h[j], k, r * (w[j] * g[j]));
+        const float hn = h[j] * r, v = r * __builtin_fmaf(-hn, k, w[j] * g[j]);
         d[j] = a.dsum ? v + d[j] : v;
-        s[j] = __builtin_fmaf(g[j], h[j] * r, dw[i * V + j]);
+        s[j] = __builtin_fmaf(g[j], hn, dw[i * V + j]);
       }
       // dx may be dsum: this thread has read its own columns.
       if constexpr (WIDE)
