@@ -456,7 +456,9 @@ int cq_rms_norm_grad(const void* dout, const void* sum, const void* dsum, int dt
 /* The codebook of the 8-bit product: level k ~ scale * (256 hi[k] + lo[k]).
  * cq_q8_levels picks the scale that fits the levels (nullable: built-in table
  * of the width) best in the mean square over N(0,1), once per codebook; each
- * level is met to within 2.1e-5 of the largest. */
+ * level is met to within 2.1e-5 of the largest.  CQ_ERR_ARG for tables whose
+ * largest level lies below about 6e-33: their scale would not be a normal
+ * float32. */
 typedef struct {
   int8_t hi[CQ_MAX_LEVELS];
   int8_t lo[CQ_MAX_LEVELS];

@@ -18,6 +18,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <limits>
 #include <map>
 #include <mutex>
 #include <numeric>
@@ -1265,7 +1266,7 @@ int cq_q8_levels(int bits, const float* levels, int n_levels, cq_q8_table* table
     p[i] = std::max(upto - below, 1e-6);  // a cell no N(0,1) value meets still counts a little
     below = upto;
   }
-  double best = -1.0;
+  double best = -1.0, a_best = 0.0;
   int m_best[cq::kMaxLevels] = {0};
   for (int largest = kHigh; largest >= kLow; --largest) {
     double cm = 0.0, mm = 0.0, err = 0.0;
@@ -1284,11 +1285,15 @@ int cq_q8_levels(int bits, const float* levels, int n_levels, cq_q8_table* table
     }
     if (near && (best < 0.0 || err < best)) {
       best = err;
-      table->scale = static_cast<float>(a);
+      a_best = a;
       for (int i = 0; i < L; ++i) m_best[i] = m[i];
     }
   }
-  if (best < 0.0) return fail(CQ_ERR_ARG, "levels cannot be held in 16 bits");  // their largest overflows or vanishes
+  // The product's factor scale / sqrt(G), G up to 256, has to stay a normal
+  // float32: below that the scale loses its bits, down to 0.
+  if (best < 0.0 || a_best < 16.0 * std::numeric_limits<float>::min())
+    return fail(CQ_ERR_ARG, "levels cannot be held in 16 bits and a float32 scale");
+  table->scale = static_cast<float>(a_best);
   std::memset(table->hi, 0, sizeof(table->hi));
   std::memset(table->lo, 0, sizeof(table->lo));
   for (int i = 0; i < L; ++i) {
