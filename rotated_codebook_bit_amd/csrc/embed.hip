@@ -845,8 +845,22 @@ int64_t align256(int64_t b) { return (b + 255) & ~int64_t(255); }
 int piece_of(int64_t n) { return n <= 8192 ? 16 : n <= 65536 ? 32 : 64; }
 int64_t pieces_of(int64_t n) { return (n + piece_of(n) - 1) / piece_of(n); }
 
-bool scans(int64_t n, int64_t dim) {
-  return n > 0 && n <= kScanMost && (dim + kSlice - 1) / kSlice <= kScanCompares / (n * n);
+// Table rows per clearing block of a scan, and the scan's blocks.
+int64_t scan_rows(const EmbedGradArgs& a) {
+  const int64_t fit = kScanBytes / (a.dim * (a.grad_bf16 ? 2 : 4));
+  return fit < 1 ? 1 : fit < kScanRows ? fit : kScanRows;
+}
+int64_t scan_clear_blocks(const EmbedGradArgs& a) {
+  const int64_t rows = scan_rows(a);
+  return a.accumulate ? 0 : (a.vocab + rows - 1) / rows;
+}
+
+// Tables of 2^30 narrow rows would take the clearing blocks past a launch's
+// 2^32 threads; the sort's clearing blocks loop.
+bool scans(const EmbedGradArgs& a) {
+  const int64_t slices = (a.dim + kSlice - 1) / kSlice;
+  return a.n > 0 && a.n <= kScanMost && slices <= kScanCompares / (a.n * a.n) &&
+         a.n * slices + scan_clear_blocks(a) <= most_blocks(kBlock);
 }
 
 // Workspace of the sort: sorted keys and positions (twice in the many-block sort), the
@@ -924,10 +938,8 @@ hipError_t launch_embed_at(const EmbedArgs& all, hipStream_t s) {
 
 template <bool BF16>
 hipError_t launch_grad_scan(const EmbedGradArgs& a, hipStream_t s) {
-  const int64_t slices = (a.dim + kSlice - 1) / kSlice, sums = a.n * slices;
-  const int64_t fit = kScanBytes / (a.dim * (a.grad_bf16 ? 2 : 4)), rows = fit < 1 ? 1 : fit < kScanRows ? fit : kScanRows;
-  const int64_t clear = a.accumulate ? 0 : (a.vocab + rows - 1) / rows;
-  const dim3 grid(static_cast<uint32_t>(sums + clear)), block(kBlock);
+  const int64_t slices = (a.dim + kSlice - 1) / kSlice, sums = a.n * slices, rows = scan_rows(a);
+  const dim3 grid(static_cast<uint32_t>(sums + scan_clear_blocks(a))), block(kBlock);
   const uint32_t n_sums = static_cast<uint32_t>(sums), n_slices = static_cast<uint32_t>(slices);
   if (a.dim % 4 == 0)
     embed_grad_scan_kernel<BF16, true><<<grid, block, 0, s>>>(a, n_sums, n_slices, static_cast<uint32_t>(rows));
@@ -976,7 +988,7 @@ hipError_t launch_embed_grad(const EmbedGradArgs& a, uint8_t* ws, hipStream_t s)
     count_kernel<<<dim3(clear_blocks(a, kBlock, kMaxClear)), dim3(kBlock), 0, s>>>(a, 0, nullptr, nullptr, 0);
     return hipGetLastError();
   }
-  if (scans(a.n, a.dim)) return a.dout_bf16 ? launch_grad_scan<true>(a, s) : launch_grad_scan<false>(a, s);
+  if (scans(a)) return a.dout_bf16 ? launch_grad_scan<true>(a, s) : launch_grad_scan<false>(a, s);
   const GradSpace g = grad_space(a.n, a.vocab, a.dim);
   auto at = [&](int64_t off) { return reinterpret_cast<uint32_t*>(ws + off); };
   uint32_t *keys = at(0), *order = at(g.list);
