@@ -475,6 +475,9 @@ int cq_q8_levels(int bits, const float* levels, int n_levels, cq_q8_table* table
  * step) to many.  The sums within a group are exact integers on the table's
  * 16-bit levels, the sum over groups float32.  k a multiple of G, at most
  * 2^22, n_out below 2^27; trit storage is converted with cq_repack first.  table: host.
+ * The 2^32 threads of a launch bound the sizes too (CQ_ERR_UNSUPPORTED past
+ * them): n_out <= 2^27 - 16 up to 64 batch rows (32 at G = 256), more rows
+ * ceil(n_out / 128) * ceil(batch / 128) < 2^24.
  * workspace: cq_dequant_gemm_q8_workspace bytes (0 for many calls: NULL). */
 int cq_dequant_gemm_q8_workspace(int64_t n_out, int64_t k, int64_t batch, int group_size, int64_t* bytes);
 int cq_dequant_gemm_q8(const uint8_t* packed, const uint16_t* norms, int64_t n_out, int64_t k, int bits,

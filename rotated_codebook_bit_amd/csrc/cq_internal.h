@@ -717,6 +717,7 @@ struct GemmQ8Args {
   int y_bf16;
 };
 int64_t gemm_q8_workspace(int64_t n_out, int64_t k, int64_t batch, int group_size);
+int64_t gemm_q8_threads(int64_t n_out, int64_t k, int64_t batch, int group_size);  // of the product's launch
 hipError_t launch_gemm_q8_empty(const GemmQ8Args& a, hipStream_t stream);  // k = 0: zeros
 hipError_t launch_gemm_q8(const GemmQ8Args& a, int sbits, int group_size, Q8Levels lv, float* ws, hipStream_t stream);
 

@@ -641,6 +641,11 @@ constexpr int64_t kFewRows = 64;
 constexpr int kRowTiles = 4;  // row tiles of 32 of the tiled kernel
 constexpr int kCus = 256;
 
+int64_t few_blocks(int64_t n_out) { return (n_out + 15) / 16; }
+int64_t tile_count(int64_t n_out, int64_t batch) {  // of the tiled kernel, per range of k
+  return (n_out + kGemmCols - 1) / kGemmCols * ((batch + 32 * kRowTiles - 1) / (32 * kRowTiles));
+}
+
 // The ranges of k that an estimate finds fastest: rounds of one block per CU,
 // 1.6 us per tile and block (1.1 to 1.6 measured), two blocks on a CU at 1.7
 // times one; then 3 us and 8 bytes per partial sum at 4 TB/s to join them.  Measured (us, ranges
@@ -656,7 +661,7 @@ Plan plan_for(int64_t n_out, int64_t k, int64_t batch, int group_size) {
   }
   const int kt = group_size > 128 ? group_size : 128;
   const int64_t tiles = (k + kt - 1) / kt;
-  const int64_t blocks = (n_out + kGemmCols - 1) / kGemmCols * ((batch + 32 * kRowTiles - 1) / (32 * kRowTiles));
+  const int64_t blocks = tile_count(n_out, batch);
   p.per = static_cast<int>(tiles);
   double best = 0.0;
   // Ranges of 4 tiles or more, and no more than two blocks per CU.
@@ -676,7 +681,7 @@ Plan plan_for(int64_t n_out, int64_t k, int64_t batch, int group_size) {
 
 template <int SB, int G, int MT, int P>
 hipError_t launch_few(const GemmQ8Args& a, const Q8Levels& lv, float unit, hipStream_t s) {
-  const dim3 grid(static_cast<uint32_t>((a.n_out + 15) / 16));
+  const dim3 grid(static_cast<uint32_t>(few_blocks(a.n_out)));
   few_kernel<SB, G, MT, P, kFewWaves><<<grid, dim3(kFewWaves * kWave), 0, s>>>(a, lv, unit);
   return hipGetLastError();
 }
@@ -692,7 +697,7 @@ hipError_t launch_for(const GemmQ8Args& a, const Q8Levels& lv, const Plan& p, fl
       return launch_few<SB, G, 4, 1>(a, lv, unit, s);
     }
   }
-  const int64_t tiles = (a.n_out + kGemmCols - 1) / kGemmCols * ((a.batch + 32 * kRowTiles - 1) / (32 * kRowTiles));
+  const int64_t tiles = tile_count(a.n_out, a.batch);
   float* part = p.ksplit > 1 ? ws : nullptr;
   gemm_q8_kernel<SB, G, kRowTiles><<<dim3(static_cast<uint32_t>(tiles * p.ksplit)), dim3(kGemmBlock), 0, s>>>(
       a, lv, unit, part, p.ksplit, p.per);
@@ -715,6 +720,12 @@ int64_t gemm_q8_workspace(int64_t n_out, int64_t k, int64_t batch, int group_siz
   if (n_out <= 0 || k <= 0 || batch <= 0) return 0;
   const Plan p = plan_for(n_out, k, batch, group_size);
   return p.ksplit > 1 ? static_cast<int64_t>(p.ksplit) * batch * n_out * 4 : 0;
+}
+
+int64_t gemm_q8_threads(int64_t n_out, int64_t k, int64_t batch, int group_size) {
+  if (n_out <= 0 || k <= 0 || batch <= 0) return 0;
+  const Plan p = plan_for(n_out, k, batch, group_size);
+  return p.few ? few_blocks(n_out) * kFewWaves * kWave : tile_count(n_out, batch) * p.ksplit * kGemmBlock;
 }
 
 hipError_t launch_gemm_q8_empty(const GemmQ8Args& a, hipStream_t s) {

@@ -1311,8 +1311,9 @@ static int check_q8_sizes(int64_t n_out, int64_t k, int64_t batch, int group_siz
   if (batch < 1) return fail(CQ_ERR_ARG, "batch must be >= 1");
   if (k % group_size) return fail(CQ_ERR_UNSUPPORTED, "k=%lld is not a multiple of %d", (long long)k, group_size);
   if (k > cq::kQ8MaxK) return fail(CQ_ERR_UNSUPPORTED, "k=%lld: this product takes k <= 2^22", (long long)k);
-  if (n_out >= (int64_t(1) << 27) || batch > kMaxIndex || !fits(n_out, std::max(k, batch), 4) || !fits(batch, k, 4) ||
-      ceil_div(n_out, 128) > kMaxIndex / ceil_div(batch, 128) / 8 || ceil_div(batch, 8) > kMaxIndex * 16 / std::max<int64_t>(n_out, 1))
+  if (n_out >= (int64_t(1) << 27) || batch > kMaxIndex || !fits(n_out, std::max(k, batch), 4) || !fits(batch, k, 4))
+    return fail(CQ_ERR_UNSUPPORTED, "n_out must be below 2^27, batch at most 2^31 - 2");
+  if (cq::gemm_q8_threads(n_out, k, batch, group_size) > 0xFFFFFFFFll)
     return fail(CQ_ERR_UNSUPPORTED, "batch * n_out is past this call's grid");
   return CQ_OK;
 }
