@@ -198,8 +198,14 @@ constexpr int kDigit = 256;       // 8-bit digits, least significant first
 // Tokens and vocabulary that one launch sorts, the fill running beside it: two
 // passes in one block took 32.6 us for 12000 tokens of 1000, four launches over
 // tiles 24 and their gaps, ranges take 17.1 (6000 of 4000: 18.4, 23 and 9.7).
-// Past it every range's look at all tokens would cost more than tiles do.
-constexpr int64_t kSortOne = 16384, kSortVocab = int64_t(1) << 20;
+// 2^14 tokens are what a range's list in shared memory holds (64 KiB).  Past
+// 2^18 rows there are so many ranges, each reading all tokens, that tiles are
+// faster, first with many tokens.  Whole calls, ranges and tiles, us, 3000, 8192 and 16384 bf16 rows of 64 into 128256 rows 24.1 and
+// 45.9, 26.7 and 49.2, 42.5 and 55.3; into 256000 31.9 and 50.7, 38.7 and 54.6,
+// 60.8 and 58.4; into 524288 52.5 and 62.6, 62.2 and 65.3, 103.5 and 71.2; into
+// 2^20 88.4 and 86.6, 108 and 89.6, 179 and 94.4 (rows of 512 into 524288 228
+// and 217, 244 and 220, 268 and 228).
+constexpr int64_t kSortOne = 16384, kSortVocab = int64_t(1) << 18;
 bool one_launch_sorts(int64_t n, int64_t vocab) { return n <= kSortOne && vocab <= kSortVocab; }
 
 // A constant in a register of its own, so that hold_value() holds that one.

@@ -162,6 +162,17 @@ def test_short_lists_of_wide_rows(n, vocab, dim):
     check("wide rows", t, vocab, dim)
 
 
+@pytest.mark.parametrize("vocab", [(1 << 18) - 1, 1 << 18, (1 << 18) + 1])
+@pytest.mark.parametrize("n", [3000, 16384])
+def test_ranges_or_tiles(vocab, n):
+    """Both sides of the vocabulary past which tiles sort short lists too."""
+    rng = np.random.default_rng(vocab + n)
+    t = rng.integers(-1, vocab + 1, n)
+    t[: n // 3] = vocab - 1
+    check("ranges or tiles", t, vocab, 20, "bf16", "f32")
+    check("ranges or tiles", t, vocab, 20, "f32", "bf16", True, 32)
+
+
 @pytest.mark.parametrize("n", [4096, 4097, 8192, 8193, 16384, 16385, 65536, 65537, 200001])
 def test_lengths(n):
     rng = np.random.default_rng(n)
