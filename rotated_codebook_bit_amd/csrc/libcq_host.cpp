@@ -1247,7 +1247,8 @@ int cq_rms_norm_grad(const void* dout, const void* sum, const void* dsum, int dt
 // [24576, 32639] (both bytes then fit), the rounded levels and the scale that
 // fits them best, weighted by the cells' shares of N(0,1); the best of all.
 // With the largest level simply at the top the error is up to 2.7e-5 of the
-// output at 16 levels; the search brings it to a few 1e-6.
+// output at 16 levels; the search brings it to 6.5e-6 (8 levels 9.7e-7, 3 and
+// 4 levels 2e-8 to 3.4e-8: few levels can be met almost exactly).
 int cq_q8_levels(int bits, const float* levels, int n_levels, cq_q8_table* table) {
   g_last_error[0] = 0;
   int L, rc;
