@@ -412,9 +412,12 @@ int cq_embed_packed(const void* tokens, int token_bytes, int64_t n, const uint8_
  * accumulate == 0: every one of the vocab x dim values is written (zeros for
  * tokens that do not occur); 1: the sums are added to grad, and only rows of
  * tokens that occur are touched.  Ids outside [0, vocab) contribute nothing.
- * The positions are sorted by token first, so each row is summed in a fixed
- * order.  workspace: cq_embed_grad_workspace bytes (host only, pure; about
- * 8 to 16 bytes per position, plus dim / 8 per position past 64). */
+ * Long lists are sorted by token, short ones compared position by position;
+ * either way each row is summed in an order that n and dim fix.  workspace:
+ * cq_embed_grad_workspace bytes (host only, pure): per position 8 bytes, past
+ * 16384 positions or 2^18 rows 16.5, and for sums of long runs 8 dim / P with
+ * P = 16 up to 8192 positions, 32 up to 65536 and 64 beyond (none for at most
+ * P positions).  Short lists pass it too, though they do not use it. */
 int cq_embed_grad_workspace(int64_t n, int64_t vocab, int64_t dim, int64_t* bytes);
 int cq_embed_grad(const void* tokens, int token_bytes, int64_t n, const void* dout, int dout_dtype,
                   int64_t vocab, int64_t dim, float scale, int accumulate, void* grad, int grad_dtype,
@@ -425,7 +428,8 @@ int cq_embed_grad(const void* tokens, int token_bytes, int64_t n, const void* do
  * CQ_BF16), weight (nullable: ones) weight_dtype, out out_dtype.  h is formed
  * and normalised in float32; sum (nullable) receives it rounded to `dtype`
  * and may be x or residual itself.  cols <= 32768 (CQ_ERR_UNSUPPORTED
- * otherwise: a row is held in registers).  eps >= 0. */
+ * otherwise: a row is held in registers).  eps >= 0.  The sum of squares is
+ * float32: a row whose sum passes it (values near 1e19) comes out as zeros. */
 int cq_add_rms_norm(const void* x, const void* residual, int dtype, const void* weight, int weight_dtype,
                     int64_t rows, int64_t cols, float eps, void* sum, void* out, int out_dtype, void* stream);
 
@@ -435,8 +439,8 @@ int cq_add_rms_norm(const void* x, const void* residual, int dtype, const void* 
  * q = round(rotated / s), ties to even, in [-127, 127].  q is rows x cols
  * int8, scale has rows float32 values: the rotated activations are q * s.
  * cols must be a multiple of group_size (32, 64, 128 or 256).  A row whose
- * rotated values all lie below 2^-118 has scale 0 and q 0; a row with a
- * value that is not finite has scale NaN and q 0. */
+ * rotated values all lie below 2^-118 / sqrt(G) has scale 0 and q 0; a row
+ * with a value that is not finite has scale NaN and q 0. */
 int cq_add_rms_norm_q8(const void* x, const void* residual, int dtype, const void* weight, int weight_dtype,
                        int64_t rows, int64_t cols, int group_size, float eps, void* sum, int8_t* q,
                        float* scale, void* stream);

@@ -11,17 +11,18 @@
 // stages inside a lane and the rest between lanes (lanes.h).
 //
 // Gradient: grad[v] = scale * sum of dout[i] over the positions i with
-// token i = v, added in position order.  The positions are sorted by token
-// (a stable radix sort); then the sorted list is cut into pieces of 64
-// positions, and a wave streams the rows of dout of one piece over 256
+// token i = v.  The positions are sorted by token (a stable radix sort); then
+// the sorted list is cut into pieces of 16, 32 or 64 positions by its length,
+// and a wave streams the rows of dout of one piece over 256
 // columns, writing a table row where a token's run ends: no atomics, and no
-// order that changes between runs.  Runs longer than a piece leave one sum
-// per piece, which are added in order afterwards.  The rows of absent tokens,
+// order that changes between runs: position order within a piece.  Runs longer
+// than a piece leave one sum per piece, which are added afterwards in four
+// consecutive shares and these in order.  The rows of absent tokens,
 // most of the bytes at training sizes, are cleared by a plain fill that runs
 // beside the sort.  Short lists are not sorted: one launch compares every
 // position with all others (below).
-// 16384 bf16 rows of 4096 into 32000 rows of float32 (0.66 GB): 94 us for the
-// fill with the sort beside it, 55 for the sums, 9 to join long runs, 4.2 TB/s
+// 16384 bf16 rows of 4096 into 32000 rows of float32 (0.66 GB): 91 us for the
+// fill with the sort beside it, 56 for the sums, 9 to join long runs, 4.2 TB/s
 // over all; a block per table row that searched the sorted list for its run,
 // zeros included, took 250.  With cached instead of streaming stores the fill
 // takes 75 us and the sums, behind its write-backs, 76.
@@ -406,8 +407,11 @@ sort_ranges_kernel(EmbedGradArgs a, uint32_t ranges, uint32_t* __restrict__ keys
 
 // One pass of the many-block sort.  count_kernel leaves every tile's digit
 // counts in counts[tile][256]; scatter_kernel adds the counts of smaller
-// digits and of earlier tiles itself (tiles * 1 KiB from the L2, a fraction
-// of a tile's own keys up to thousands of tiles) and moves its tile's keys.
+// digits and of earlier tiles itself (tiles * 1 KiB from the L2; a tile's own
+// keys and positions are 16 KiB) and moves its tile's keys.  That saves a
+// launch per pass and grows with the square of the tiles: whole calls on rows
+// of 4 into 32000 rows take 64 us for 2^17 tokens, 80 for 2^18, 194 for 2^20,
+// 854 for 2^22 and 2038 for 2^23.
 constexpr int kTileIpt = 8, kSortTile = kTileIpt * kBlock;  // 2048 keys per block
 
 __device__ __forceinline__ void tile_keys(const EmbedGradArgs& a, const uint32_t* keys, const uint32_t* order,
@@ -732,7 +736,11 @@ embed_grad_join_kernel(EmbedGradArgs a, const uint32_t* __restrict__ keys, const
 // rows into 8192 rows: 8 of 96 4.8 and 9.6, 256 of 1000 8.1 and 19.3, 777 of
 // 1000 11.2 and 20.3, 2048 of 500 (2^23) 12.9 and 23.6, 1024 of 2048 (2^23)
 // 22.9 and 25.2, 1024 of 4096 (2^24) 42.5 and 37.0, 2048 of 2048 (2^25) 41.7
-// and 26.5.
+// and 26.5.  Sizes cannot tell how often one token comes up: with half of the
+// positions one token its rows are one block's, and the sort is faster from
+// some 700 positions on (bf16: 256 of 1000 10.3 and 18.8, 777 of 1000 22.8 and
+// 20.4, 1448 of 1024 30.4 and 20.8, 2896 of 256 53.7 and 22.7, where distinct
+// tokens take 8.6 and 16.7, 12.0 and 17.4, 15.9 and 17.7, 12.6 and 16.1).
 constexpr int64_t kScanCompares = int64_t(1) << 23;
 constexpr int64_t kScanMost = 2896;  // tokens: the square root of that
 constexpr int kScanList = (kScanMost + kBlock - 1) / kBlock * kWave;
@@ -845,9 +853,12 @@ uint32_t blocks_of(int64_t waves) { return static_cast<uint32_t>((waves + kWaves
 
 int64_t align256(int64_t b) { return (b + 255) & ~int64_t(255); }
 // Positions per piece: short lists in small pieces, so that enough waves
-// stream them (777 float32 rows of 1000: 8.0 us in pieces
-// of 16, 12.6 of 32, 21.2 of 64; 16384 bf16 rows of 4096 51.0, 54.9, 56.3, and
-// 14.4, 8.9, 6.2 us to join the longer runs).
+// stream them, long ones in large ones, which leave fewer sums to join.  Whole
+// calls in pieces of 16, 32 and 64, us, bf16 rows: 3000 of 1000 21.7, 26.6 and
+// 37.1; 8192 of 1000 27.3, 31.8 and 40.2; 8192 of 4096 127, 125 and 131; 16384
+// of 4096 146, 143 and 144; 65536 of 1024 98.9, 90.4 and 94.5; 131072 of 1024
+// 145, 128 and 126; with half of the positions one token 8192 of 1000 39.2, 39.4
+// and 46.7, 65536 of 1024 160, 123 and 102, 131072 of 1024 272, 197 and 162.
 int piece_of(int64_t n) { return n <= 8192 ? 16 : n <= 65536 ? 32 : 64; }
 int64_t pieces_of(int64_t n) { return (n + piece_of(n) - 1) / piece_of(n); }
 

@@ -9,9 +9,9 @@
 //
 // The levels enter as 16-bit whole numbers, c ~ scale * (256 hi + lo), so
 // every sum within a group is an exact integer: two v_mfma_i32 per product,
-// the hi products' sum shifted up by 8 as the lo products' starting value
-// (|sum| <= 256 * 128 * 32768 = 2^30 at the largest group).  Only the step
-// between groups, one fma with the group's norm, rounds.  Two integer terms
+// the hi products' sum shifted up by 8 and added to the lo products' (|sum| <=
+// 256 * 128 * 32768 = 2^30 at the largest group).  Only its conversion and the
+// step between groups, one fma with the group's norm, round.  Two integer terms
 // take the matrix cores as long as one bf16 product of the same shape would,
 // and the activations are a quarter of the bytes of float32.
 #include <type_traits>
@@ -126,10 +126,15 @@ __device__ __forceinline__ i32x4 ordered(i32x4 q) {
 // 29.8 us.  So a wave loads a unit's codes and activations in memory order
 // (whole lines), one unit ahead, passes them through its own piece of LDS
 // (rows an odd number of 16 bytes apart, so that 8 rows of one column fall on
-// different banks) and reads the operands there: 14.4 and 18.5 us.  What is
-// left at one batch row is mostly the decoding, about a vector operation and
-// a half per 2-bit code (11008 x 4096: 6.4 us, 1.9 TB/s of its bytes; 4096 x
-// 4096: 4.1, 32000 x 4096: 12.8).
+// different banks) and reads the operands there: 14.4 and 18.5 us.  One batch
+// row, 2 bits: 4096 x 4096 4.1 us, 11008 x 4096 6.4 (1.9 TB/s of its bytes),
+// 32000 x 4096 12.8, or 2.9 us and 0.31 per 1000 outputs.  By the counters the
+// vector units are busy for half of the time (3.2 of 6.4 us; 2.4 operations a
+// code, the decoding and all else) and the waves wait for loads and LDS for 55%
+// of theirs; at 37 rows (4-bit 4096 x 11008, two waves per SIMD) half (7.4 of
+// 15 us; 5.6 a code) and 36%.  Each wave takes its units one after the other, so
+// what bounds both is the chain of load, store, read and product that so few
+// waves do not cover.
 
 // What a wave stages per unit: 16 rows of codes, MT 16 / P rows of
 // activations and, for activation rows of the other group, a run of zeros.
