@@ -493,6 +493,145 @@ int cq_dequant_gemm_q8(const uint8_t* packed, const uint16_t* norms, int64_t n_o
                        int64_t batch, void* y, int y_dtype, void* workspace, int64_t workspace_bytes,
                        void* stream);
 
+/* ---- An attention block and a model's end ----------------------------------
+ *
+ * Between the query, key and value projections and the output projection: the
+ * norm of queries and keys for each head with the position rotation, and
+ * attention over prompts and caches; behind the last product: the log
+ * probabilities of given tokens.  Each with its gradient.  The rules of the
+ * section before hold (nothing allocated, workspaces from host-only size
+ * functions, capture, determinism), but for the tensors of heads, which may
+ * be strided. */
+
+/* Value d of head h of row i: data[i * row_stride + h * head_stride + d]
+ * (strides in values), d < head_dim.  data 16-byte aligned; strides not
+ * negative and multiples of 8 (bf16) or 4 (float32) values, row_stride at
+ * most 2^22.  So queries, keys and values may be parts of one projection's
+ * output, and rows of a cache.  Inputs may have rows or heads that share
+ * memory (stride 0); no value of an output may lie twice. */
+typedef struct {
+  void* data;
+  int64_t row_stride;
+  int64_t head_stride;
+} cq_heads;
+
+/* Queries q (n rows of q_heads heads) and keys k (n rows of kv_heads), each
+ * head x of head_dim values on its own:
+ *   y = x * rsqrt(mean(x^2) + eps) * weight    (norm = 1; norm = 0: y = x),
+ * then the first rotary_dim values of y turn in pairs, pair j < rotary_dim / 2
+ * by the angle t = positions[i] * freqs[j]: values j and j + rotary_dim / 2
+ * (interleaved = 0) or 2 j and 2 j + 1 (interleaved = 1) become
+ *   a cos t - b sin t,  b cos t + a sin t.
+ * The product positions[i] * freqs[j] is taken in 64 bits (freqs: device,
+ * float32, nullable with rotary_dim = 0, like positions; position_bytes 4 or
+ * 8), the rest in float32, rounded once to `dtype`.  q_weight, k_weight: device,
+ * [head_dim] of weight_dtype, nullable: ones (norm = 0: must be NULL).
+ * q_out takes the n query rows; k_out takes key row i as its row slots[i]
+ * (slot_bytes 4 or 8, slots in [0, cache_rows); other slots: the row is not
+ * written) or, slots NULL, as its row i.  v, v_out (both or neither NULL): values
+ * copied to the same rows.  Rows of a cache that no slot names stay as they
+ * are; of equal slots any one's row may stay.  q_out may be q, without slots
+ * k_out may be k and v_out v (same data and strides).  head_dim: a multiple of
+ * 8, at most 256; rotary_dim even, at most head_dim. */
+int cq_qk_norm_rope(const cq_heads* q, const cq_heads* k, const cq_heads* v, int dtype, int64_t n, int q_heads,
+                    int kv_heads, int head_dim, int norm, const void* q_weight, const void* k_weight,
+                    int weight_dtype, float eps, const void* positions, int position_bytes, const float* freqs,
+                    int rotary_dim, int interleaved, const cq_heads* q_out, const cq_heads* k_out,
+                    const cq_heads* v_out, const void* slots, int slot_bytes, int64_t cache_rows, void* stream);
+
+/* Gradient of cq_qk_norm_rope (without slots) at its inputs q and k (norm = 0:
+ * not read, may be NULL): dq_out and dk_out are what reaches its outputs, dq and
+ * dk what reaches q and k; dq may be dq_out, dk dk_out.  dq_weight, dk_weight:
+ * float32 [head_dim], nullable, summed over rows and heads (norm = 0: must be
+ * NULL).  workspace: cq_qk_norm_rope_grad_workspace bytes (only with a weight's
+ * gradient). */
+int cq_qk_norm_rope_grad_workspace(int64_t n, int q_heads, int kv_heads, int head_dim, int64_t* bytes);
+int cq_qk_norm_rope_grad(const cq_heads* dq_out, const cq_heads* dk_out, const cq_heads* q, const cq_heads* k, int dtype,
+                         int64_t n, int q_heads, int kv_heads, int head_dim, int norm, const void* q_weight,
+                         const void* k_weight, int weight_dtype, float eps, const void* positions, int position_bytes,
+                         const float* freqs, int rotary_dim, int interleaved, const cq_heads* dq, const cq_heads* dk,
+                         float* dq_weight, float* dk_weight, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* The sequences of an attention call.  Sequence s < n_seq has the query rows
+ * q_starts[s] .. q_starts[s+1] - 1 and the key rows k_starts[s] .. k_starts[s]
+ * + k_lens[s] - 1.  All three are device arrays of index_bytes (4 or 8):
+ *   q_starts  n_seq + 1 entries, ascending; NULL: equal parts of rows_q;
+ *   k_starts  n_seq + 1 entries, ascending, without k_lens (keys end where the
+ *             next sequence's start), n_seq with it; NULL: equal parts of rows_k;
+ *   k_lens    n_seq entries; NULL: up to the next start.
+ * So a packed batch gives q_starts and k_starts, a regular one nothing, and
+ * decoding over a cache of equal parts k_lens alone.  Parts that are not equal
+ * (rows not a multiple of n_seq) are CQ_ERR_ARG.  What the arrays hold is not
+ * known to the host: starts and lengths that leave the tensors are cut to them,
+ * and of starts that do not ascend some rows may not be computed. */
+typedef struct {
+  int64_t n_seq;
+  int64_t rows_q;
+  int64_t rows_k;
+  const void* q_starts;
+  const void* k_starts;
+  const void* k_lens;
+  int index_bytes;
+} cq_sequences;
+
+/* Attention: for query row i (the i-th of its sequence's n_q) and head h, over
+ * the sequence's keys j < n_k of key head h / (q_heads / kv_heads),
+ *   x_j = scale * q . k_j,  lse = log sum_j exp(x_j),  out = sum_j exp(x_j - lse) v_j,
+ * causal = 1: only over j <= i + n_k - n_q (the last query sees every key).  A
+ * row that sees no key has out 0 and lse -infinity.  lse: float32
+ * [rows_q][q_heads], nullable.  Rows of out and lse in no sequence, and keys in
+ * none, are not touched.  Scores, sums and out are float32, out rounded once; bf16
+ * calls with more than 32 rows and heads per sequence and key head round the
+ * probabilities to bf16.  Sequences may share key rows.  A value of k or v that is
+ * not finite may reach any row of out of the sequences whose key it is, seen or
+ * not, and no other.
+ * head_dim: a multiple of 8, at most 128; q_heads a multiple of kv_heads;
+ * scale > 0.  workspace: cq_attention_workspace bytes (0 for many calls: NULL);
+ * how the keys are split, and so its size, depends on the sizes, head_dim,
+ * dtype and on whether q_starts and k_starts are NULL. */
+int cq_attention_workspace(const cq_sequences* seqs, int dtype, int q_heads, int kv_heads, int head_dim, int64_t* bytes);
+int cq_attention(const cq_heads* q, const cq_heads* k, const cq_heads* v, int dtype, const cq_sequences* seqs,
+                 int q_heads, int kv_heads, int head_dim, int causal, float scale, const cq_heads* out, float* lse,
+                 void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Gradient of cq_attention at its inputs, its out and its lse: dq (rows_q,
+ * q_heads), dk and dv (rows_k, kv_heads; summed over the group's query heads)
+ * of what reaches out.  Rows in no sequence are not touched.  Every key row may
+ * belong to one sequence only.  workspace: cq_attention_grad_workspace bytes. */
+int cq_attention_grad_workspace(const cq_sequences* seqs, int dtype, int q_heads, int kv_heads, int head_dim,
+                                int64_t* bytes);
+int cq_attention_grad(const cq_heads* dout, const cq_heads* q, const cq_heads* k, const cq_heads* v, const cq_heads* out,
+                      const float* lse, int dtype, const cq_sequences* seqs, int q_heads, int kv_heads, int head_dim,
+                      int causal, float scale, const cq_heads* dq, const cq_heads* dk, const cq_heads* dv,
+                      void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Per row of logits (rows of vocab values of `dtype`, row r at logits + r *
+ * row_stride values, logits 16-byte aligned, row_stride >= vocab), x = scale *
+ * logits, scale > 0 (one over a temperature), in float32:
+ *   lse = log sum exp(x),  logprob = x[tokens[r]] - lse (token_bytes 4 or 8; a
+ * token outside [0, vocab): 0),  entropy = -sum p log p with p = exp(x - lse),
+ * and the `top` (0 .. 64, at most vocab) largest logits, equal ones by lower
+ * index: top_ids int64 [rows][top], top_logprobs float32 [rows][top].
+ * logprob, entropy, lse: float32 [rows], each nullable (tokens with logprob).
+ * Logits of -infinity (tokens not allowed) have probability 0.  A row of
+ * nothing else: lse -infinity, entropy 0, log probabilities -infinity.  A row
+ * with a NaN or +infinity: all its values NaN, its top tokens those, NaN first. */
+int cq_token_logprobs(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t row_stride, float scale,
+                      const void* tokens, int token_bytes, float* logprob, float* entropy, float* lse, int top,
+                      int64_t* top_ids, float* top_logprobs, void* stream);
+
+/* Gradient with respect to the logits, from the forward's lse (and entropy,
+ * with dentropy): with p = exp(x - lse),
+ *   dlogits[j] = scale * (dlogprob ([j = token] - p_j) - dentropy p_j (x_j - lse + entropy)).
+ * dlogprob, dentropy (nullable: zero): float32 [rows].  A token outside
+ * [0, vocab) has no logprob, so its dlogprob is not used.  dlogits has `dtype`
+ * and out_stride >= vocab; it may be logits (with row_stride).  A row of -infinity
+ * has gradient 0. */
+int cq_token_logprobs_grad(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t row_stride, float scale,
+                           const void* tokens, int token_bytes, const float* lse, const float* dlogprob,
+                           const float* dentropy, const float* entropy, void* dlogits, int64_t out_stride,
+                           void* stream);
+
 /* Static description of a status code. */
 const char* cq_status_str(int status);
 

@@ -10,7 +10,9 @@ a call fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
+from typing import Any, NamedTuple
 
 import numpy as np
 
@@ -20,7 +22,8 @@ __all__ = [
     "dequant_matvec_many_noalloc",
     "fake_quant", "blob_layout", "quantize_many", "dequantize_many", "dequant_gemm",
     "dequant_gemm_many", "embed", "embed_packed", "embed_grad", "add_rms_norm", "add_rms_norm_q8", "rms_norm_grad",
-    "Q8Table", "q8_levels", "dequant_gemm_q8",
+    "Q8Table", "q8_levels", "dequant_gemm_q8", "qk_norm_rope", "qk_norm_rope_grad", "attention", "attention_grad",
+    "TokenLogprobs", "token_logprobs", "token_logprobs_grad",
 ]
 
 TERNARY = 158
@@ -57,6 +60,28 @@ class MatvecDesc(ctypes.Structure):
     """cq_matvec_desc: one matrix of cq_dequant_matvec_many."""
     _fields_ = [("packed", ctypes.c_void_p), ("norms", ctypes.c_void_p), ("n_out", ctypes.c_int64),
                 ("k", ctypes.c_int64), ("x", ctypes.c_void_p), ("y", ctypes.c_void_p)]
+
+
+class Heads(ctypes.Structure):
+    """cq_heads: a tensor of heads, strides in values."""
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class Sequences(ctypes.Structure):
+    """cq_sequences: the sequences of an attention call."""
+    _fields_ = [("n_seq", ctypes.c_int64), ("rows_q", ctypes.c_int64), ("rows_k", ctypes.c_int64),
+                ("q_starts", ctypes.c_void_p), ("k_starts", ctypes.c_void_p), ("k_lens", ctypes.c_void_p),
+                ("index_bytes", ctypes.c_int)]
+
+
+class TokenLogprobs(NamedTuple):
+    """What token_logprobs returns, per row: the token's log probability, the
+    entropy, the log of the sum, and the most probable tokens (None without)."""
+    logprob: Any
+    entropy: Any
+    lse: Any
+    top: Any
+    top_logprob: Any
 
 
 class Q8Table(ctypes.Structure):
@@ -122,6 +147,21 @@ def lib() -> ctypes.CDLL:
         L.cq_dequant_gemm_q8_workspace.argtypes = [i64, i64, i64, i32, p64]
         L.cq_dequant_gemm_q8.argtypes = [vp, vp, i64, i64, i32, i32, ctypes.POINTER(Q8Table), vp, vp, i64, vp, i32, vp,
                                          i64, vp]
+        hp, sp = ctypes.POINTER(Heads), ctypes.POINTER(Sequences)
+        rotation = [i32, i64, i32, i32, i32, i32, vp, vp, i32, f32, vp, i32, vp, i32, i32]
+        L.cq_qk_norm_rope.argtypes = [hp, hp, hp, *rotation, hp, hp, hp, vp, i32, i64, vp]
+        L.cq_qk_norm_rope_grad_workspace.argtypes = [i64, i32, i32, i32, p64]
+        L.cq_qk_norm_rope_grad.argtypes = [hp, hp, hp, hp, *rotation, hp, hp, vp, vp, vp, i64, vp]
+        L.cq_attention_workspace.argtypes = [sp, i32, i32, i32, i32, p64]
+        L.cq_attention.argtypes = [hp, hp, hp, i32, sp, i32, i32, i32, i32, f32, hp, vp, vp, i64, vp]
+        L.cq_attention_grad_workspace.argtypes = L.cq_attention_workspace.argtypes
+        L.cq_attention_grad.argtypes = [hp, hp, hp, hp, hp, vp, i32, sp, i32, i32, i32, i32, f32, hp, hp, hp, vp, i64, vp]
+        L.cq_token_logprobs.argtypes = [vp, i32, i64, i64, i64, f32, vp, i32, vp, vp, vp, i32, vp, vp, vp]
+        L.cq_token_logprobs_grad.argtypes = [vp, i32, i64, i64, i64, f32, vp, i32, vp, vp, vp, vp, vp, i64, vp]
+        for name in ("cq_qk_norm_rope", "cq_qk_norm_rope_grad_workspace", "cq_qk_norm_rope_grad", "cq_attention_workspace",
+                     "cq_attention", "cq_attention_grad_workspace", "cq_attention_grad", "cq_token_logprobs",
+                     "cq_token_logprobs_grad"):
+            getattr(L, name).restype = i32
         for name in ("cq_embed", "cq_embed_packed", "cq_embed_grad_workspace", "cq_embed_grad", "cq_add_rms_norm",
                      "cq_add_rms_norm_q8", "cq_rms_norm_grad_workspace", "cq_rms_norm_grad", "cq_q8_levels",
                      "cq_dequant_gemm_q8_workspace", "cq_dequant_gemm_q8"):
@@ -820,3 +860,316 @@ def dequant_gemm_q8(packed, norms, n_out: int, k: int, bits: int, table: Q8Table
         packed.data_ptr(), norms.data_ptr(), n_out, k, bits, group_size, ctypes.byref(table), q.data_ptr(), scale.data_ptr(),
         batch, y.data_ptr(), oc, _opt(ws), wb, _raw_stream(dev)))
     return y
+
+
+# -- an attention block and a model's end ------------------------------------------
+
+def _heads_device(heads, flat) -> int:
+    """Index of the one CUDA device of all given tensors: `heads` may be
+    strided (but for a head's values), `flat` are contiguous; (name, tensor or
+    None) pairs."""
+    dev = _device(flat)
+    for name, t in heads:
+        if t is None:
+            continue
+        if t.dim() != 3:
+            raise ValueError(f"{name} must be [rows, heads, head_dim], got {tuple(t.shape)}")
+        if t.stride(2) != 1 and t.shape[2] > 1:
+            raise ValueError(f"{name}: a head's values must be contiguous")
+        d = t.get_device()
+        if d < 0:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if dev < 0:
+            dev = d
+        elif d != dev:
+            raise ValueError(f"{name} is on device {d}, the other tensors on {dev}")
+    return dev
+
+
+def _heads(t):
+    """A cq_heads of a [rows, heads, head_dim] tensor (None: NULL)."""
+    if t is None:
+        return None
+    rows, heads, _ = t.shape
+    return ctypes.byref(Heads(t.data_ptr(), t.stride(0) if rows > 1 else 0, t.stride(1) if heads > 1 else 0))
+
+
+def _same_kind(like_name, like, pairs):
+    """Every tensor of `pairs`, (name, tensor or None, shape), has the dtype
+    of `like` and its shape."""
+    for name, t, shape in pairs:
+        if t is not None and (t.dtype != like.dtype or tuple(t.shape) != tuple(shape)):
+            raise ValueError(f"{name} must be {like.dtype} (as {like_name}) of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+
+
+def _index_bytes(name, t) -> int:
+    import torch
+    if t.dtype == torch.int64:
+        return 8
+    if t.dtype == torch.int32:
+        return 4
+    raise TypeError(f"{name} must be int32 or int64, got {t.dtype}")
+
+
+def _rotation_args(q, k, positions, freqs, q_weight, k_weight, eps, norm, interleaved):
+    """The arguments that qk_norm_rope and its gradient share, checked: the C
+    call's from dtype to interleaved."""
+    import torch
+    code = _dtype_code("q", q)
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q and k must be [rows, heads, head_dim]")
+    n, qh, d = q.shape
+    _same_kind("q", q, (("k", k, (n, k.shape[1], d)),))
+    rotary = 0 if freqs is None else 2 * freqs.numel()
+    pb = 8
+    if rotary:
+        if freqs.dtype != torch.float32:
+            raise TypeError(f"freqs must be float32, got {freqs.dtype}")
+        if positions is None or positions.numel() != n:
+            raise ValueError(f"positions must hold {n} values")
+        pb = _index_bytes("positions", positions)
+    wc = F32
+    weights = [(name, w) for name, w in (("q_weight", q_weight), ("k_weight", k_weight)) if w is not None]
+    for name, w in weights:
+        if not norm:
+            raise ValueError(f"{name} belongs to the norm")
+        if w.numel() != d:
+            raise ValueError(f"{name} must hold {d} values")
+        if w.dtype != weights[0][1].dtype:
+            raise TypeError("q_weight and k_weight must have one dtype")
+        wc = _dtype_code(name, w)
+    return (code, n, qh, k.shape[1], d, int(bool(norm)), _opt(q_weight), _opt(k_weight), wc, eps,
+            positions.data_ptr() if rotary else None, pb, freqs.data_ptr() if rotary else None, rotary, int(bool(interleaved)))
+
+
+def qk_norm_rope(q, k, positions=None, freqs=None, q_weight=None, k_weight=None, eps: float = 1e-6, norm: bool = True,
+                 interleaved: bool = False, v=None, slots=None, q_out=None, k_out=None, v_out=None, stream=None):
+    """(q_out, k_out), with v (q_out, k_out, v_out): queries [n, q_heads, D] and
+    keys [n, kv_heads, D], each head through its root-mean-square norm times
+    q_weight / k_weight [D] (norm=False: as it is), the first 2 * len(freqs)
+    values then turned in pairs by positions[i] * freqs[j] (values j and j + len(freqs), or
+    neighbours with interleaved=True).  Tensors of heads may be strided, e.g.
+    parts of one projection's output.  slots [n]: key row i (and v's) goes to row
+    slots[i] of k_out and v_out, a cache [rows, kv_heads, D] given by the caller;
+    slots outside it write nothing.  Without slots the outputs may be given too,
+    q_out=q and k_out=k among them."""
+    args = _rotation_args(q, k, positions, freqs, q_weight, k_weight, eps, norm, interleaved)
+    n, kvh, d = k.shape
+    rows = n
+    if slots is not None:
+        if slots.numel() != n:
+            raise ValueError(f"slots must hold {n} values")
+        if k_out is None or (v is not None and v_out is None):
+            raise ValueError("slots need k_out (and v_out with v)")
+        rows = k_out.shape[0]
+    if v is None and v_out is not None:
+        raise ValueError("v_out needs v")
+    _same_kind("q", q, (("v", v, (n, kvh, d)), ("q_out", q_out, q.shape), ("k_out", k_out, (rows, kvh, d)),
+                        ("v_out", v_out, (rows, kvh, d))))
+    heads = (("q", q), ("k", k), ("v", v), ("q_out", q_out), ("k_out", k_out), ("v_out", v_out))
+    flat = (("positions", positions), ("freqs", freqs), ("q_weight", q_weight), ("k_weight", k_weight), ("slots", slots))
+    dev = _heads_device(heads, flat)
+    if not _here(dev, stream):
+        return _elsewhere(dev, stream, heads + flat, lambda: qk_norm_rope(
+            q, k, positions, freqs, q_weight, k_weight, eps, norm, interleaved, v, slots, q_out, k_out, v_out))
+    q_out = _out_tensor("q_out", q_out, q.shape, q.dtype, q)
+    k_out = _out_tensor("k_out", k_out, (rows, kvh, d), q.dtype, q)
+    v_out = None if v is None else _out_tensor("v_out", v_out, (rows, kvh, d), q.dtype, q)
+    _check("cq_qk_norm_rope", lib().cq_qk_norm_rope(
+        _heads(q), _heads(k), _heads(v), *args, _heads(q_out), _heads(k_out), _heads(v_out), _opt(slots),
+        8 if slots is None else _index_bytes("slots", slots), rows, _raw_stream(dev)))
+    return (q_out, k_out) if v is None else (q_out, k_out, v_out)
+
+
+def qk_norm_rope_grad(dq_out, dk_out, q, k, positions=None, freqs=None, q_weight=None, k_weight=None, eps: float = 1e-6,
+                      norm: bool = True, interleaved: bool = False, dq=None, dk=None, workspace=None, stream=None):
+    """(dq, dk, dq_weight, dk_weight) of qk_norm_rope at its inputs, from what
+    reaches its outputs; the weights' gradients are float32 [D] (norm=False:
+    None).  dq may be dq_out, dk may be dk_out."""
+    import torch
+    args = _rotation_args(q, k, positions, freqs, q_weight, k_weight, eps, norm, interleaved)
+    _, n, qh, kvh, d = args[:5]
+    _same_kind("q", q, (("dq_out", dq_out, q.shape), ("dk_out", dk_out, k.shape), ("dq", dq, q.shape), ("dk", dk, k.shape)))
+    heads = (("q", q), ("k", k), ("dq_out", dq_out), ("dk_out", dk_out), ("dq", dq), ("dk", dk))
+    flat = (("positions", positions), ("freqs", freqs), ("q_weight", q_weight), ("k_weight", k_weight), ("workspace", workspace))
+    dev = _heads_device(heads, flat)
+    if not _here(dev, stream):
+        return _elsewhere(dev, stream, heads + flat, lambda: qk_norm_rope_grad(
+            dq_out, dk_out, q, k, positions, freqs, q_weight, k_weight, eps, norm, interleaved, dq, dk, workspace))
+    dq = _out_tensor("dq", dq, q.shape, q.dtype, q)
+    dk = _out_tensor("dk", dk, k.shape, q.dtype, q)
+    dqw = dkw = ws = None
+    wb = 0
+    if norm:
+        dqw, dkw = q.new_empty(d, dtype=torch.float32), q.new_empty(d, dtype=torch.float32)
+        ws, wb = _workspace("cq_qk_norm_rope_grad_workspace", (n, qh, kvh, d), workspace, q)
+    _check("cq_qk_norm_rope_grad", lib().cq_qk_norm_rope_grad(
+        _heads(dq_out), _heads(dk_out), _heads(q), _heads(k), *args, _heads(dq), _heads(dk), _opt(dqw), _opt(dkw), _opt(ws), wb,
+        _raw_stream(dev)))
+    return dq, dk, dqw, dkw
+
+
+def _attention_args(q, k, v, sequences, q_starts, k_starts, k_lens, scale):
+    """(Sequences, dtype code, q_heads, kv_heads, head_dim, scale) of an
+    attention call, checked."""
+    code = _dtype_code("q", q)
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q and k must be [rows, heads, head_dim]")
+    rows_q, qh, d = q.shape
+    rows_k, kvh, _ = k.shape
+    _same_kind("q", q, (("k", k, (rows_k, kvh, d)), ("v", v, (rows_k, kvh, d))))
+    n = sequences
+    for name, t, more in (("q_starts", q_starts, 1), ("k_lens", k_lens, 0), ("k_starts", k_starts, 0 if k_lens is not None else 1)):
+        if t is None:
+            continue
+        if t.dim() != 1 or t.numel() < more:
+            raise ValueError(f"{name} must be [sequences{' + 1' if more else ''}]")
+        if n is None:
+            n = t.numel() - more
+        elif t.numel() != n + more:
+            raise ValueError(f"{name} must hold {n + more} values for {n} sequences, got {t.numel()}")
+    n = 1 if n is None else n
+    bytes_ = {_index_bytes(name, t) for name, t in (("q_starts", q_starts), ("k_starts", k_starts), ("k_lens", k_lens))
+              if t is not None}
+    if len(bytes_) > 1:
+        raise TypeError("q_starts, k_starts and k_lens must have one dtype")
+    seqs = Sequences(n, rows_q, rows_k, _opt(q_starts), _opt(k_starts), _opt(k_lens), bytes_.pop() if bytes_ else 4)
+    return seqs, code, qh, kvh, d, 1.0 / math.sqrt(max(d, 1)) if scale is None else scale
+
+
+def attention(q, k, v, sequences=None, q_starts=None, k_starts=None, k_lens=None, causal: bool = True, scale=None, out=None,
+              lse=None, workspace=None, stream=None):
+    """(out, lse): attention of queries [rows_q, q_heads, D] over keys and values
+    [rows_k, kv_heads, D] (q_heads a multiple of kv_heads; strided heads allowed), out
+    of q's shape, lse float32 [rows_q, q_heads].  Sequences, int32 or int64 on the
+    device: q_starts and k_starts [n + 1] for a packed batch; neither for
+    `sequences` (1) equal parts; k_lens [n] for keys that are the first of their
+    part, or from k_starts [n] on, as in a cache.  With causal the last query of a
+    sequence sees all its keys.  scale: 1 / sqrt(D) by default.  Rows of no
+    sequence are zeros (lse 0), or left as they are where out or lse is given."""
+    import torch
+    seqs, code, qh, kvh, d, scale = _attention_args(q, k, v, sequences, q_starts, k_starts, k_lens, scale)
+    _same_kind("q", q, (("out", out, q.shape),))
+    heads = (("q", q), ("k", k), ("v", v), ("out", out))
+    flat = (("q_starts", q_starts), ("k_starts", k_starts), ("k_lens", k_lens), ("lse", lse), ("workspace", workspace))
+    dev = _heads_device(heads, flat)
+    if not _here(dev, stream):
+        return _elsewhere(dev, stream, heads + flat, lambda: attention(
+            q, k, v, sequences, q_starts, k_starts, k_lens, causal, scale, out, lse, workspace))
+    new = torch.empty if q_starts is None else torch.zeros  # starts may leave rows out
+    out = new(q.shape, dtype=q.dtype, device=q.device) if out is None else out
+    if lse is None:
+        lse = new(q.shape[:2], dtype=torch.float32, device=q.device)
+    else:
+        _out_tensor("lse", lse, q.shape[:2], torch.float32, q)
+    sp = ctypes.byref(seqs)
+    ws, wb = _workspace("cq_attention_workspace", (sp, code, qh, kvh, d), workspace, q)
+    _check("cq_attention", lib().cq_attention(
+        _heads(q), _heads(k), _heads(v), code, sp, qh, kvh, d, int(bool(causal)), scale, _heads(out), lse.data_ptr(), _opt(ws), wb,
+        _raw_stream(dev)))
+    return out, lse
+
+
+def attention_grad(dout, q, k, v, out, lse, sequences=None, q_starts=None, k_starts=None, k_lens=None, causal: bool = True,
+                   scale=None, dq=None, dk=None, dv=None, workspace=None, stream=None):
+    """(dq, dk, dv) of attention at its inputs, its out and its lse, from what
+    reaches out (dout, of out's shape).  Every key row may belong to one
+    sequence only.  Rows of no sequence are zeros, or left as they are in
+    tensors that are given."""
+    import torch
+    seqs, code, qh, kvh, d, scale = _attention_args(q, k, v, sequences, q_starts, k_starts, k_lens, scale)
+    _same_kind("q", q, (("dout", dout, q.shape), ("out", out, q.shape), ("dq", dq, q.shape), ("dk", dk, k.shape),
+                        ("dv", dv, k.shape)))
+    if lse.dtype != torch.float32 or lse.shape != q.shape[:2]:
+        raise ValueError(f"lse must be float32 {tuple(q.shape[:2])}, got {lse.dtype} {tuple(lse.shape)}")
+    heads = (("q", q), ("k", k), ("v", v), ("dout", dout), ("out", out), ("dq", dq), ("dk", dk), ("dv", dv))
+    flat = (("q_starts", q_starts), ("k_starts", k_starts), ("k_lens", k_lens), ("lse", lse), ("workspace", workspace))
+    dev = _heads_device(heads, flat)
+    if not _here(dev, stream):
+        return _elsewhere(dev, stream, heads + flat, lambda: attention_grad(
+            dout, q, k, v, out, lse, sequences, q_starts, k_starts, k_lens, causal, scale, dq, dk, dv, workspace))
+    new_q = torch.empty if q_starts is None else torch.zeros
+    new_k = torch.empty if k_starts is None and k_lens is None else torch.zeros
+    dq = new_q(q.shape, dtype=q.dtype, device=q.device) if dq is None else dq
+    dk = new_k(k.shape, dtype=q.dtype, device=q.device) if dk is None else dk
+    dv = new_k(k.shape, dtype=q.dtype, device=q.device) if dv is None else dv
+    sp = ctypes.byref(seqs)
+    ws, wb = _workspace("cq_attention_grad_workspace", (sp, code, qh, kvh, d), workspace, q)
+    _check("cq_attention_grad", lib().cq_attention_grad(
+        _heads(dout), _heads(q), _heads(k), _heads(v), _heads(out), lse.data_ptr(), code, sp, qh, kvh, d, int(bool(causal)), scale,
+        _heads(dq), _heads(dk), _heads(dv), _opt(ws), wb, _raw_stream(dev)))
+    return dq, dk, dv
+
+
+def _logit_rows(name, t, shape):
+    """Row stride of logits [*shape, vocab]: contiguous, or a matrix whose rows are."""
+    if t.dim() < 1 or tuple(t.shape[:-1]) != tuple(shape):
+        raise ValueError(f"{name} must be [*{tuple(shape)}, vocab], got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return t.shape[-1]
+    if t.dim() != 2 or t.stride(1) != 1 or t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name} must be contiguous, or a matrix of contiguous rows")
+    return t.stride(0)
+
+
+def _logits_device(logits, named) -> int:
+    if logits.get_device() < 0:
+        raise ValueError("logits must be a CUDA tensor")
+    dev = _device(named)
+    if dev >= 0 and dev != logits.get_device():
+        raise ValueError(f"logits are on device {logits.get_device()}, the other tensors on {dev}")
+    return logits.get_device()
+
+
+def token_logprobs(logits, tokens, scale: float = 1.0, top: int = 0, stream=None):
+    """TokenLogprobs(logprob, entropy, lse, top, top_logprob) of logits [..., vocab]
+    (float32 or bfloat16) times scale, one over a temperature: log probability
+    of tokens [...] (0 for a token outside the vocabulary), entropy and log of
+    the sum, float32 [...], and with top > 0 the most probable tokens, int64
+    [..., top], equal ones by lower index, with their log probabilities."""
+    import torch
+    code, tb = _dtype_code("logits", logits), _token_bytes(tokens)
+    stride = _logit_rows("logits", logits, tokens.shape)
+    dev = _logits_device(logits, (("tokens", tokens),))
+    if not _here(dev, stream):
+        return _elsewhere(dev, stream, (("logits", logits), ("tokens", tokens)), lambda: token_logprobs(logits, tokens, scale, top))
+    rows, vocab = tokens.numel(), logits.shape[-1]
+    logprob, entropy, lse = torch.empty((3, *tokens.shape), dtype=torch.float32, device=logits.device).unbind(0)
+    ids = lps = None
+    if top > 0:
+        ids = torch.empty((*tokens.shape, top), dtype=torch.int64, device=logits.device)
+        lps = torch.empty((*tokens.shape, top), dtype=torch.float32, device=logits.device)
+    _check("cq_token_logprobs", lib().cq_token_logprobs(
+        logits.data_ptr(), code, rows, vocab, stride, scale, tokens.data_ptr(), tb, logprob.data_ptr(), entropy.data_ptr(),
+        lse.data_ptr(), top, _opt(ids), _opt(lps), _raw_stream(dev)))
+    return TokenLogprobs(logprob, entropy, lse, ids, lps)
+
+
+def token_logprobs_grad(logits, tokens, lse, dlogprob, dentropy=None, entropy=None, scale: float = 1.0, dlogits=None,
+                        stream=None):
+    """Gradient of token_logprobs with respect to the logits, from its lse
+    (and entropy, with dentropy) and what reaches logprob and entropy, float32 of
+    tokens' shape.  Of logits' dtype and shape; dlogits may be logits."""
+    import torch
+    code, tb = _dtype_code("logits", logits), _token_bytes(tokens)
+    stride = _logit_rows("logits", logits, tokens.shape)
+    if dentropy is not None and entropy is None:
+        raise ValueError("dentropy needs entropy")
+    named = (("tokens", tokens), ("lse", lse), ("dlogprob", dlogprob), ("dentropy", dentropy), ("entropy", entropy))
+    for name, t in named[1:]:
+        if t is not None and (t.dtype != torch.float32 or t.shape != tokens.shape):
+            raise ValueError(f"{name} must be float32 {tuple(tokens.shape)}, got {t.dtype} {tuple(t.shape)}")
+    if dlogits is not None and (dlogits.dtype != logits.dtype or dlogits.shape != logits.shape
+                                or dlogits.get_device() != logits.get_device()):
+        raise ValueError(f"dlogits must be {logits.dtype} {tuple(logits.shape)} on logits' device")
+    out_stride = logits.shape[-1] if dlogits is None else _logit_rows("dlogits", dlogits, tokens.shape)
+    dev = _logits_device(logits, named)
+    if not _here(dev, stream):
+        return _elsewhere(dev, stream, named + (("logits", logits), ("dlogits", dlogits)), lambda: token_logprobs_grad(
+            logits, tokens, lse, dlogprob, dentropy, entropy, scale, dlogits))
+    if dlogits is None:
+        dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    _check("cq_token_logprobs_grad", lib().cq_token_logprobs_grad(
+        logits.data_ptr(), code, tokens.numel(), logits.shape[-1], stride, scale, tokens.data_ptr(), tb, lse.data_ptr(),
+        dlogprob.data_ptr(), _opt(dentropy), _opt(entropy), dlogits.data_ptr(), out_stride, _raw_stream(dev)))
+    return dlogits

@@ -20,7 +20,7 @@ OUT = os.path.join(PKG, "libcq.so")
 BUILD = os.path.join(PKG, "_build")
 
 SOURCES = ["libcq_host.cpp", "quantize.hip", "dequantize.hip", "matvec.hip", "matvec_rot.hip", "upload.hip", "gemm.hip", "repack.hip", "groups.hip", "noalloc.hip",
-           "embed.hip", "norm.hip", "gemm_q8.hip"]
+           "embed.hip", "norm.hip", "gemm_q8.hip", "rotate.hip", "attention.hip", "attention_grad.hip", "logprobs.hip"]
 
 ARCH = "gfx950"
 COMMON = ["-O3", "-fPIC", "-std=c++17", "-Wall", f"-I{os.path.join(ROOT, 'include')}"]

@@ -1,0 +1,448 @@
+// Attention over packed sequences, causal or not, with grouped heads, for
+// prompts and for tokens that read a cache.
+//
+// For query i of a sequence and a query head of the group of key head h:
+//   x_j = scale q . k_j,  p_j = exp(x_j - lse),  lse = log sum_j exp(x_j),  out = sum_j p_j v_j
+// over the keys j it sees.  One pass over the keys: the running maximum and
+// sum of each row stay in the lane that owns the row.
+//
+// Rows of a block are the queries of a whole group, (query, head) pairs with
+// the head running fastest, so that a group's heads share each tile of keys.
+// Scores are formed transposed, k . q^T, on the 32x32 matrix instructions: a
+// lane then holds 16 scores of one row, the row's statistics need one
+// exchange between the two halves of a wave, and the probabilities already
+// lie as the second product's operand (out^T = v^T . p^T), which reads v by
+// columns (attention.h).  Probabilities are rounded to bf16 for bf16 inputs
+// (their sum is taken in float32 before): an error of half a step of each
+// probability, as large as that of the stored output itself.
+#include <type_traits>
+
+#include "attention.h"
+
+namespace cq {
+namespace {
+
+// A row's running state, in powers of two: scores times scale * log2(e).
+struct RowState {
+  float top;  // the reference that probabilities are taken against
+  float sum;  // of this lane's half of the keys
+};
+
+// Probabilities of SUBS x 32 scores against the running reference, which moves
+// up (and the output with it) only when a row's maximum passes it by 2^8:
+// below that the sums stay far from float32's limits, and the output's
+// rescaling is left out for most tiles.
+template <int SUBS, int DT>
+__device__ __forceinline__ void soften(f32_x16 (&s)[SUBS], float factor, RowState& st, f32_x16 (&o)[DT]) {
+  float top = s[0][0];
+#pragma unroll
+  for (int sub = 0; sub < SUBS; ++sub)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) top = fmaxf(top, s[sub][r]);
+  float a, b;
+  both_halves(top, &a, &b);
+  top = fmaxf(a, b) * factor;
+  if (__any(top > st.top + 8.0f)) {
+    const float up = fmaxf(top, st.top);
+    const float shrink = st.top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(st.top - up);
+    st.sum *= shrink;
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) o[dt][r] *= shrink;
+    st.top = up;
+  }
+  const float ref = st.top == -INFINITY ? 0.0f : st.top;  // no key seen yet: every score is -inf
+#pragma unroll
+  for (int sub = 0; sub < SUBS; ++sub)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[sub][r], factor, -ref));
+      s[sub][r] = p;
+      st.sum += p;
+    }
+}
+
+constexpr int kWaves = 4;        // of a block
+constexpr int kBlockRows = kWaves * kRows;
+constexpr int kTileKeys = 64;
+
+// Prompts: a block of 4 waves owns 128 rows and walks over tiles of 64 keys,
+// the next tile on its way into the other half of shared memory meanwhile.
+template <bool BF16, int DP>
+__global__ void __launch_bounds__(kWaves * kWave, BF16 ? 2 : 1) attention_kernel(AttnArgs a, int64_t tiles) {
+  typedef Tile<BF16, DP, kTileKeys> T;
+  constexpr int kElem = T::kElem, kSubs = kTileKeys / 32, kDepth = DP / 16, kDt = DP / 32;
+  __shared__ __attribute__((aligned(16))) uint8_t k_tile0[T::kBytes], k_tile1[T::kBytes], v_tile0[T::kBytes], v_tile1[T::kBytes];
+  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), half = lane >> 5;
+  const int group = a.q_heads / a.kv_heads;
+  // Blocks in turn take the key heads, so that one head's keys stay in few
+  // XCDs' caches, and the last rows of a sequence, which see most, come first.
+  const int kv_head = static_cast<int>(blockIdx.x % a.kv_heads);
+  SeqRows seq;
+  int64_t tile;
+  if (!find_tile(a.seqs, tiles - 1 - blockIdx.x / a.kv_heads,
+                 [&](const SeqRows& s) { return (s.nq * group + kBlockRows - 1) / kBlockRows; }, &seq, &tile))
+    return;
+  const int64_t rows = seq.nq * group, r0 = tile * kBlockRows + wave * kRows;
+  const Row row = row_of(r0 + (lane & 31), rows, group);
+  const int64_t block_last = row_of(min(tile * kBlockRows + kBlockRows, rows) - 1, rows, group).query;
+  const int64_t wave_last = row_of(min(r0 + kRows, rows) - 1, rows, group).query;
+  const int64_t block_keys = keys_seen(seq, block_last, a.causal);
+  const int64_t wave_keys = r0 < rows ? keys_seen(seq, wave_last, a.causal) : 0;
+  const int64_t all_see = r0 < rows ? keys_seen(seq, row_of(r0, rows, group).query, a.causal) : 0;  // keys that every row sees
+  const int64_t seen = row.exists ? keys_seen(seq, row.query, a.causal) : 0;
+
+  const uint8_t* const q_row =
+      row.exists ? row_data(a.q, seq.q0 + row.query, static_cast<int64_t>(kv_head) * group + row.head, kElem) : nullptr;
+  Operand<BF16> q[kDepth];
+  load_row_operands<BF16, DP>(q_row, a.head_dim, half, q);
+
+  const TileLoader<BF16, DP, kTileKeys, kWaves> k_load(wave, lane, a.k.row, a.head_dim), v_load(wave, lane, a.v.row, a.head_dim);
+  const RowOperand<BF16, DP> by_row(lane);
+  const ColumnOperand<BF16, DP> by_column(lane);
+  const uint8_t* const k0 = row_data(a.k, seq.k0, kv_head, kElem);
+  const uint8_t* const v0 = row_data(a.v, seq.k0, kv_head, kElem);
+  const float factor = a.scale * kLog2e;
+
+  RowState st{-INFINITY, 0.0f};
+  f32_x16 o[kDt];
+#pragma unroll
+  for (int dt = 0; dt < kDt; ++dt)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) o[dt][r] = 0.0f;
+
+  const int64_t n_tiles = (block_keys + kTileKeys - 1) / kTileKeys;
+  auto issue = [&](int64_t t, uint8_t* kt, uint8_t* vt) __attribute__((always_inline)) {
+    const int64_t key = t * kTileKeys;
+    k_load.issue(k0 + key * a.k.row * kElem, seq.nk - key, kt);
+    v_load.issue(v0 + key * a.v.row * kElem, seq.nk - key, vt);
+  };
+  auto compute = [&](int64_t t, const uint8_t* kt, const uint8_t* vt) __attribute__((always_inline)) {
+    const int64_t key = t * kTileKeys;
+    if (key >= wave_keys) return;
+    f32_x16 s[kSubs];
+#pragma unroll
+    for (int sub = 0; sub < kSubs; ++sub)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) s[sub][r] = 0.0f;
+#pragma unroll
+    for (int kk = 0; kk < kDepth; ++kk)
+#pragma unroll
+      for (int sub = 0; sub < kSubs; ++sub) multiply<BF16>(s[sub], by_row.load(kt, sub, kk), q[kk]);
+    if (key + kTileKeys > all_see) {
+      const int left = static_cast<int>(min(seen - key, int64_t(kTileKeys))) - 4 * half;
+#pragma unroll
+      for (int sub = 0; sub < kSubs; ++sub)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (32 * sub + result_row(r) >= left) s[sub][r] = -INFINITY;
+    }
+    soften<kSubs, kDt>(s, factor, st, o);
+#pragma unroll
+    for (int step = 0; step < 2 * kSubs; ++step) {
+      const Operand<BF16> p = result_operand<BF16>(s[step / 2], step % 2);
+#pragma unroll
+      for (int dt = 0; dt < kDt; ++dt) multiply<BF16>(o[dt], by_column.load(vt, step, dt), p);
+    }
+  };
+
+  if (n_tiles > 0) issue(0, k_tile0, v_tile0);
+  for (int64_t t = 0; t < n_tiles; t += 2) {
+    wait_loads<0>();
+    __syncthreads();
+    if (t + 1 < n_tiles) issue(t + 1, k_tile1, v_tile1);
+    compute(t, k_tile0, v_tile0);
+    if (t + 1 >= n_tiles) break;
+    wait_loads<0>();
+    __syncthreads();
+    if (t + 2 < n_tiles) issue(t + 2, k_tile0, v_tile0);
+    compute(t + 1, k_tile1, v_tile1);
+  }
+
+  float sum_a, sum_b;
+  both_halves(st.sum, &sum_a, &sum_b);
+  const float sum = sum_a + sum_b;
+  const int64_t out_row = seq.q0 + row.query, out_head = static_cast<int64_t>(kv_head) * group + row.head;
+  store_columns<BF16, DP>(o, sum == 0.0f ? 0.0f : 1.0f / sum, row.exists ? row_data(a.out, out_row, out_head, kElem) : nullptr,
+                          a.head_dim, half);
+  if (a.lse && row.exists && half == 0)
+    a.lse[out_row * a.q_heads + out_head] = sum == 0.0f ? -INFINITY : (st.top + __builtin_log2f(sum)) * kLn2;
+}
+
+// ---- Few rows: the keys split over waves and blocks -------------------------------
+
+// Keys of split s of a tile of rows whose last row sees `keys`.
+__device__ __forceinline__ int64_t split_keys(int64_t keys, int splits, int step) {
+  const int64_t each = (keys + splits - 1) / splits;
+  return (each + step - 1) / step * step;
+}
+
+template <bool BF16, int DP>
+struct SplitShape {
+  // Two tiles of keys and of values per wave: 16 KiB (bf16, 128) to 64.
+  static constexpr int kTile = Tile<BF16, DP, 32>::kBytes;
+  static constexpr int kWaves = 4 * kTile * 4 > 131072 ? 2 : 4;
+  static constexpr int kStep = 32 * kWaves;  // keys that a block takes in one turn
+  static constexpr int kPitch = DP + 4;      // floats per row of a wave's output in shared memory
+};
+
+// A block takes one tile of up to 32 rows and one split of its keys; each wave
+// walks over its own tiles of 32 keys, which only it loads and reads, so no
+// wave waits for another before the end.
+template <bool BF16, int DP>
+__global__ void __launch_bounds__((SplitShape<BF16, DP>::kWaves * kWave), 1) attention_split_kernel(AttnArgs a) {
+  typedef SplitShape<BF16, DP> Shape;
+  typedef Tile<BF16, DP, 32> T;
+  constexpr int kElem = T::kElem, kDepth = DP / 16, kDt = DP / 32, W = Shape::kWaves;
+  __shared__ __attribute__((aligned(16))) uint8_t tiles[W][4 * T::kBytes];
+  __shared__ float tops[W][kRows], sums[W][kRows];
+  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), half = lane >> 5;
+  const int group = a.q_heads / a.kv_heads;
+  const int split = static_cast<int>(blockIdx.x % a.splits);
+  const int kv_head = static_cast<int>(blockIdx.x / a.splits % a.kv_heads);
+  SeqRows seq;
+  int64_t tile;
+  if (!find_tile(a.seqs, blockIdx.x / a.splits / a.kv_heads,
+                 [&](const SeqRows& s) { return (s.nq * group + kRows - 1) / kRows; }, &seq, &tile))
+    return;
+  const int64_t rows = seq.nq * group, r0 = tile * kRows;
+  const int64_t keys = keys_seen(seq, row_of(min(r0 + kRows, rows) - 1, rows, group).query, a.causal);
+  const int64_t each = split_keys(keys, a.splits, Shape::kStep);
+  const int64_t begin = split * each, end = min(begin + each, keys);
+  if (split > 0 && begin >= keys) return;  // the first split writes rows that see nothing
+  const Row row = row_of(r0 + (lane & 31), rows, group);
+  const int64_t all_see = keys_seen(seq, row_of(r0, rows, group).query, a.causal);
+  const int64_t seen = row.exists ? keys_seen(seq, row.query, a.causal) : 0;
+  const int64_t out_row = seq.q0 + row.query, out_head = static_cast<int64_t>(kv_head) * group + row.head;
+
+  Operand<BF16> q[kDepth];
+  load_row_operands<BF16, DP>(row.exists ? row_data(a.q, out_row, out_head, kElem) : nullptr, a.head_dim, half, q);
+  const TileLoader<BF16, DP, 32, 1> k_load(0, lane, a.k.row, a.head_dim), v_load(0, lane, a.v.row, a.head_dim);
+  constexpr int kPending = 2 * TileLoader<BF16, DP, 32, 1>::kLoads;  // of one turn
+  const RowOperand<BF16, DP> by_row(lane);
+  const ColumnOperand<BF16, DP> by_column(lane);
+  const uint8_t* const k0 = row_data(a.k, seq.k0, kv_head, kElem);
+  const uint8_t* const v0 = row_data(a.v, seq.k0, kv_head, kElem);
+  const float factor = a.scale * kLog2e;
+
+  RowState st{-INFINITY, 0.0f};
+  f32_x16 o[kDt];
+#pragma unroll
+  for (int dt = 0; dt < kDt; ++dt)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) o[dt][r] = 0.0f;
+
+  uint8_t* const mine = tiles[wave];
+  auto issue = [&](int64_t key, uint8_t* kt) __attribute__((always_inline)) {
+    k_load.issue(k0 + key * a.k.row * kElem, seq.nk - key, kt);
+    v_load.issue(v0 + key * a.v.row * kElem, seq.nk - key, kt + T::kBytes);
+  };
+  auto compute = [&](int64_t key, const uint8_t* kt) __attribute__((always_inline)) {
+    f32_x16 s[1];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) s[0][r] = 0.0f;
+#pragma unroll
+    for (int kk = 0; kk < kDepth; ++kk) multiply<BF16>(s[0], by_row.load(kt, 0, kk), q[kk]);
+    if (key + 32 > min(all_see, end)) {
+      const int left = static_cast<int>(min(min(seen, end) - key, int64_t(32))) - 4 * half;
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        if (result_row(r) >= left) s[0][r] = -INFINITY;
+    }
+    soften<1, kDt>(s, factor, st, o);
+#pragma unroll
+    for (int step = 0; step < 2; ++step) {
+      const Operand<BF16> p = result_operand<BF16>(s[0], step);
+      Operand<BF16> rest;
+      if constexpr (BF16) {
+        // What the rounding left: memory bounds this kernel, the second product is free.
+        f32_x16 left;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) left[8 * step + j] = s[0][8 * step + j] - static_cast<float>(p[j]);
+        rest = result_operand<BF16>(left, step);
+      }
+#pragma unroll
+      for (int dt = 0; dt < kDt; ++dt) {
+        const Operand<BF16> v = by_column.load(kt + T::kBytes, step, dt);
+        multiply<BF16>(o[dt], v, p);
+        if constexpr (BF16) multiply<BF16>(o[dt], v, rest);
+      }
+    }
+  };
+
+  int64_t key = begin + 32 * wave;
+  if (key < end) issue(key, mine);
+  for (int turn = 0; key < end; key += Shape::kStep, turn ^= 1) {
+    uint8_t* const now = mine + turn * 2 * T::kBytes;
+    if (key + Shape::kStep < end) {
+      wait_lds_writes();  // the last turn's reads of the other half are done
+      issue(key + Shape::kStep, mine + (turn ^ 1) * 2 * T::kBytes);
+      wait_loads<kPending>();
+    } else {
+      wait_loads<0>();
+    }
+    compute(key, now);
+  }
+
+  // The waves' rows together: each leaves its output, maximum and sum.
+  float* const part = reinterpret_cast<float*>(mine);
+  static_assert(kRows * Shape::kPitch * 4 <= 4 * T::kBytes, "a wave's output fits its tiles");
+  float sum_a, sum_b;
+  both_halves(st.sum, &sum_a, &sum_b);
+  const float sum = sum_a + sum_b;
+  wait_lds_writes();  // this wave's reads of its tiles are done, too
+#pragma unroll
+  for (int dt = 0; dt < kDt; ++dt) {
+    uint4 w[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      w[g] = pack_piece<false>(reinterpret_cast<const float*>(&o[dt]) + 4 * g);
+      *reinterpret_cast<uint4*>(part + (lane & 31) * Shape::kPitch + 32 * dt + 8 * g + 4 * half) = w[g];
+    }
+    hold_until_lds_written(w);
+  }
+  if (half == 0) {
+    tops[wave][lane] = st.top;
+    sums[wave][lane] = sum;
+    wait_lds_writes();
+    hold_value(st.top);
+    hold_value(sum);
+  }
+  __syncthreads();
+  constexpr int kQuads = DP / 4;
+  for (int i = threadIdx.x; i < kRows * kQuads; i += W * kWave) {
+    const int r = i / kQuads, d = i % kQuads * 4;
+    const Row w = row_of(r0 + r, rows, group);
+    if (!w.exists || d >= a.head_dim) continue;
+    float top = tops[0][r];
+#pragma unroll
+    for (int j = 1; j < W; ++j) top = fmaxf(top, tops[j][r]);
+    float total = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      const float share = tops[j][r] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(tops[j][r] - top);
+      total = __builtin_fmaf(share, sums[j][r], total);
+      const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(tiles[j]) + r * Shape::kPitch + d);
+      acc[0] = __builtin_fmaf(share, v.x, acc[0]);
+      acc[1] = __builtin_fmaf(share, v.y, acc[1]);
+      acc[2] = __builtin_fmaf(share, v.z, acc[2]);
+      acc[3] = __builtin_fmaf(share, v.w, acc[3]);
+    }
+    const int64_t at = (seq.q0 + w.query) * a.q_heads + static_cast<int64_t>(kv_head) * group + w.head;
+    if (a.splits > 1) {
+      // A sequence of rows: [split][row and head][head_dim + 4], output, maximum, sum.
+      float* const p = a.ws + (split * a.seqs.rows_q * a.q_heads + at) * (a.head_dim + 4);
+      *reinterpret_cast<float4*>(p + d) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      if (d == 0) *reinterpret_cast<float2*>(p + a.head_dim) = make_float2(top, total);
+    } else {
+      const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+      uint8_t* const out = row_data(a.out, seq.q0 + w.query, static_cast<int64_t>(kv_head) * group + w.head, kElem) + d * kElem;
+      if constexpr (BF16)
+        *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
+      else
+        *reinterpret_cast<float4*>(out) = make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
+      if (a.lse && d == 0) a.lse[at] = total == 0.0f ? -INFINITY : (top + __builtin_log2f(total)) * kLn2;
+    }
+  }
+}
+
+// Joins the splits' shares of the rows of a tile.
+template <bool BF16, int DP>
+__global__ void __launch_bounds__(256) attention_join_kernel(AttnArgs a) {
+  constexpr int kElem = BF16 ? 2 : 4;
+  const int group = a.q_heads / a.kv_heads;
+  const int kv_head = static_cast<int>(blockIdx.x % a.kv_heads);
+  SeqRows seq;
+  int64_t tile;
+  if (!find_tile(a.seqs, blockIdx.x / a.kv_heads, [&](const SeqRows& s) { return (s.nq * group + kRows - 1) / kRows; }, &seq, &tile))
+    return;
+  const int64_t rows = seq.nq * group, r0 = tile * kRows;
+  const int64_t keys = keys_seen(seq, row_of(min(r0 + kRows, rows) - 1, rows, group).query, a.causal);
+  const int64_t each = split_keys(keys, a.splits, SplitShape<BF16, DP>::kStep);
+  const int live = keys <= each ? 1 : static_cast<int>((keys + each - 1) / each);
+  constexpr int kQuads = DP / 4;  // lanes of a row
+  for (int r = threadIdx.x / kQuads; r < kRows; r += 256 / kQuads) {
+    const Row w = row_of(r0 + r, rows, group);
+    const int d = threadIdx.x % kQuads * 4;
+    if (!w.exists || d >= a.head_dim) continue;
+    const int64_t head = static_cast<int64_t>(kv_head) * group + w.head, at = (seq.q0 + w.query) * a.q_heads + head;
+    const int64_t pitch = a.head_dim + 4, step = a.seqs.rows_q * a.q_heads * pitch;
+    const float* const p = a.ws + at * pitch;
+    float top = -INFINITY;
+    for (int s = 0; s < live; ++s) top = fmaxf(top, p[s * step + a.head_dim]);
+    float total = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s = 0; s < live; ++s) {
+      const float2 ms = *reinterpret_cast<const float2*>(p + s * step + a.head_dim);
+      const float4 v = *reinterpret_cast<const float4*>(p + s * step + d);
+      const float share = ms.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ms.x - top);
+      total = __builtin_fmaf(share, ms.y, total);
+      acc[0] = __builtin_fmaf(share, v.x, acc[0]);
+      acc[1] = __builtin_fmaf(share, v.y, acc[1]);
+      acc[2] = __builtin_fmaf(share, v.z, acc[2]);
+      acc[3] = __builtin_fmaf(share, v.w, acc[3]);
+    }
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+    uint8_t* const out = row_data(a.out, seq.q0 + w.query, head, kElem) + d * kElem;
+    if constexpr (BF16)
+      *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
+    else
+      *reinterpret_cast<float4*>(out) = make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
+    if (a.lse && d == 0) a.lse[at] = total == 0.0f ? -INFINITY : (top + __builtin_log2f(total)) * kLn2;
+  }
+}
+
+// Few rows per sequence take the split kernel.
+bool few_rows(const AttnSeqs& s, int group) { return s.rows_q * group <= kRows * s.n_seq; }
+
+int split_step(int head_dim, bool bf16) {
+  if (bf16) return head_dim <= 64 ? SplitShape<true, 64>::kStep : SplitShape<true, 128>::kStep;
+  return head_dim <= 64 ? SplitShape<false, 64>::kStep : SplitShape<false, 128>::kStep;
+}
+
+template <bool BF16, int DP>
+hipError_t launch_at(const AttnArgs& a, hipStream_t stream) {
+  const int group = a.q_heads / a.kv_heads;
+  if (!few_rows(a.seqs, group)) {
+    const int64_t tiles = q_tiles(a.seqs, group, kBlockRows);
+    attention_kernel<BF16, DP><<<dim3(static_cast<uint32_t>(tiles * a.kv_heads)), dim3(kWaves * kWave), 0, stream>>>(a, tiles);
+    return hipGetLastError();
+  }
+  const int64_t units = q_tiles(a.seqs, group, kRows) * a.kv_heads;
+  attention_split_kernel<BF16, DP>
+      <<<dim3(static_cast<uint32_t>(units * a.splits)), dim3(SplitShape<BF16, DP>::kWaves * kWave), 0, stream>>>(a);
+  if (a.splits > 1) attention_join_kernel<BF16, DP><<<dim3(static_cast<uint32_t>(units)), dim3(256), 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int attention_splits(const AttnSeqs& s, int q_heads, int kv_heads, int head_dim, bool bf16) {
+  const int group = q_heads / kv_heads;
+  if (!few_rows(s, group)) return 1;
+  const int64_t units = q_tiles(s, group, kRows) * kv_heads;
+  const int64_t longest = s.k_starts ? s.rows_k : s.rows_k / s.n_seq, step = split_step(head_dim, bf16);
+  const int64_t fill = ceil_div(4 * kCus, units);
+  const int64_t want = fill < ceil_div(longest, 8 * step) ? ceil_div(longest, 8 * step) : fill;
+  const int64_t most = ceil_div(longest, 2 * step);
+  const int64_t splits = want < most ? want : most;
+  return static_cast<int>(splits < 1 ? 1 : splits > 64 ? 64 : splits);
+}
+
+int64_t attention_workspace(const AttnSeqs& s, int q_heads, int kv_heads, int head_dim, bool bf16) {
+  const int splits = attention_splits(s, q_heads, kv_heads, head_dim, bf16);
+  return splits > 1 ? splits * s.rows_q * q_heads * (head_dim + 4) * 4 : 0;
+}
+
+int64_t attention_blocks(const AttnSeqs& s, int q_heads, int kv_heads, int head_dim, bool bf16) {
+  const int group = q_heads / kv_heads;
+  if (!few_rows(s, group)) return q_tiles(s, group, kBlockRows) * kv_heads;
+  return q_tiles(s, group, kRows) * kv_heads * attention_splits(s, q_heads, kv_heads, head_dim, bf16);
+}
+
+hipError_t launch_attention(const AttnArgs& a, bool bf16, hipStream_t s) {
+  if (bf16) return a.head_dim <= 64 ? launch_at<true, 64>(a, s) : launch_at<true, 128>(a, s);
+  return a.head_dim <= 64 ? launch_at<false, 64>(a, s) : launch_at<false, 128>(a, s);
+}
+
+}  // namespace cq

@@ -721,4 +721,105 @@ int64_t gemm_q8_threads(int64_t n_out, int64_t k, int64_t batch, int group_size)
 hipError_t launch_gemm_q8_empty(const GemmQ8Args& a, hipStream_t stream);  // k = 0: zeros
 hipError_t launch_gemm_q8(const GemmQ8Args& a, int sbits, int group_size, Q8Levels lv, float* ws, hipStream_t stream);
 
+// Compute units of an MI355X, for choices that sizes alone have to fix (a
+// workspace's size is asked for without a device).
+constexpr int kCus = 256;
+
+// ---- Attention (attention.hip, attention_grad.hip) --------------------------------------
+
+// Sequences of a packed batch (see cq_attention): offsets on the device, null
+// for equal parts.
+struct AttnSeqs {
+  const void* q_starts;
+  const void* k_starts;
+  const void* k_lens;
+  int index_bytes;
+  int64_t n_seq, rows_q, rows_k;
+};
+// Value d of head h of row i: data[(i * row + h * head + d) values].
+struct HeadRows {
+  uint8_t* data;
+  int64_t row, head;  // in values
+};
+constexpr int kAttnMaxHead = 128;
+constexpr int64_t kAttnMaxRowStride = int64_t(1) << 22;  // values: 32-bit offsets within a tile of 64 rows
+struct AttnArgs {
+  AttnSeqs seqs;
+  HeadRows q, k, v, out;
+  float* lse;  // [rows_q][q_heads]
+  int q_heads, kv_heads, head_dim;
+  int causal;
+  float scale;
+  // Gradient: inputs dout and out, outputs dq, dk, dv.
+  HeadRows dout, dq, dk, dv;
+  // Workspace.  Forward in splits: per split, row and head the unnormalised
+  // output, its maximum (in powers of two) and sum.  Gradient: per head and
+  // row the log of the sum in powers of two, and sum(dout * out).
+  float* ws;
+  int splits;
+};
+// Splits of the keys (1: none, no workspace) and workspace bytes of a call.
+int attention_splits(const AttnSeqs& s, int q_heads, int kv_heads, int head_dim, bool bf16);
+int64_t attention_workspace(const AttnSeqs& s, int q_heads, int kv_heads, int head_dim, bool bf16);
+int64_t attention_blocks(const AttnSeqs& s, int q_heads, int kv_heads, int head_dim, bool bf16);  // of 256 threads, the largest launch
+hipError_t launch_attention(const AttnArgs& a, bool bf16, hipStream_t stream);
+int64_t attention_grad_workspace(const AttnSeqs& s, int q_heads, int kv_heads, int head_dim, bool bf16);
+int64_t attention_grad_blocks(const AttnSeqs& s, int q_heads, int kv_heads, int head_dim, bool bf16);
+hipError_t launch_attention_grad(const AttnArgs& a, bool bf16, hipStream_t stream);
+
+// ---- Norm of queries and keys with the position rotation (rotate.hip) --------------------
+
+struct RotateArgs {
+  HeadRows q, k, v;            // v.data null: none
+  HeadRows q_out, k_out, v_out;  // forward outputs; gradient: q_out, k_out receive dq, dk
+  HeadRows dq, dk;             // gradient: what reaches the rotated queries and keys
+  int64_t n;
+  int q_heads, kv_heads, head_dim;
+  int norm;  // 0: rotation only
+  const void* q_weight;  // null: ones
+  const void* k_weight;
+  int w_bf16;
+  float eps;
+  const void* positions;
+  int position_bytes;
+  const float* freqs;
+  int rotary_dim;
+  int interleaved;
+  const void* slots;  // null: row i
+  int slot_bytes;
+  int64_t cache_rows;
+  float* part;  // gradient: shares of the weights' gradients, per block [2][head_dim]
+};
+int64_t rotate_blocks(int64_t n, int q_heads, int kv_heads, bool values, int head_dim);  // of 256 threads
+hipError_t launch_rotate_heads(const RotateArgs& a, bool bf16, hipStream_t stream);
+int rotate_grad_blocks(int64_t n, int q_heads, int kv_heads, int head_dim);
+hipError_t launch_rotate_heads_grad(RotateArgs a, bool bf16, float* dq_weight, float* dk_weight, float* ws, hipStream_t stream);
+
+// ---- Log probabilities of tokens (logprobs.hip) ------------------------------------------
+
+constexpr int kMaxTop = 64;
+constexpr int64_t kMaxVocab = int64_t(1) << 28;  // 32-bit offsets within a row
+struct LogprobArgs {
+  const uint8_t* logits;
+  int64_t rows, vocab, row_stride;  // row_stride in values
+  float scale;
+  const void* tokens;
+  int token_bytes;
+  float* logprob;
+  float* entropy;
+  float* lse;
+  int top;
+  int64_t* top_ids;
+  float* top_logprobs;
+  // Gradient
+  const float* dlogprob;
+  const float* dentropy;  // null: none
+  uint8_t* dlogits;
+  int64_t out_stride;
+};
+int64_t logprobs_blocks(int64_t rows, int64_t vocab, bool bf16);
+hipError_t launch_logprobs(const LogprobArgs& a, bool bf16, hipStream_t stream);
+int64_t logprobs_grad_blocks(int64_t rows, int64_t vocab, bool bf16);
+hipError_t launch_logprobs_grad(const LogprobArgs& a, bool bf16, hipStream_t stream);
+
 }  // namespace cq

@@ -1364,6 +1364,499 @@ int cq_dequant_gemm_q8(const uint8_t* packed, const uint16_t* norms, int64_t n_o
                     "8-bit product launch");
 }
 
+// ---- An attention block and a model's end ---------------------------------------
+
+namespace {
+
+constexpr int kMaxHeads = 4096;
+
+// A tensor of heads as it lies in memory, in bytes.
+struct Lattice {
+  uintptr_t at;
+  int64_t rows, heads, row, head, width;
+  uintptr_t end() const { return rows && heads ? at + (rows - 1) * row + (heads - 1) * head + width : at; }
+};
+Lattice lattice(const cq_heads* t, int64_t rows, int heads, int head_dim, int dtype) {
+  const int64_t b = dtype_bytes(dtype);
+  if (!t || !t->data) return Lattice{0, 0, 0, 0, 0, 0};
+  return Lattice{reinterpret_cast<uintptr_t>(t->data), rows, heads, t->row_stride * b, t->head_stride * b, head_dim * b};
+}
+
+// Whether two tensors share memory.  Parts of one projection's output
+// interleave: with equal row strides they are apart if their columns are, with
+// equal head strides too if their places within a head's stride are.
+bool share(const Lattice& a, const Lattice& b) {
+  if (a.at >= b.end() || b.at >= a.end()) return false;
+  const int64_t wa = (a.heads - 1) * a.head + a.width, wb = (b.heads - 1) * b.head + b.width;
+  auto apart = [](int64_t period, int64_t shift, int64_t na, int64_t nb) {
+    const int64_t d = ((shift % period) + period) % period;
+    return d >= na && d + nb <= period;
+  };
+  const int64_t shift = static_cast<int64_t>(b.at - a.at);
+  if (a.rows > 1 && b.rows > 1 && a.row == b.row && a.row > 0 && apart(a.row, shift, wa, wb)) return false;
+  if (a.row == b.row && a.head == b.head && a.head > 0 && a.row % a.head == 0 && apart(a.head, shift, a.width, b.width)) return false;
+  return true;
+}
+bool share_flat(const Lattice& a, const void* p, int64_t bytes) {
+  return p && bytes > 0 && a.end() > a.at && overlap(reinterpret_cast<const void*>(a.at), a.end() - a.at, p, static_cast<size_t>(bytes));
+}
+
+int check_heads(const char* name, const cq_heads* t, int64_t rows, int heads, int head_dim, int dtype, bool output) {
+  if (rows == 0) return CQ_OK;
+  if (!t || !t->data) return fail(CQ_ERR_NULL, "%s is NULL", name);
+  if (t->row_stride < 0 || t->head_stride < 0) return fail(CQ_ERR_ARG, "%s has a negative stride", name);
+  const int64_t unit = 16 / dtype_bytes(dtype);
+  if (!aligned(t->data, 16) || t->row_stride % unit || t->head_stride % unit)
+    return fail(CQ_ERR_ALIGN, "%s needs 16-byte alignment of its data, rows and heads", name);
+  if (t->row_stride > cq::kAttnMaxRowStride) return fail(CQ_ERR_UNSUPPORTED, "%s: row_stride is at most 2^22", name);
+  int64_t span;
+  if (__builtin_mul_overflow(t->head_stride, static_cast<int64_t>(heads), &span) || span > (int64_t(1) << 58))
+    return fail(CQ_ERR_UNSUPPORTED, "%s: head_stride is too large", name);
+  if (!output) return CQ_OK;
+  const int64_t rs = t->row_stride, hs = t->head_stride;
+  const bool by_rows = (heads == 1 || hs >= head_dim) && (rows == 1 || rs >= (heads - 1) * hs + head_dim);
+  const bool by_heads = (rows == 1 || rs >= head_dim) && (heads == 1 || hs >= (rows - 1) * rs + head_dim);
+  if (!by_rows && !by_heads) return fail(CQ_ERR_ARG, "%s has rows or heads that share memory", name);
+  return CQ_OK;
+}
+
+cq::HeadRows head_rows(const cq_heads* t) {
+  if (!t) return cq::HeadRows{nullptr, 0, 0};
+  return cq::HeadRows{static_cast<uint8_t*>(t->data), t->row_stride, t->head_stride};
+}
+
+bool same_heads(const cq_heads* a, const cq_heads* b) {
+  return a && b && a->data == b->data && a->row_stride == b->row_stride && a->head_stride == b->head_stride;
+}
+
+int check_head_counts(int dtype, int q_heads, int kv_heads, int head_dim, int most) {
+  if (!is_dtype(dtype)) return fail(CQ_ERR_ARG, "unknown dtype %d", dtype);
+  if (q_heads < 1 || kv_heads < 1 || head_dim < 1) return fail(CQ_ERR_ARG, "q_heads, kv_heads and head_dim must be positive");
+  if (q_heads > kMaxHeads || kv_heads > kMaxHeads) return fail(CQ_ERR_UNSUPPORTED, "at most %d heads", kMaxHeads);
+  if (head_dim % 8 || head_dim > most)
+    return fail(CQ_ERR_UNSUPPORTED, "head_dim=%d: multiples of 8 up to %d", head_dim, most);
+  return CQ_OK;
+}
+
+constexpr int kRotateMaxHead = 256;
+
+// The arguments that both directions of cq_qk_norm_rope share.
+int check_rotate(int dtype, int64_t n, int q_heads, int kv_heads, int head_dim, int norm, const void* q_weight,
+                 const void* k_weight, int weight_dtype, float eps, const void* positions, int position_bytes,
+                 const float* freqs, int rotary_dim, int interleaved, cq::RotateArgs* a) {
+  if (int rc = check_head_counts(dtype, q_heads, kv_heads, head_dim, kRotateMaxHead)) return rc;
+  if (n < 0) return fail(CQ_ERR_ARG, "negative size");
+  if (n > kMaxIndex) return fail(CQ_ERR_UNSUPPORTED, "n must be at most 2^31 - 2");
+  if ((norm != 0 && norm != 1) || (interleaved != 0 && interleaved != 1)) return fail(CQ_ERR_ARG, "norm and interleaved are 0 or 1");
+  if (!norm && (q_weight || k_weight)) return fail(CQ_ERR_ARG, "weights belong to the norm");
+  if ((q_weight || k_weight) && !is_dtype(weight_dtype)) return fail(CQ_ERR_ARG, "unknown weight_dtype %d", weight_dtype);
+  if (norm && (!(eps >= 0.0f) || !std::isfinite(eps))) return fail(CQ_ERR_ARG, "eps must be finite and not negative");
+  if (rotary_dim < 0 || rotary_dim % 2 || rotary_dim > head_dim)
+    return fail(CQ_ERR_ARG, "rotary_dim=%d must be even and at most head_dim", rotary_dim);
+  if ((q_weight || k_weight) && (!aligned(q_weight, dtype_bytes(weight_dtype)) || !aligned(k_weight, dtype_bytes(weight_dtype))))
+    return fail(CQ_ERR_ALIGN, "weights need their type's alignment");
+  if (rotary_dim) {
+    if (position_bytes != 4 && position_bytes != 8) return fail(CQ_ERR_ARG, "position_bytes=%d must be 4 or 8", position_bytes);
+    if (n && (!positions || !freqs)) return fail(CQ_ERR_NULL, "positions/freqs is NULL");
+    if (!aligned(positions, position_bytes) || !aligned(freqs, 4))
+      return fail(CQ_ERR_ALIGN, "positions need %d-byte, freqs 4-byte alignment", position_bytes);
+  }
+  a->n = n;
+  a->q_heads = q_heads;
+  a->kv_heads = kv_heads;
+  a->head_dim = head_dim;
+  a->norm = norm;
+  a->q_weight = q_weight;
+  a->k_weight = k_weight;
+  a->w_bf16 = weight_dtype == CQ_BF16;
+  a->eps = eps;
+  a->positions = positions;
+  a->position_bytes = position_bytes;
+  a->freqs = freqs;
+  a->rotary_dim = rotary_dim;
+  a->interleaved = interleaved;
+  return CQ_OK;
+}
+
+// What check_rotate's pointers span, against an output.
+bool meets_rotate_inputs(const Lattice& out, const cq::RotateArgs& a) {
+  const int64_t w = a.head_dim * (a.w_bf16 ? 2 : 4);
+  return share_flat(out, a.q_weight, w) || share_flat(out, a.k_weight, w) ||
+         (a.rotary_dim && (share_flat(out, a.positions, a.n * a.position_bytes) || share_flat(out, a.freqs, a.rotary_dim * 2)));
+}
+
+int check_seqs(const cq_sequences* q, cq::AttnSeqs* out) {
+  if (!q) return fail(CQ_ERR_NULL, "seqs is NULL");
+  if (q->n_seq < 0 || q->rows_q < 0 || q->rows_k < 0) return fail(CQ_ERR_ARG, "negative size");
+  if (q->n_seq > kMaxIndex || q->rows_q > kMaxIndex || q->rows_k > kMaxIndex)
+    return fail(CQ_ERR_UNSUPPORTED, "sequences and rows must be at most 2^31 - 2");
+  const bool any = q->q_starts || q->k_starts || q->k_lens;
+  if (any && q->index_bytes != 4 && q->index_bytes != 8) return fail(CQ_ERR_ARG, "index_bytes=%d must be 4 or 8", q->index_bytes);
+  if (any && (!aligned(q->q_starts, q->index_bytes) || !aligned(q->k_starts, q->index_bytes) || !aligned(q->k_lens, q->index_bytes)))
+    return fail(CQ_ERR_ALIGN, "starts and lengths need %d-byte alignment", q->index_bytes);
+  if (q->n_seq && !q->q_starts && q->rows_q % q->n_seq) return fail(CQ_ERR_ARG, "rows_q is not a multiple of n_seq");
+  if (q->n_seq && !q->k_starts && q->rows_k % q->n_seq) return fail(CQ_ERR_ARG, "rows_k is not a multiple of n_seq");
+  *out = cq::AttnSeqs{q->q_starts, q->k_starts, q->k_lens, q->index_bytes, q->n_seq, q->rows_q, q->rows_k};
+  return CQ_OK;
+}
+bool meets_seqs(const void* p, int64_t bytes, const cq_sequences* q) {
+  return meets_any(p, bytes,
+                   {{q->q_starts, (q->n_seq + 1) * q->index_bytes},
+                    {q->k_starts, (q->n_seq + (q->k_lens ? 0 : 1)) * q->index_bytes},
+                    {q->k_lens, q->n_seq * q->index_bytes}});
+}
+bool lattice_meets_seqs(const Lattice& a, const cq_sequences* q) {
+  return meets_seqs(reinterpret_cast<const void*>(a.at), a.end() - a.at, q);
+}
+
+int check_attention(int dtype, const cq_sequences* seqs, int q_heads, int kv_heads, int head_dim, cq::AttnSeqs* s) {
+  if (int rc = check_head_counts(dtype, q_heads, kv_heads, head_dim, cq::kAttnMaxHead)) return rc;
+  if (q_heads % kv_heads) return fail(CQ_ERR_ARG, "q_heads=%d is not a multiple of kv_heads=%d", q_heads, kv_heads);
+  return check_seqs(seqs, s);
+}
+
+int attention_args(int causal, float scale, int q_heads, int kv_heads, int head_dim, cq::AttnArgs* a) {
+  if (causal != 0 && causal != 1) return fail(CQ_ERR_ARG, "causal is 0 or 1");
+  if (!(scale > 0.0f) || !std::isfinite(scale)) return fail(CQ_ERR_ARG, "scale must be finite and positive");
+  a->q_heads = q_heads;
+  a->kv_heads = kv_heads;
+  a->head_dim = head_dim;
+  a->causal = causal;
+  a->scale = scale;
+  return CQ_OK;
+}
+
+int check_logits(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t row_stride, float scale) {
+  if (!is_dtype(dtype)) return fail(CQ_ERR_ARG, "unknown dtype %d", dtype);
+  if (rows < 0 || vocab < 0) return fail(CQ_ERR_ARG, "negative size");
+  if (row_stride < vocab) return fail(CQ_ERR_ARG, "row_stride is below vocab");
+  if (!(scale > 0.0f) || !std::isfinite(scale)) return fail(CQ_ERR_ARG, "scale must be finite and positive");
+  if (rows > kMaxIndex || vocab > cq::kMaxVocab || !fits(rows, row_stride, 4))
+    return fail(CQ_ERR_UNSUPPORTED, "rows must be at most 2^31 - 2, vocab 2^28");
+  if (rows && vocab && !logits) return fail(CQ_ERR_NULL, "logits is NULL");
+  if (!aligned(logits, 16)) return fail(CQ_ERR_ALIGN, "logits need 16-byte alignment");
+  return CQ_OK;
+}
+
+}  // namespace
+
+int cq_qk_norm_rope(const cq_heads* q, const cq_heads* k, const cq_heads* v, int dtype, int64_t n, int q_heads,
+                    int kv_heads, int head_dim, int norm, const void* q_weight, const void* k_weight, int weight_dtype,
+                    float eps, const void* positions, int position_bytes, const float* freqs, int rotary_dim,
+                    int interleaved, const cq_heads* q_out, const cq_heads* k_out, const cq_heads* v_out,
+                    const void* slots, int slot_bytes, int64_t cache_rows, void* stream) {
+  g_last_error[0] = 0;
+  cq::RotateArgs a{};
+  int rc;
+  if ((rc = check_rotate(dtype, n, q_heads, kv_heads, head_dim, norm, q_weight, k_weight, weight_dtype, eps, positions,
+                         position_bytes, freqs, rotary_dim, interleaved, &a)))
+    return rc;
+  if (slots) {
+    if (slot_bytes != 4 && slot_bytes != 8) return fail(CQ_ERR_ARG, "slot_bytes=%d must be 4 or 8", slot_bytes);
+    if (cache_rows < 0) return fail(CQ_ERR_ARG, "negative size");
+    if (cache_rows > kMaxIndex) return fail(CQ_ERR_UNSUPPORTED, "cache_rows must be at most 2^31 - 2");
+    if (!aligned(slots, slot_bytes)) return fail(CQ_ERR_ALIGN, "slots need %d-byte alignment", slot_bytes);
+  }
+  if (!v != !v_out) return fail(CQ_ERR_NULL, "v and v_out come together");
+  if (n == 0) return CQ_OK;
+  const int64_t out_rows = slots ? cache_rows : n;
+  if ((rc = check_heads("q", q, n, q_heads, head_dim, dtype, false)) || (rc = check_heads("k", k, n, kv_heads, head_dim, dtype, false)) ||
+      (rc = check_heads("q_out", q_out, n, q_heads, head_dim, dtype, true)) ||
+      (rc = check_heads("k_out", k_out, out_rows, kv_heads, head_dim, dtype, true)))
+    return rc;
+  if (v && ((rc = check_heads("v", v, n, kv_heads, head_dim, dtype, false)) ||
+            (rc = check_heads("v_out", v_out, out_rows, kv_heads, head_dim, dtype, true))))
+    return rc;
+  if (cq::rotate_blocks(n, q_heads, kv_heads, v != nullptr, head_dim) > cq::most_blocks(256))
+    return fail(CQ_ERR_UNSUPPORTED, "n is past this call's grid");
+  const Lattice in[3] = {lattice(q, n, q_heads, head_dim, dtype), lattice(k, n, kv_heads, head_dim, dtype),
+                         lattice(v, n, kv_heads, head_dim, dtype)};
+  const Lattice out[3] = {lattice(q_out, n, q_heads, head_dim, dtype), lattice(k_out, out_rows, kv_heads, head_dim, dtype),
+                          lattice(v_out, out_rows, kv_heads, head_dim, dtype)};
+  const bool in_place[3] = {same_heads(q, q_out), !slots && same_heads(k, k_out), !slots && same_heads(v, v_out)};
+  for (int i = 0; i < 3; ++i) {
+    bool bad = meets_rotate_inputs(out[i], a) || share_flat(out[i], slots, n * slot_bytes);
+    for (int j = 0; j < 3; ++j) {
+      bad = bad || (!(i == j && in_place[i]) && share(out[i], in[j]));
+      bad = bad || (i < j && share(out[i], out[j]));
+    }
+    if (bad) return fail(CQ_ERR_ARG, "input and output buffers overlap");
+  }
+  a.q = head_rows(q);
+  a.k = head_rows(k);
+  a.v = head_rows(v);
+  a.q_out = head_rows(q_out);
+  a.k_out = head_rows(k_out);
+  a.v_out = head_rows(v_out);
+  a.slots = slots;
+  a.slot_bytes = slot_bytes;
+  a.cache_rows = cache_rows;
+  return hip_status(cq::launch_rotate_heads(a, dtype == CQ_BF16, static_cast<hipStream_t>(stream)), "rotation launch");
+}
+
+int cq_qk_norm_rope_grad_workspace(int64_t n, int q_heads, int kv_heads, int head_dim, int64_t* bytes) {
+  g_last_error[0] = 0;
+  if (int rc = check_head_counts(CQ_F32, q_heads, kv_heads, head_dim, kRotateMaxHead)) return rc;
+  if (n < 0) return fail(CQ_ERR_ARG, "negative size");
+  if (n > kMaxIndex) return fail(CQ_ERR_UNSUPPORTED, "n must be at most 2^31 - 2");
+  if (!bytes) return fail(CQ_ERR_NULL, "bytes is NULL");
+  *bytes = n ? int64_t(8) * head_dim * cq::rotate_grad_blocks(n, q_heads, kv_heads, head_dim) : 0;
+  return CQ_OK;
+}
+
+int cq_qk_norm_rope_grad(const cq_heads* dq_out, const cq_heads* dk_out, const cq_heads* q, const cq_heads* k, int dtype,
+                         int64_t n, int q_heads, int kv_heads, int head_dim, int norm, const void* q_weight,
+                         const void* k_weight, int weight_dtype, float eps, const void* positions, int position_bytes,
+                         const float* freqs, int rotary_dim, int interleaved, const cq_heads* dq, const cq_heads* dk,
+                         float* dq_weight, float* dk_weight, void* workspace, int64_t workspace_bytes, void* stream) {
+  g_last_error[0] = 0;
+  cq::RotateArgs a{};
+  int rc;
+  if ((rc = check_rotate(dtype, n, q_heads, kv_heads, head_dim, norm, q_weight, k_weight, weight_dtype, eps, positions,
+                         position_bytes, freqs, rotary_dim, interleaved, &a)))
+    return rc;
+  if (!norm && (dq_weight || dk_weight)) return fail(CQ_ERR_ARG, "weights belong to the norm");
+  if (!aligned(dq_weight, 4) || !aligned(dk_weight, 4)) return fail(CQ_ERR_ALIGN, "weights' gradients need 4-byte alignment");
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int64_t wbytes = int64_t(4) * head_dim;
+  if (meets_any(dq_weight, wbytes, {{dk_weight, wbytes}})) return fail(CQ_ERR_ARG, "input and output buffers overlap");
+  if (n == 0) {
+    if (dq_weight && (rc = hip_status(cq::launch_zero(dq_weight, head_dim, s), "zero launch"))) return rc;
+    return dk_weight ? hip_status(cq::launch_zero(dk_weight, head_dim, s), "zero launch") : CQ_OK;
+  }
+  if ((rc = check_heads("dq_out", dq_out, n, q_heads, head_dim, dtype, false)) ||
+      (rc = check_heads("dk_out", dk_out, n, kv_heads, head_dim, dtype, false)) ||
+      (norm && ((rc = check_heads("q", q, n, q_heads, head_dim, dtype, false)) ||
+                (rc = check_heads("k", k, n, kv_heads, head_dim, dtype, false)))) ||
+      (rc = check_heads("dq", dq, n, q_heads, head_dim, dtype, true)) ||
+      (rc = check_heads("dk", dk, n, kv_heads, head_dim, dtype, true)))
+    return rc;
+  const bool weights = dq_weight || dk_weight;
+  const int64_t need = weights ? int64_t(8) * head_dim * cq::rotate_grad_blocks(n, q_heads, kv_heads, head_dim) : 0;
+  if ((rc = check_workspace(workspace, workspace_bytes, need))) return rc;
+  const Region ws{need ? workspace : nullptr, need};
+  if (!norm) q = k = nullptr;
+  const Lattice in[4] = {lattice(dq_out, n, q_heads, head_dim, dtype), lattice(dk_out, n, kv_heads, head_dim, dtype),
+                         lattice(q, n, q_heads, head_dim, dtype), lattice(k, n, kv_heads, head_dim, dtype)};
+  const Lattice out[2] = {lattice(dq, n, q_heads, head_dim, dtype), lattice(dk, n, kv_heads, head_dim, dtype)};
+  const bool in_place[2] = {same_heads(dq, dq_out), same_heads(dk, dk_out)};
+  bool bad = share(out[0], out[1]);
+  for (int i = 0; i < 2; ++i) {
+    bad = bad || meets_rotate_inputs(out[i], a) || share_flat(out[i], ws.p, ws.bytes) || share_flat(out[i], dq_weight, wbytes) ||
+          share_flat(out[i], dk_weight, wbytes);
+    for (int j = 0; j < 4; ++j) bad = bad || (!(i == j && in_place[i]) && share(out[i], in[j]));
+  }
+  const int64_t w = head_dim * dtype_bytes(weight_dtype == CQ_BF16 ? CQ_BF16 : CQ_F32);
+  for (const Region& r : {Region{dq_weight, wbytes}, Region{dk_weight, wbytes}, ws}) {
+    for (const Lattice& l : in) bad = bad || share_flat(l, r.p, r.bytes);
+    bad = bad || meets_any(r.p, r.bytes, {{q_weight, w}, {k_weight, w}, {rotary_dim ? positions : nullptr, n * position_bytes},
+                                          {rotary_dim ? freqs : nullptr, int64_t(2) * rotary_dim}});
+  }
+  bad = bad || meets_any(ws.p, ws.bytes, {{dq_weight, wbytes}, {dk_weight, wbytes}});
+  if (bad) return fail(CQ_ERR_ARG, "input and output buffers overlap");
+  a.dq = head_rows(dq_out);
+  a.dk = head_rows(dk_out);
+  a.q = head_rows(q);
+  a.k = head_rows(k);
+  a.q_out = head_rows(dq);
+  a.k_out = head_rows(dk);
+  return hip_status(cq::launch_rotate_heads_grad(a, dtype == CQ_BF16, dq_weight, dk_weight, static_cast<float*>(workspace), s),
+                    "rotation gradient launch");
+}
+
+int cq_attention_workspace(const cq_sequences* seqs, int dtype, int q_heads, int kv_heads, int head_dim, int64_t* bytes) {
+  g_last_error[0] = 0;
+  cq::AttnSeqs s;
+  if (int rc = check_attention(dtype, seqs, q_heads, kv_heads, head_dim, &s)) return rc;
+  if (!bytes) return fail(CQ_ERR_NULL, "bytes is NULL");
+  *bytes = s.n_seq && s.rows_q ? cq::attention_workspace(s, q_heads, kv_heads, head_dim, dtype == CQ_BF16) : 0;
+  return CQ_OK;
+}
+
+int cq_attention(const cq_heads* q, const cq_heads* k, const cq_heads* v, int dtype, const cq_sequences* seqs, int q_heads,
+                 int kv_heads, int head_dim, int causal, float scale, const cq_heads* out, float* lse, void* workspace,
+                 int64_t workspace_bytes, void* stream) {
+  g_last_error[0] = 0;
+  cq::AttnArgs a{};
+  int rc;
+  if ((rc = check_attention(dtype, seqs, q_heads, kv_heads, head_dim, &a.seqs)) ||
+      (rc = attention_args(causal, scale, q_heads, kv_heads, head_dim, &a)))
+    return rc;
+  const int64_t rows_q = seqs->rows_q, rows_k = seqs->rows_k;
+  if (seqs->n_seq == 0 || rows_q == 0) return CQ_OK;
+  if ((rc = check_heads("q", q, rows_q, q_heads, head_dim, dtype, false)) ||
+      (rc = check_heads("k", k, rows_k, kv_heads, head_dim, dtype, false)) ||
+      (rc = check_heads("v", v, rows_k, kv_heads, head_dim, dtype, false)) ||
+      (rc = check_heads("out", out, rows_q, q_heads, head_dim, dtype, true)))
+    return rc;
+  if (!aligned(lse, 4)) return fail(CQ_ERR_ALIGN, "lse needs 4-byte alignment");
+  const bool bf16 = dtype == CQ_BF16;
+  const int64_t need = cq::attention_workspace(a.seqs, q_heads, kv_heads, head_dim, bf16);
+  if ((rc = check_workspace(workspace, workspace_bytes, need))) return rc;
+  if (cq::attention_blocks(a.seqs, q_heads, kv_heads, head_dim, bf16) > cq::most_blocks(256))
+    return fail(CQ_ERR_UNSUPPORTED, "rows and heads are past this call's grid");
+  const Region ws{need ? workspace : nullptr, need};
+  const int64_t lse_bytes = rows_q * q_heads * 4;
+  const Lattice in[3] = {lattice(q, rows_q, q_heads, head_dim, dtype), lattice(k, rows_k, kv_heads, head_dim, dtype),
+                         lattice(v, rows_k, kv_heads, head_dim, dtype)};
+  const Lattice o = lattice(out, rows_q, q_heads, head_dim, dtype);
+  bool bad = share_flat(o, lse, lse_bytes) || share_flat(o, ws.p, ws.bytes) || lattice_meets_seqs(o, seqs) || meets_seqs(lse, lse_bytes, seqs) ||
+             meets_seqs(ws.p, ws.bytes, seqs) || meets_any(lse, lse_bytes, {ws});
+  for (const Lattice& l : in) bad = bad || share(o, l) || share_flat(l, lse, lse_bytes) || share_flat(l, ws.p, ws.bytes);
+  if (bad) return fail(CQ_ERR_ARG, "input and output buffers overlap");
+  a.q = head_rows(q);
+  a.k = head_rows(k);
+  a.v = head_rows(v);
+  a.out = head_rows(out);
+  a.lse = lse;
+  a.ws = static_cast<float*>(workspace);
+  a.splits = cq::attention_splits(a.seqs, q_heads, kv_heads, head_dim, bf16);
+  return hip_status(cq::launch_attention(a, bf16, static_cast<hipStream_t>(stream)), "attention launch");
+}
+
+int cq_attention_grad_workspace(const cq_sequences* seqs, int dtype, int q_heads, int kv_heads, int head_dim, int64_t* bytes) {
+  g_last_error[0] = 0;
+  cq::AttnSeqs s;
+  if (int rc = check_attention(dtype, seqs, q_heads, kv_heads, head_dim, &s)) return rc;
+  if (!bytes) return fail(CQ_ERR_NULL, "bytes is NULL");
+  *bytes = s.n_seq ? cq::attention_grad_workspace(s, q_heads, kv_heads, head_dim, dtype == CQ_BF16) : 0;
+  return CQ_OK;
+}
+
+int cq_attention_grad(const cq_heads* dout, const cq_heads* q, const cq_heads* k, const cq_heads* v, const cq_heads* out,
+                      const float* lse, int dtype, const cq_sequences* seqs, int q_heads, int kv_heads, int head_dim,
+                      int causal, float scale, const cq_heads* dq, const cq_heads* dk, const cq_heads* dv, void* workspace,
+                      int64_t workspace_bytes, void* stream) {
+  g_last_error[0] = 0;
+  cq::AttnArgs a{};
+  int rc;
+  if ((rc = check_attention(dtype, seqs, q_heads, kv_heads, head_dim, &a.seqs)) ||
+      (rc = attention_args(causal, scale, q_heads, kv_heads, head_dim, &a)))
+    return rc;
+  const int64_t rows_q = seqs->rows_q, rows_k = seqs->rows_k;
+  if (seqs->n_seq == 0 || (rows_q == 0 && rows_k == 0)) return CQ_OK;
+  if ((rc = check_heads("dout", dout, rows_q, q_heads, head_dim, dtype, false)) ||
+      (rc = check_heads("q", q, rows_q, q_heads, head_dim, dtype, false)) ||
+      (rc = check_heads("k", k, rows_k, kv_heads, head_dim, dtype, false)) ||
+      (rc = check_heads("v", v, rows_k, kv_heads, head_dim, dtype, false)) ||
+      (rc = check_heads("out", out, rows_q, q_heads, head_dim, dtype, false)) ||
+      (rc = check_heads("dq", dq, rows_q, q_heads, head_dim, dtype, true)) ||
+      (rc = check_heads("dk", dk, rows_k, kv_heads, head_dim, dtype, true)) ||
+      (rc = check_heads("dv", dv, rows_k, kv_heads, head_dim, dtype, true)))
+    return rc;
+  if (rows_q && !lse) return fail(CQ_ERR_NULL, "lse is NULL");
+  if (!aligned(lse, 4)) return fail(CQ_ERR_ALIGN, "lse needs 4-byte alignment");
+  const bool bf16 = dtype == CQ_BF16;
+  const int64_t need = cq::attention_grad_workspace(a.seqs, q_heads, kv_heads, head_dim, bf16);
+  if ((rc = check_workspace(workspace, workspace_bytes, need))) return rc;
+  if (cq::attention_grad_blocks(a.seqs, q_heads, kv_heads, head_dim, bf16) > cq::most_blocks(256))
+    return fail(CQ_ERR_UNSUPPORTED, "rows and heads are past this call's grid");
+  const Region ws{need ? workspace : nullptr, need};
+  const int64_t lse_bytes = rows_q * q_heads * 4;
+  const Lattice in[5] = {lattice(dout, rows_q, q_heads, head_dim, dtype), lattice(q, rows_q, q_heads, head_dim, dtype),
+                         lattice(k, rows_k, kv_heads, head_dim, dtype), lattice(v, rows_k, kv_heads, head_dim, dtype),
+                         lattice(out, rows_q, q_heads, head_dim, dtype)};
+  const Lattice grads[3] = {lattice(dq, rows_q, q_heads, head_dim, dtype), lattice(dk, rows_k, kv_heads, head_dim, dtype),
+                            lattice(dv, rows_k, kv_heads, head_dim, dtype)};
+  bool bad = share(grads[0], grads[1]) || share(grads[0], grads[2]) || share(grads[1], grads[2]) || meets_seqs(ws.p, ws.bytes, seqs) ||
+             meets_any(ws.p, ws.bytes, {{lse, lse_bytes}});
+  for (const Lattice& g : grads) {
+    bad = bad || share_flat(g, lse, lse_bytes) || share_flat(g, ws.p, ws.bytes) || lattice_meets_seqs(g, seqs);
+    for (const Lattice& l : in) bad = bad || share(g, l);
+  }
+  for (const Lattice& l : in) bad = bad || share_flat(l, ws.p, ws.bytes);
+  if (bad) return fail(CQ_ERR_ARG, "input and output buffers overlap");
+  a.dout = head_rows(dout);
+  a.q = head_rows(q);
+  a.k = head_rows(k);
+  a.v = head_rows(v);
+  a.out = head_rows(out);
+  a.lse = const_cast<float*>(lse);
+  a.dq = head_rows(dq);
+  a.dk = head_rows(dk);
+  a.dv = head_rows(dv);
+  a.ws = static_cast<float*>(workspace);
+  return hip_status(cq::launch_attention_grad(a, bf16, static_cast<hipStream_t>(stream)), "attention gradient launch");
+}
+
+int cq_token_logprobs(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t row_stride, float scale,
+                      const void* tokens, int token_bytes, float* logprob, float* entropy, float* lse, int top,
+                      int64_t* top_ids, float* top_logprobs, void* stream) {
+  g_last_error[0] = 0;
+  if (int rc = check_logits(logits, dtype, rows, vocab, row_stride, scale)) return rc;
+  if (top < 0 || top > vocab) return fail(CQ_ERR_ARG, "top=%d is not within the vocabulary", top);
+  if (top > cq::kMaxTop) return fail(CQ_ERR_UNSUPPORTED, "top=%d: at most %d", top, cq::kMaxTop);
+  if (logprob && token_bytes != 4 && token_bytes != 8) return fail(CQ_ERR_ARG, "token_bytes=%d must be 4 or 8", token_bytes);
+  if (rows == 0) return CQ_OK;
+  if (logprob && !tokens) return fail(CQ_ERR_NULL, "tokens is NULL");
+  if (top && (!top_ids || !top_logprobs)) return fail(CQ_ERR_NULL, "top_ids/top_logprobs is NULL");
+  if ((logprob && !aligned(tokens, token_bytes)) || !aligned(logprob, 4) || !aligned(entropy, 4) || !aligned(lse, 4) ||
+      (top && (!aligned(top_ids, 8) || !aligned(top_logprobs, 4))))
+    return fail(CQ_ERR_ALIGN, "tokens and outputs need their types' alignment");
+  if (cq::logprobs_blocks(rows, vocab, dtype == CQ_BF16) > cq::most_blocks(256))
+    return fail(CQ_ERR_UNSUPPORTED, "rows * vocab is past this call's grid");
+  const Region in[2] = {{logits, ((rows - 1) * row_stride + vocab) * dtype_bytes(dtype)}, {logprob ? tokens : nullptr, rows * token_bytes}};
+  const Region out[5] = {{logprob, rows * 4}, {entropy, rows * 4}, {lse, rows * 4}, {top ? top_ids : nullptr, rows * top * 8},
+                         {top ? top_logprobs : nullptr, rows * top * 4}};
+  for (int i = 0; i < 5; ++i)
+    for (int j = 0; j < 5; ++j)
+      if (meets_any(out[i].p, out[i].bytes, {in[0], in[1], i < j ? out[j] : Region{nullptr, 0}}))
+        return fail(CQ_ERR_ARG, "input and output buffers overlap");
+  cq::LogprobArgs a{};
+  a.logits = static_cast<const uint8_t*>(logits);
+  a.rows = rows;
+  a.vocab = vocab;
+  a.row_stride = row_stride;
+  a.scale = scale;
+  a.tokens = tokens;
+  a.token_bytes = token_bytes;
+  a.logprob = logprob;
+  a.entropy = entropy;
+  a.lse = lse;
+  a.top = top;
+  a.top_ids = top_ids;
+  a.top_logprobs = top_logprobs;
+  return hip_status(cq::launch_logprobs(a, dtype == CQ_BF16, static_cast<hipStream_t>(stream)), "log probability launch");
+}
+
+int cq_token_logprobs_grad(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t row_stride, float scale,
+                           const void* tokens, int token_bytes, const float* lse, const float* dlogprob, const float* dentropy,
+                           const float* entropy, void* dlogits, int64_t out_stride, void* stream) {
+  g_last_error[0] = 0;
+  if (int rc = check_logits(logits, dtype, rows, vocab, row_stride, scale)) return rc;
+  if (token_bytes != 4 && token_bytes != 8) return fail(CQ_ERR_ARG, "token_bytes=%d must be 4 or 8", token_bytes);
+  if (out_stride < vocab || !fits(rows, out_stride, 4)) return fail(CQ_ERR_ARG, "out_stride is below vocab or too large");
+  if (rows == 0 || vocab == 0) return CQ_OK;
+  if (!tokens || !lse || !dlogprob || !dlogits) return fail(CQ_ERR_NULL, "tokens/lse/dlogprob/dlogits is NULL");
+  if (dentropy && !entropy) return fail(CQ_ERR_NULL, "entropy is NULL");
+  if (!aligned(tokens, token_bytes) || !aligned(lse, 4) || !aligned(dlogprob, 4) || !aligned(dentropy, 4) || !aligned(entropy, 4) ||
+      !aligned(dlogits, 16))
+    return fail(CQ_ERR_ALIGN, "dlogits needs 16-byte alignment, the others their types'");
+  if (cq::logprobs_grad_blocks(rows, vocab, dtype == CQ_BF16) > cq::most_blocks(256))
+    return fail(CQ_ERR_UNSUPPORTED, "rows * vocab is past this call's grid");
+  const int64_t b = dtype_bytes(dtype);
+  const bool in_place = dlogits == logits && out_stride == row_stride;
+  if (meets_any(dlogits, ((rows - 1) * out_stride + vocab) * b,
+                {{in_place ? nullptr : logits, ((rows - 1) * row_stride + vocab) * b}, {tokens, rows * token_bytes}, {lse, rows * 4},
+                 {dlogprob, rows * 4}, {dentropy, rows * 4}, {dentropy ? entropy : nullptr, rows * 4}}))
+    return fail(CQ_ERR_ARG, "input and output buffers overlap");
+  cq::LogprobArgs a{};
+  a.logits = static_cast<const uint8_t*>(logits);
+  a.rows = rows;
+  a.vocab = vocab;
+  a.row_stride = row_stride;
+  a.scale = scale;
+  a.tokens = tokens;
+  a.token_bytes = token_bytes;
+  a.lse = const_cast<float*>(lse);
+  a.entropy = const_cast<float*>(entropy);
+  a.dlogprob = dlogprob;
+  a.dentropy = dentropy;
+  a.dlogits = static_cast<uint8_t*>(dlogits);
+  a.out_stride = out_stride;
+  return hip_status(cq::launch_logprobs_grad(a, dtype == CQ_BF16, static_cast<hipStream_t>(stream)), "log probability gradient launch");
+}
+
 }  // extern "C"
 
 namespace cq {
