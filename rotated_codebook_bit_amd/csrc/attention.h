@@ -203,15 +203,16 @@ struct Tile {
   }
 };
 
-// Offsets of a lane's operands in a tile; steps along the head (kk: 16 values,
-// dt: 32 values) flip chunk bits, steps along the rows are constants.
+// Offsets of a lane's operands in a tile, `base` bytes (whole tiles) in; steps
+// along the head (kk: 16 values, dt: 32 values) flip chunk bits, steps along the
+// rows are constants.
 template <bool BF16, int DP>
 struct RowOperand {
   typedef Tile<BF16, DP, 32> T;
   uint32_t at;
-  __device__ __forceinline__ explicit RowOperand(int lane) {
+  __device__ __forceinline__ explicit RowOperand(int lane, int base = 0) {
     const int row = lane & 31, chunk = (lane >> 5) * (BF16 ? 1 : 2);
-    at = row * T::kPitch + ((chunk ^ T::key(row)) << 4);
+    at = base + row * T::kPitch + ((chunk ^ T::key(row)) << 4);
   }
   // Rows sub * 32 .. + 31, values 16 kk .. 16 kk + 15.
   __device__ __forceinline__ Operand<BF16> load(const uint8_t* tile, int sub, int kk) const {
@@ -233,7 +234,7 @@ struct ColumnOperand {
   typedef Tile<BF16, DP, 32> T;
   static constexpr int kParts = BF16 ? 2 : 8;
   uint32_t at[kParts];
-  __device__ __forceinline__ explicit ColumnOperand(int lane) {
+  __device__ __forceinline__ explicit ColumnOperand(int lane, int base = 0) {
     if constexpr (BF16) {
       // A transposing read gives lane i of 16 column i of a block of 4 rows
       // by 16 columns, to whose row i / 4, columns 4 (i % 4) .. + 3 it points.
@@ -241,14 +242,14 @@ struct ColumnOperand {
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         const int row = 8 * p + 4 * (block >> 1) + (i >> 2), chunk = (block & 1) * 2 + ((i & 3) >> 1);
-        at[p] = row * T::kPitch + ((chunk ^ T::key(row)) << 4) + ((i & 1) << 3);
+        at[p] = base + row * T::kPitch + ((chunk ^ T::key(row)) << 4) + ((i & 1) << 3);
       }
     } else {
       const int col = lane & 31;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int row = 4 * (lane >> 5) + (j & 3) + 8 * (j >> 2);
-        at[j] = row * T::kPitch + (((col >> 2) ^ T::key(row)) << 4) + ((col & 3) << 2);
+        at[j] = base + row * T::kPitch + (((col >> 2) ^ T::key(row)) << 4) + ((col & 3) << 2);
       }
     }
   }
@@ -294,12 +295,12 @@ struct TileLoader {
       off[i] = byte < head_bytes ? row * row_bytes + byte : 0x80000000u;
     }
   }
-  // `first`: the first row's values; valid: rows that exist, at least 1.
+  // `first`: the first row's values; valid: rows that exist (0 or below: all zeros).
   __device__ __forceinline__ void issue(const uint8_t* first, int64_t valid, uint8_t* tile) const {
 #if defined(__HIP_DEVICE_COMPILE__)
-    const uint32_t n = valid < ROWS ? static_cast<uint32_t>(valid) : ROWS;
-    const auto src = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(first), 0,
-                                                       static_cast<int>((n - 1) * row_bytes + head_bytes), 0x00020000);
+    const uint32_t n = __builtin_amdgcn_readfirstlane(valid >= ROWS ? ROWS : valid > 0 ? static_cast<int>(valid) : 0);
+    const int bytes = __builtin_amdgcn_readfirstlane(n ? static_cast<int>((n - 1) * row_bytes + head_bytes) : 0);
+    const auto src = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(first), 0, bytes, 0x00020000);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (lds_void_ptr)(tile + 16 * ((i * WAVES + wave) * kWave)), 16,

@@ -195,7 +195,9 @@ __global__ void __launch_bounds__((SplitShape<BF16, DP>::kWaves * kWave), 1) att
   typedef SplitShape<BF16, DP> Shape;
   typedef Tile<BF16, DP, 32> T;
   constexpr int kElem = T::kElem, kDepth = DP / 16, kDt = DP / 32, W = Shape::kWaves;
-  __shared__ __attribute__((aligned(16))) uint8_t tiles[W][4 * T::kBytes];
+  // Two arrays, not one indexed by the turn: the compiler has to see that the
+  // loads under way do not meet the tile being read, or waits for them.
+  __shared__ __attribute__((aligned(16))) uint8_t tiles0[W * 2 * T::kBytes], tiles1[W * 2 * T::kBytes];
   __shared__ float tops[W][kRows], sums[W][kRows];
   const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), half = lane >> 5;
   const int group = a.q_heads / a.kv_heads;
@@ -233,7 +235,8 @@ __global__ void __launch_bounds__((SplitShape<BF16, DP>::kWaves * kWave), 1) att
 #pragma unroll
     for (int r = 0; r < 16; ++r) o[dt][r] = 0.0f;
 
-  uint8_t* const mine = tiles[wave];
+  uint8_t* const even = tiles0 + wave * 2 * T::kBytes;
+  uint8_t* const odd = tiles1 + wave * 2 * T::kBytes;
   auto issue = [&](int64_t key, uint8_t* kt) __attribute__((always_inline)) {
     k_load.issue(k0 + key * a.k.row * kElem, seq.nk - key, kt);
     v_load.issue(v0 + key * a.v.row * kElem, seq.nk - key, kt + T::kBytes);
@@ -271,27 +274,37 @@ __global__ void __launch_bounds__((SplitShape<BF16, DP>::kWaves * kWave), 1) att
     }
   };
 
-  int64_t key = begin + 32 * wave;
-  if (key < end) issue(key, mine);
-  for (int turn = 0; key < end; key += Shape::kStep, turn ^= 1) {
-    uint8_t* const now = mine + turn * 2 * T::kBytes;
+  // One turn's loads are under way while the turn before is computed.
+  auto turn = [&](int64_t key, const uint8_t* now, uint8_t* next) __attribute__((always_inline)) {
     if (key + Shape::kStep < end) {
       wait_lds_writes();  // the last turn's reads of the other half are done
-      issue(key + Shape::kStep, mine + (turn ^ 1) * 2 * T::kBytes);
+      issue(key + Shape::kStep, next);
       wait_loads<kPending>();
     } else {
       wait_loads<0>();
     }
     compute(key, now);
+  };
+  int64_t key = begin + 32 * wave;
+  if (key < end) issue(key, even);
+  while (key < end) {
+    turn(key, even, odd);
+    key += Shape::kStep;
+    if (key >= end) break;
+    turn(key, odd, even);
+    key += Shape::kStep;
   }
 
   // The waves' rows together: each leaves its output, maximum and sum.
-  float* const part = reinterpret_cast<float*>(mine);
-  static_assert(kRows * Shape::kPitch * 4 <= 4 * T::kBytes, "a wave's output fits its tiles");
+  auto part_of = [&](int w) __attribute__((always_inline)) {
+    return reinterpret_cast<float*>((w < W / 2 ? tiles0 : tiles1) + w % (W / 2) * 4 * T::kBytes);
+  };
+  static_assert(kRows * Shape::kPitch * 4 <= 4 * T::kBytes, "a wave's output fits two of its tiles");
+  float* const part = part_of(wave);
   float sum_a, sum_b;
   both_halves(st.sum, &sum_a, &sum_b);
   const float sum = sum_a + sum_b;
-  wait_lds_writes();  // this wave's reads of its tiles are done, too
+  __syncthreads();  // every wave has read its tiles
 #pragma unroll
   for (int dt = 0; dt < kDt; ++dt) {
     uint4 w[4];
@@ -323,7 +336,7 @@ __global__ void __launch_bounds__((SplitShape<BF16, DP>::kWaves * kWave), 1) att
     for (int j = 0; j < W; ++j) {
       const float share = tops[j][r] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(tops[j][r] - top);
       total = __builtin_fmaf(share, sums[j][r], total);
-      const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(tiles[j]) + r * Shape::kPitch + d);
+      const float4 v = *reinterpret_cast<const float4*>(part_of(j) + r * Shape::kPitch + d);
       acc[0] = __builtin_fmaf(share, v.x, acc[0]);
       acc[1] = __builtin_fmaf(share, v.y, acc[1]);
       acc[2] = __builtin_fmaf(share, v.z, acc[2]);
@@ -347,10 +360,13 @@ __global__ void __launch_bounds__((SplitShape<BF16, DP>::kWaves * kWave), 1) att
   }
 }
 
-// Joins the splits' shares of the rows of a tile.
+// Joins the splits' shares of the rows of a tile: a wave takes a row, lane s
+// the maximum and sum of split s, then teams of lanes of 4 values every
+// (64 / team)-th split each.
 template <bool BF16, int DP>
 __global__ void __launch_bounds__(256) attention_join_kernel(AttnArgs a) {
-  constexpr int kElem = BF16 ? 2 : 4;
+  constexpr int kElem = BF16 ? 2 : 4, kQuads = DP / 4, kTeams = kWave / kQuads;
+  const int lane = threadIdx.x & (kWave - 1), team = lane / kQuads;
   const int group = a.q_heads / a.kv_heads;
   const int kv_head = static_cast<int>(blockIdx.x % a.kv_heads);
   SeqRows seq;
@@ -361,36 +377,61 @@ __global__ void __launch_bounds__(256) attention_join_kernel(AttnArgs a) {
   const int64_t keys = keys_seen(seq, row_of(min(r0 + kRows, rows) - 1, rows, group).query, a.causal);
   const int64_t each = split_keys(keys, a.splits, SplitShape<BF16, DP>::kStep);
   const int live = keys <= each ? 1 : static_cast<int>((keys + each - 1) / each);
-  constexpr int kQuads = DP / 4;  // lanes of a row
-  for (int r = threadIdx.x / kQuads; r < kRows; r += 256 / kQuads) {
+  const int d = lane % kQuads * 4;
+  const int64_t pitch = a.head_dim + 4, step = a.seqs.rows_q * a.q_heads * pitch;
+  for (int r = threadIdx.x / kWave; r < kRows && r0 + r < rows; r += 256 / kWave) {
     const Row w = row_of(r0 + r, rows, group);
-    const int d = threadIdx.x % kQuads * 4;
-    if (!w.exists || d >= a.head_dim) continue;
     const int64_t head = static_cast<int64_t>(kv_head) * group + w.head, at = (seq.q0 + w.query) * a.q_heads + head;
-    const int64_t pitch = a.head_dim + 4, step = a.seqs.rows_q * a.q_heads * pitch;
     const float* const p = a.ws + at * pitch;
-    float top = -INFINITY;
-    for (int s = 0; s < live; ++s) top = fmaxf(top, p[s * step + a.head_dim]);
-    float total = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int s = 0; s < live; ++s) {
-      const float2 ms = *reinterpret_cast<const float2*>(p + s * step + a.head_dim);
-      const float4 v = *reinterpret_cast<const float4*>(p + s * step + d);
-      const float share = ms.x == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(ms.x - top);
-      total = __builtin_fmaf(share, ms.y, total);
-      acc[0] = __builtin_fmaf(share, v.x, acc[0]);
-      acc[1] = __builtin_fmaf(share, v.y, acc[1]);
-      acc[2] = __builtin_fmaf(share, v.z, acc[2]);
-      acc[3] = __builtin_fmaf(share, v.w, acc[3]);
+    float top = -INFINITY, sum = 0.0f;
+    if (lane < live) {
+      const float2 ms = *reinterpret_cast<const float2*>(p + lane * step + a.head_dim);
+      top = ms.x;
+      sum = ms.y;
     }
+    float best = top;
+#pragma unroll
+    for (int x = 1; x < kWave; x <<= 1) best = fmaxf(best, __shfl_xor(best, x));
+    const float share = top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(top - best);
+    const float total = wave_sum(share * sum);
+    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    const bool inside = d < a.head_dim;
+    constexpr int kAhead = 8;  // loads in flight
+    for (int s = team; s < live + team; s += kAhead * kTeams) {
+      float4 v[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int split = s + i * kTeams;
+        v[i] = inside && split < live ? *reinterpret_cast<const float4*>(p + split * step + d) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int split = s + i * kTeams;
+        const float f = __shfl(share, split < live ? split : kWave - 1);
+        if (split >= live) continue;
+        acc[0] = __builtin_fmaf(f, v[i].x, acc[0]);
+        acc[1] = __builtin_fmaf(f, v[i].y, acc[1]);
+        acc[2] = __builtin_fmaf(f, v[i].z, acc[2]);
+        acc[3] = __builtin_fmaf(f, v[i].w, acc[3]);
+      }
+    }
+#pragma unroll
+    for (int x = kQuads; x < kWave; x <<= 1)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[j] += __shfl_xor(acc[j], x);
     const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-    uint8_t* const out = row_data(a.out, seq.q0 + w.query, head, kElem) + d * kElem;
-    if constexpr (BF16)
-      *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
-    else
-      *reinterpret_cast<float4*>(out) = make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
-    if (a.lse && d == 0) a.lse[at] = total == 0.0f ? -INFINITY : (top + __builtin_log2f(total)) * kLn2;
+    if (inside && team == 0) {
+      uint8_t* const out = row_data(a.out, seq.q0 + w.query, head, kElem) + d * kElem;
+      if constexpr (BF16)
+        *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
+      else
+        *reinterpret_cast<float4*>(out) = make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
+    }
+    if (a.lse && lane == 0) a.lse[at] = total == 0.0f ? -INFINITY : (best + __builtin_log2f(total)) * kLn2;
   }
 }
+
+constexpr int kMostSplits = kWave;  // a lane of the joining wave each
 
 // Few rows per sequence take the split kernel.
 bool few_rows(const AttnSeqs& s, int group) { return s.rows_q * group <= kRows * s.n_seq; }
@@ -426,7 +467,7 @@ int attention_splits(const AttnSeqs& s, int q_heads, int kv_heads, int head_dim,
   const int64_t want = fill < ceil_div(longest, 8 * step) ? ceil_div(longest, 8 * step) : fill;
   const int64_t most = ceil_div(longest, 2 * step);
   const int64_t splits = want < most ? want : most;
-  return static_cast<int>(splits < 1 ? 1 : splits > 64 ? 64 : splits);
+  return static_cast<int>(splits < 1 ? 1 : splits > kMostSplits ? kMostSplits : splits);
 }
 
 int64_t attention_workspace(const AttnSeqs& s, int q_heads, int kv_heads, int head_dim, bool bf16) {

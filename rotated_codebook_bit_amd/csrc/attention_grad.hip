@@ -141,39 +141,57 @@ __global__ void __launch_bounds__(kWaves * kWave, BF16 ? 2 : 1) attention_dq_ker
   store_columns<BF16, DP>(dq, a.scale, row.exists ? row_data(a.dq, at, head, kElem) : nullptr, a.head_dim, half);
 }
 
-// dk and dv of 128 keys, 32 per wave, over the rows of every head of the group
-// in tiles of 64.  Scores are formed as q . k^T here: a lane holds 16 rows of
-// one key, which is the operand of both sums over the rows.
-constexpr int kTileRows = 64;
+// dk and dv of a block's keys, 32 per wave, over the rows of every head of the
+// group in turns of 32.  Scores are formed as q . k^T here: a lane holds 16
+// rows of one key, which is the operand of both sums over the rows.
+//
+// A wave needs 128 registers for dk and dv and 64 for its keys and values, so
+// one wave has a SIMD to itself and nothing else fills its waits: the next
+// turn's scores are formed while this turn's probabilities are (their
+// instructions interleaved), and rows are loaded three turns ahead into a ring
+// of four (in arrays of their own, as the compiler waits for all loads under way
+// where it cannot tell their places apart).
+//
+// HEADS: streams of heads in a block.  The first keys of a long sequence are
+// seen by all its rows, so one stream over all heads of the group makes a few
+// blocks that outlast the others; two streams over half of the heads each, by
+// two waves of 64 keys each, halve the longest block, and their sums meet in
+// shared memory.
+constexpr int kTurnRows = 32;
 
-template <bool BF16, int DP>
+template <bool BF16, int DP, int HEADS>
 __global__ void __launch_bounds__(kWaves * kWave, 1) attention_dkv_kernel(AttnArgs a) {
-  typedef Tile<BF16, DP, kTileRows> T;
-  constexpr int kElem = T::kElem, kSubs = kTileRows / 32, kDepth = DP / 16, kDt = DP / 32;
-  __shared__ __attribute__((aligned(16))) uint8_t q_tile0[T::kBytes], q_tile1[T::kBytes], do_tile0[T::kBytes], do_tile1[T::kBytes];
-  __shared__ __attribute__((aligned(16))) float stat0[2 * kTileRows], stat1[2 * kTileRows];  // log sums, D
-  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), half = lane >> 5;
+  typedef Tile<BF16, DP, kTurnRows> T;
+  constexpr int kElem = T::kElem, kDepth = DP / 16, kDt = DP / 32, kKeyWaves = kWaves / HEADS, kBlockKeys = kKeyWaves * kRows;
+  constexpr int kBytes = HEADS * T::kBytes, kStat = HEADS * 2 * kWave;
+  __shared__ __attribute__((aligned(16))) uint8_t q0[kBytes], q1[kBytes], q2[kBytes], q3[kBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t do0[kBytes], do1[kBytes], do2[kBytes], do3[kBytes];
+  __shared__ __attribute__((aligned(16))) float stat0[kStat], stat1[kStat], stat2[kStat], stat3[kStat];  // log sums, D
+  const int lane = threadIdx.x & (kWave - 1), half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) % kKeyWaves;    // along the keys
+  const int stream = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) / kKeyWaves;  // of heads
   const int group = a.q_heads / a.kv_heads;
   const int kv_head = static_cast<int>(blockIdx.x % a.kv_heads);
   SeqRows seq;
   int64_t tile;
-  if (!find_tile(a.seqs, blockIdx.x / a.kv_heads, [&](const SeqRows& s) { return (s.nk + kBlockRows - 1) / kBlockRows; }, &seq,
+  if (!find_tile(a.seqs, blockIdx.x / a.kv_heads, [&](const SeqRows& s) { return (s.nk + kBlockKeys - 1) / kBlockKeys; }, &seq,
                  &tile))
     return;
-  const int64_t key0 = tile * kBlockRows, wave_key = key0 + wave * kRows, key = wave_key + (lane & 31);
+  const int64_t key0 = tile * kBlockKeys, wave_key = key0 + wave * kRows, key = wave_key + (lane & 31);
   const bool exists = key < seq.nk;
   // Row i sees keys up to i + ahead.
   const int64_t ahead = seq.nk - seq.nq;
-  const int64_t first_row = a.causal ? cut(key0 - ahead, 0, seq.nq) : 0;  // the first that sees key0
-  const int64_t first_tile = first_row / kTileRows, row_tiles = (seq.nq + kTileRows - 1) / kTileRows;
-  const int64_t per_head = seq.nq > first_row ? row_tiles - first_tile : 0;
+  const int64_t first_row = a.causal ? cut(key0 - ahead, 0, seq.nq) / kTurnRows * kTurnRows : 0;  // of the turn with the first that sees key0
+  const int64_t per_head = (seq.nq - first_row + kTurnRows - 1) / kTurnRows;
+  const int64_t turns = per_head * ((group + HEADS - 1) / HEADS);  // of the longest stream
 
   Operand<BF16> k[kDepth], v[kDepth];
   load_row_operands<BF16, DP>(exists ? row_data(a.k, seq.k0 + key, kv_head, kElem) : nullptr, a.head_dim, half, k);
   load_row_operands<BF16, DP>(exists ? row_data(a.v, seq.k0 + key, kv_head, kElem) : nullptr, a.head_dim, half, v);
-  const TileLoader<BF16, DP, kTileRows, kWaves> q_load(wave, lane, a.q.row, a.head_dim), do_load(wave, lane, a.dout.row, a.head_dim);
-  const RowOperand<BF16, DP> by_row(lane);
-  const ColumnOperand<BF16, DP> by_column(lane);
+  const TileLoader<BF16, DP, kTurnRows, kKeyWaves> q_load(wave, lane, a.q.row, a.head_dim), do_load(wave, lane, a.dout.row, a.head_dim);
+  constexpr int kLoads = 2 * TileLoader<BF16, DP, kTurnRows, kKeyWaves>::kLoads;  // of a turn, without the statistics
+  const RowOperand<BF16, DP> by_row(lane, stream * T::kBytes);
+  const ColumnOperand<BF16, DP> by_column(lane, stream * T::kBytes);
   const float factor = a.scale * kLog2e;
 
   f32_x16 dk[kDt], dv[kDt];
@@ -182,99 +200,222 @@ __global__ void __launch_bounds__(kWaves * kWave, 1) attention_dkv_kernel(AttnAr
 #pragma unroll
     for (int r = 0; r < 16; ++r) dk[dt][r] = dv[dt][r] = 0.0f;
 
-  // Turn u is tile first_tile + u % per_head of head u / per_head of the group; the loader is one turn ahead.
-  const int64_t turns = per_head * group;
-  int64_t load_tile = first_tile, load_head = static_cast<int64_t>(kv_head) * group, this_tile = first_tile;
+  // A stream's turns: the rows from first_row on of heads stream, stream + HEADS, ... of the group.
+  int head = stream;                     // being loaded
+  int64_t load_row = first_row, this_row = first_row;
+  const uint8_t *q_at, *do_at;
+  float* stat_at;
+  auto start_head = [&]() __attribute__((always_inline)) {
+    const int64_t h = static_cast<int64_t>(kv_head) * group + (head < group ? head : 0);
+    load_row = first_row;
+    q_at = row_data(a.q, seq.q0 + first_row, h, kElem);
+    do_at = row_data(a.dout, seq.q0 + first_row, h, kElem);
+    stat_at = (wave ? dots(a, h) : log_sums(a, h)) + seq.q0 + first_row;
+  };
+  start_head();
   auto issue = [&](uint8_t* qt, uint8_t* dot, float* stat) __attribute__((always_inline)) {
-    const int64_t i = load_tile * kTileRows, left = seq.nq - i;
-    q_load.issue(row_data(a.q, seq.q0 + i, load_head, kElem), left, qt);
-    do_load.issue(row_data(a.dout, seq.q0 + i, load_head, kElem), left, dot);
+    const int64_t left = head < group ? seq.nq - load_row : 0;  // past the last head: zeros, which add nothing
+    q_load.issue(q_at, left, qt + stream * T::kBytes);
+    do_load.issue(do_at, left, dot + stream * T::kBytes);
 #if defined(__HIP_DEVICE_COMPILE__)
     if (wave < 2) {
       // Rows past the sequence read as zeros: P = 1 there, times dout = 0.
-      float* const p = (wave ? dots(a, load_head) : log_sums(a, load_head)) + seq.q0 + i;
-      const auto src = __builtin_amdgcn_make_buffer_rsrc(p, 0, static_cast<int>(min(left, int64_t(kTileRows)) * 4), 0x00020000);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (lds_void_ptr)(stat + wave * kTileRows), 4, lane * 4, 0, 0, 0);
+      const auto src = __builtin_amdgcn_make_buffer_rsrc(
+          stat_at, 0, __builtin_amdgcn_readfirstlane(static_cast<int>(min(left, int64_t(kTurnRows)) * 4)), 0x00020000);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (lds_void_ptr)(stat + (2 * stream + wave) * kWave), 4, lane * 4, 0, 0, 0);
     }
 #endif
-    if (++load_tile == row_tiles) {
-      load_tile = first_tile;
-      ++load_head;
+    load_row += kTurnRows;
+    q_at += kTurnRows * a.q.row * kElem;
+    do_at += kTurnRows * a.dout.row * kElem;
+    stat_at += kTurnRows;
+    if (load_row >= seq.nq) {
+      head += HEADS;
+      start_head();
     }
   };
-  auto compute = [&](const uint8_t* qt, const uint8_t* dot, const float* stat) __attribute__((always_inline)) {
-    const int64_t i0 = this_tile * kTileRows;
-    if (++this_tile == row_tiles) this_tile = first_tile;
-    if (wave_key >= seq.nk) return;
+  // Scores and dout . v of a turn's rows.
+  auto scores = [&](const uint8_t* qt, const uint8_t* dot, f32_x16& s, f32_x16& dp) __attribute__((always_inline)) {
 #pragma unroll
-    for (int sub = 0; sub < kSubs; ++sub) {
-      const int64_t i = i0 + 32 * sub;
-      if (a.causal && i + 31 + ahead < wave_key) continue;  // no row of these sees a key of this wave
-      f32_x16 s, dp;
+    for (int r = 0; r < 16; ++r) s[r] = dp[r] = 0.0f;
 #pragma unroll
-      for (int r = 0; r < 16; ++r) s[r] = dp[r] = 0.0f;
+    for (int kk = 0; kk < kDepth; ++kk) {
+      multiply<BF16>(s, by_row.load(qt, 0, kk), k[kk]);
+      multiply<BF16>(dp, by_row.load(dot, 0, kk), v[kk]);
+    }
+  };
+  // From a turn's scores to its probabilities (s) and dS (dp), then the sums;
+  // the next turn's scores meanwhile, in one stretch of code without branches.
+  auto step = [&](int64_t i, const uint8_t* qt, const uint8_t* dot, const float* stat, const uint8_t* next_q, const uint8_t* next_do,
+                  f32_x16& s, f32_x16& dp, f32_x16& next_s, f32_x16& next_dp) __attribute__((always_inline)) {
+    float l[16], d[16];
+    stat += stream * 2 * kWave;
 #pragma unroll
-      for (int kk = 0; kk < kDepth; ++kk) {
-        multiply<BF16>(s, by_row.load(qt, sub, kk), k[kk]);
-        multiply<BF16>(dp, by_row.load(dot, sub, kk), v[kk]);
+    for (int g = 0; g < 4; ++g) {
+      const float4 ls = *reinterpret_cast<const float4*>(stat + 8 * g + 4 * half);
+      const float4 dd = *reinterpret_cast<const float4*>(stat + kWave + 8 * g + 4 * half);
+      l[4 * g] = ls.x, l[4 * g + 1] = ls.y, l[4 * g + 2] = ls.z, l[4 * g + 3] = ls.w;
+      d[4 * g] = dd.x, d[4 * g + 1] = dd.y, d[4 * g + 2] = dd.z, d[4 * g + 3] = dd.w;
+    }
+    if (a.causal && i + ahead < wave_key + 31) {
+      const int see = static_cast<int>(cut(key - ahead - i, 0, kTurnRows)) - 4 * half;  // rows from here on see the key
+#pragma unroll
+      for (int r = 0; r < 16; ++r) l[r] = result_row(r) < see ? INFINITY : l[r];  // P = 0
+    }
+    Operand<BF16> do_col = by_column.load(dot, 0, 0), q_col = by_column.load(qt, 0, 0);
+#if defined(__HIP_DEVICE_COMPILE__)
+    __builtin_amdgcn_sched_barrier(0);
+#endif
+    // A product of the next turn's scores, an operand's read two products
+    // ahead, and a share of this turn's probabilities, in this order: the
+    // matrix cores work on one product while the rest is issued.
+    constexpr int kProducts = 2 * kDepth, kShare = 16 / kProducts ? 16 / kProducts : 1, kAhead = 3;
+    auto operand = [&](int n) __attribute__((always_inline)) { return by_row.load(n & 1 ? next_do : next_q, 0, n >> 1); };
+    Operand<BF16> ops[kProducts];
+#pragma unroll
+    for (int n = 0; n < kAhead; ++n) ops[n] = operand(n);
+#pragma unroll
+    for (int r = 0; r < 16; ++r) next_s[r] = next_dp[r] = 0.0f;
+#pragma unroll
+    for (int n = 0; n < kProducts; ++n) {
+      if (n + kAhead < kProducts) ops[n + kAhead] = operand(n + kAhead);
+      if (n & 1)
+        multiply<BF16>(next_dp, ops[n], v[n >> 1]);
+      else
+        multiply<BF16>(next_s, ops[n], k[n >> 1]);
+#pragma unroll
+      for (int r = n * kShare; r < n * kShare + kShare; ++r) {
+        s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], factor, -l[r]));
+        if (r) dp[r - 1] = s[r - 1] * (dp[r - 1] - d[r - 1]);
       }
+#if defined(__HIP_DEVICE_COMPILE__)
+      if constexpr (BF16) __builtin_amdgcn_sched_barrier(0);
+#endif
+    }
+    dp[15] = s[15] * (dp[15] - d[15]);
+    Operand<BF16> p[2], ds[2];
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const float4 ls = *reinterpret_cast<const float4*>(stat + 32 * sub + 8 * g + 4 * half);
-        const float4 dd = *reinterpret_cast<const float4*>(stat + kTileRows + 32 * sub + 8 * g + 4 * half);
-        const float l[4] = {ls.x, ls.y, ls.z, ls.w}, d[4] = {dd.x, dd.y, dd.z, dd.w};
+    for (int h = 0; h < 2; ++h) {
+      p[h] = result_operand<BF16>(s, h);
+      ds[h] = result_operand<BF16>(dp, h);
+    }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int r = 4 * g + j;
-          s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], factor, -l[j]));
-          dp[r] = s[r] * (dp[r] - d[j]);
-        }
+    for (int n = 0; n < 2 * kDt; ++n) {
+      const int h = n / kDt, dt = n % kDt, next = n + 1 < 2 * kDt ? n + 1 : 0;
+      const Operand<BF16> do_now = do_col, q_now = q_col;
+      if (n + 1 < 2 * kDt) {
+        do_col = by_column.load(dot, next / kDt, next % kDt);
+        q_col = by_column.load(qt, next / kDt, next % kDt);
       }
-      if (a.causal && i + ahead < wave_key + 31) {
-        const int see = static_cast<int>(cut(key - ahead - i, 0, 32)) - 4 * half;  // rows from here on see the key
+      multiply<BF16>(dv[dt], do_now, p[h]);
+      multiply<BF16>(dk[dt], q_now, ds[h]);
+    }
+#if defined(__HIP_DEVICE_COMPILE__)
+    if constexpr (BF16) {
 #pragma unroll
-        for (int r = 0; r < 16; ++r)
-          if (result_row(r) < see) s[r] = dp[r] = 0.0f;
-      }
-#pragma unroll
-      for (int step = 0; step < 2; ++step) {
-        const Operand<BF16> p = result_operand<BF16>(s, step), ds = result_operand<BF16>(dp, step);
-#pragma unroll
-        for (int dt = 0; dt < kDt; ++dt) {
-          multiply<BF16>(dv[dt], by_column.load(dot, 2 * sub + step, dt), p);
-          multiply<BF16>(dk[dt], by_column.load(qt, 2 * sub + step, dt), ds);
-        }
+      for (int n = 0; n < 2 * kDt; ++n) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
       }
     }
+    __builtin_amdgcn_sched_barrier(0);
+#endif
+  };
+  // The turn in `qt`; the following one's rows are in next_q, and free_q, the turn before's, takes the one three ahead.
+  auto turn = [&](const uint8_t* qt, const uint8_t* dot, const float* stat, const uint8_t* next_q, const uint8_t* next_do, uint8_t* free_q,
+                  uint8_t* free_do, float* free_stat, f32_x16& s, f32_x16& dp, f32_x16& next_s, f32_x16& next_dp)
+                  __attribute__((always_inline)) {
+    // All but the youngest turn's loads: waves 0 and 1 have one more.
+    if (wave < 2)
+      wait_loads<kLoads + 1>();
+    else
+      wait_loads<kLoads>();
+    __syncthreads();
+    issue(free_q, free_do, free_stat);
+    const int64_t i = this_row;
+    this_row = i + kTurnRows >= seq.nq ? first_row : i + kTurnRows;
+    step(i, qt, dot, stat, next_q, next_do, s, dp, next_s, next_dp);
   };
 
-  if (turns > 0) issue(q_tile0, do_tile0, stat0);
-  for (int64_t u = 0; u < turns; u += 2) {
+  // Turns by the ring's length, so that each place in it is an array of its own.
+  if (turns > 0) {
+    f32_x16 s_a, dp_a, s_b, dp_b;
+    issue(q0, do0, stat0);
+    issue(q1, do1, stat1);
+    issue(q2, do2, stat2);
     wait_loads<0>();
     __syncthreads();
-    if (u + 1 < turns) issue(q_tile1, do_tile1, stat1);
-    compute(q_tile0, do_tile0, stat0);
-    if (u + 1 >= turns) break;
-    wait_loads<0>();
-    __syncthreads();
-    if (u + 2 < turns) issue(q_tile0, do_tile0, stat0);
-    compute(q_tile1, do_tile1, stat1);
+    scores(q0, do0, s_a, dp_a);
+    for (int64_t u = 0; u < turns; u += 4) {
+      turn(q0, do0, stat0, q1, do1, q3, do3, stat3, s_a, dp_a, s_b, dp_b);
+      turn(q1, do1, stat1, q2, do2, q0, do0, stat0, s_b, dp_b, s_a, dp_a);
+      turn(q2, do2, stat2, q3, do3, q1, do1, stat1, s_a, dp_a, s_b, dp_b);
+      turn(q3, do3, stat3, q0, do0, q2, do2, stat2, s_b, dp_b, s_a, dp_a);
+    }
+    wait_loads<0>();  // none is under way into memory that is given back
+  }
+  if constexpr (HEADS == 2) {
+    // The second stream's sums, 32 values of a head at a time, through shared memory.
+    static_assert(kKeyWaves * kWave * 64 <= kBytes, "a part of dk fits a place of the ring");
+    const int at = wave * kWave * 4 + lane;  // in 16 bytes, as 4 x 64 lanes
+#pragma unroll
+    for (int dt = 0; dt < kDt; ++dt) {
+      __syncthreads();
+      if (stream) {
+        uint4 w[8];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          w[2 * g] = pack_piece<false>(reinterpret_cast<const float*>(&dk[dt]) + 4 * g);
+          w[2 * g + 1] = pack_piece<false>(reinterpret_cast<const float*>(&dv[dt]) + 4 * g);
+          reinterpret_cast<uint4*>(q0)[at + g * kWave] = w[2 * g];
+          reinterpret_cast<uint4*>(do0)[at + g * kWave] = w[2 * g + 1];
+        }
+        hold_until_lds_written(w);
+      }
+      __syncthreads();
+      if (!stream) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          float x[4], y[4];
+          unpack_piece<false>(reinterpret_cast<const uint4*>(q0)[at + g * kWave], x);
+          unpack_piece<false>(reinterpret_cast<const uint4*>(do0)[at + g * kWave], y);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            dk[dt][4 * g + j] += x[j];
+            dv[dt][4 * g + j] += y[j];
+          }
+        }
+      }
+    }
+    if (stream) return;
   }
   store_columns<BF16, DP>(dk, a.scale, exists ? row_data(a.dk, seq.k0 + key, kv_head, kElem) : nullptr, a.head_dim, half);
   store_columns<BF16, DP>(dv, 1.0f, exists ? row_data(a.dv, seq.k0 + key, kv_head, kElem) : nullptr, a.head_dim, half);
 }
 
-int64_t k_tiles(const AttnSeqs& s) {
-  return tile_bound(s, s.k_starts ? -1 : s.rows_k / s.n_seq, s.rows_k, kBlockRows);
+int64_t k_tiles(const AttnSeqs& s, int per_tile) {
+  return tile_bound(s, s.k_starts ? -1 : s.rows_k / s.n_seq, s.rows_k, per_tile);
 }
+
+// Two streams where a group has several heads and their rings fit shared memory.
+bool two_streams(int group, int head_dim, bool bf16) { return group > 1 && (bf16 || head_dim <= 64); }
 
 template <bool BF16, int DP>
 hipError_t launch_at(const AttnArgs& a, hipStream_t stream) {
-  const int64_t tiles = q_tiles(a.seqs, a.q_heads / a.kv_heads, kBlockRows);
+  const int group = a.q_heads / a.kv_heads;
+  const int64_t tiles = q_tiles(a.seqs, group, kBlockRows);
   if (tiles)
     attention_dq_kernel<BF16, DP><<<dim3(static_cast<uint32_t>(tiles * a.kv_heads)), dim3(kWaves * kWave), 0, stream>>>(a, tiles);
-  const int64_t kt = k_tiles(a.seqs);
-  if (kt) attention_dkv_kernel<BF16, DP><<<dim3(static_cast<uint32_t>(kt * a.kv_heads)), dim3(kWaves * kWave), 0, stream>>>(a);
+  const bool two = two_streams(group, a.head_dim, BF16);
+  const dim3 grid(static_cast<uint32_t>(k_tiles(a.seqs, (two ? 2 : 4) * kRows) * a.kv_heads)), block(kWaves * kWave);
+  if (grid.x == 0) return hipGetLastError();
+  if constexpr (BF16 || DP <= 64) {
+    if (two) {
+      attention_dkv_kernel<BF16, DP, 2><<<grid, block, 0, stream>>>(a);
+      return hipGetLastError();
+    }
+  }
+  attention_dkv_kernel<BF16, DP, 1><<<grid, block, 0, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -285,7 +426,7 @@ int64_t attention_grad_workspace(const AttnSeqs& s, int q_heads, int kv_heads, i
 }
 
 int64_t attention_grad_blocks(const AttnSeqs& s, int q_heads, int kv_heads, int head_dim, bool bf16) {
-  const int64_t q = q_tiles(s, q_heads / kv_heads, kBlockRows), k = k_tiles(s);
+  const int64_t q = q_tiles(s, q_heads / kv_heads, kBlockRows), k = k_tiles(s, 2 * kRows);
   return (q > k ? q : k) * kv_heads;
 }
 

@@ -790,7 +790,6 @@ struct RotateArgs {
   int64_t cache_rows;
   float* part;  // gradient: shares of the weights' gradients, per block [2][head_dim]
 };
-int64_t rotate_blocks(int64_t n, int q_heads, int kv_heads, bool values, int head_dim);  // of 256 threads
 hipError_t launch_rotate_heads(const RotateArgs& a, bool bf16, hipStream_t stream);
 int rotate_grad_blocks(int64_t n, int q_heads, int kv_heads, int head_dim);
 hipError_t launch_rotate_heads_grad(RotateArgs a, bool bf16, float* dq_weight, float* dk_weight, float* ws, hipStream_t stream);

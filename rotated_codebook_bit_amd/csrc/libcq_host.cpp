@@ -1567,8 +1567,6 @@ int cq_qk_norm_rope(const cq_heads* q, const cq_heads* k, const cq_heads* v, int
   if (v && ((rc = check_heads("v", v, n, kv_heads, head_dim, dtype, false)) ||
             (rc = check_heads("v_out", v_out, out_rows, kv_heads, head_dim, dtype, true))))
     return rc;
-  if (cq::rotate_blocks(n, q_heads, kv_heads, v != nullptr, head_dim) > cq::most_blocks(256))
-    return fail(CQ_ERR_UNSUPPORTED, "n is past this call's grid");
   const Lattice in[3] = {lattice(q, n, q_heads, head_dim, dtype), lattice(k, n, kv_heads, head_dim, dtype),
                          lattice(v, n, kv_heads, head_dim, dtype)};
   const Lattice out[3] = {lattice(q_out, n, q_heads, head_dim, dtype), lattice(k_out, out_rows, kv_heads, head_dim, dtype),

@@ -60,9 +60,7 @@ REFUSALS = [
     (L.cq_qk_norm_rope, ROTATE, ALIGN, [dict(q=heads(A + 8)), dict(k=heads(B, 514)), dict(ko=heads(H, 512, 66)), dict(pos=E + 4), dict(freqs=F + 2),
                                         dict(qw=D + 2), dict(slots=J + 4)]),
     (L.cq_qk_norm_rope, ROTATE, UNSUPPORTED, [dict(d=60), dict(d=264), dict(n=1 << 31), dict(qh=5000), dict(rows=1 << 31),
-                                              dict(q=heads(A, (1 << 22) + 4)), dict(k=heads(B, 512, 1 << 60)),
-                                              dict(n=1 << 30, slots=None, q=heads(A, 0), k=heads(B, 0), v=None, vo=None, qh=64,
-                                                   qo=heads(1 << 44, 1 << 13), ko=heads(1 << 50, 1 << 13))]),
+                                              dict(q=heads(A, (1 << 22) + 4)), dict(k=heads(B, 512, 1 << 60))]),
     (L.cq_qk_norm_rope_grad, ROTATE_GRAD, ARG, [dict(norm=0), dict(wb=100), dict(dqw=I + 4096), dict(dq=heads(C)), dict(dq=heads(A, 1024)),
                                                 dict(dk=heads(G)), dict(dq=heads(J)), dict(dqw=C), dict(dqw=E), dict(ws=A), dict(ws=I),
                                                 dict(dk=heads(H, 32)), dict(dq=heads(F))]),
