@@ -169,15 +169,25 @@ __device__ __forceinline__ void multiply(f32_x16& c, const Operand<BF16>& a, con
 // is the order in which column_operand() reads a tile's rows.
 template <bool BF16>
 __device__ __forceinline__ Operand<BF16> result_operand(const f32_x16& c, int step) {
-  Operand<BF16> o;
+  if constexpr (BF16) {
+    const uint4 w = make_uint4(pack_bf16(c[8 * step], c[8 * step + 1]), pack_bf16(c[8 * step + 2], c[8 * step + 3]),
+                               pack_bf16(c[8 * step + 4], c[8 * step + 5]), pack_bf16(c[8 * step + 6], c[8 * step + 7]));
+    return __builtin_bit_cast(bf16_x8, w);
+  } else {
+    Operand<BF16> o;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if constexpr (BF16)
-      o[j] = static_cast<__bf16>(c[8 * step + j]);
-    else
-      o[j] = c[8 * step + j];
+    for (int j = 0; j < 8; ++j) o[j] = c[8 * step + j];
+    return o;
   }
-  return o;
+}
+
+// Keeps the compiler from moving instructions across: where an order of reads
+// and products was chosen by hand it would undo it, each product then waiting
+// for operands that were read just before.
+__device__ __forceinline__ void pin() {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __builtin_amdgcn_sched_barrier(0);
+#endif
 }
 
 // Row of element r of a 32 x 32 result, without the lane's 4 (l / 32).

@@ -126,10 +126,16 @@ __global__ void __launch_bounds__(kWaves * kWave, BF16 ? 2 : 1) attention_kernel
     for (int sub = 0; sub < kSubs; ++sub)
 #pragma unroll
       for (int r = 0; r < 16; ++r) s[sub][r] = 0.0f;
+    constexpr int kAhead = 4;  // operands read before their product
+    Operand<BF16> keys[kSubs * kDepth];
 #pragma unroll
-    for (int kk = 0; kk < kDepth; ++kk)
+    for (int n = 0; n < kAhead; ++n) keys[n] = by_row.load(kt, n % kSubs, n / kSubs);
 #pragma unroll
-      for (int sub = 0; sub < kSubs; ++sub) multiply<BF16>(s[sub], by_row.load(kt, sub, kk), q[kk]);
+    for (int n = 0; n < kSubs * kDepth; ++n) {
+      if (n + kAhead < kSubs * kDepth) keys[n + kAhead] = by_row.load(kt, (n + kAhead) % kSubs, (n + kAhead) / kSubs);
+      multiply<BF16>(s[n % kSubs], keys[n], q[n / kSubs]);
+      if constexpr (BF16) pin();
+    }
     if (key + kTileKeys > all_see) {
       const int left = static_cast<int>(min(seen - key, int64_t(kTileKeys))) - 4 * half;
 #pragma unroll
@@ -139,11 +145,19 @@ __global__ void __launch_bounds__(kWaves * kWave, BF16 ? 2 : 1) attention_kernel
           if (32 * sub + result_row(r) >= left) s[sub][r] = -INFINITY;
     }
     soften<kSubs, kDt>(s, factor, st, o);
+    Operand<BF16> values[2 * kSubs * kDt];
+#pragma unroll
+    for (int n = 0; n < kDt; ++n) values[n] = by_column.load(vt, n / kDt, n % kDt);
 #pragma unroll
     for (int step = 0; step < 2 * kSubs; ++step) {
       const Operand<BF16> p = result_operand<BF16>(s[step / 2], step % 2);
 #pragma unroll
-      for (int dt = 0; dt < kDt; ++dt) multiply<BF16>(o[dt], by_column.load(vt, step, dt), p);
+      for (int dt = 0; dt < kDt; ++dt) {
+        const int n = step * kDt + dt;
+        if (step + 1 < 2 * kSubs) values[n + kDt] = by_column.load(vt, step + 1, dt);
+        multiply<BF16>(o[dt], values[n], p);
+        if constexpr (BF16) pin();
+      }
     }
   };
 

@@ -105,10 +105,19 @@ __global__ void __launch_bounds__(kWaves * kWave, BF16 ? 2 : 1) attention_dq_ker
       f32_x16 s, dp;
 #pragma unroll
       for (int r = 0; r < 16; ++r) s[r] = dp[r] = 0.0f;
+      constexpr int kAhead = 4;  // operands read before their product
+      auto operand = [&](int n) __attribute__((always_inline)) { return by_row.load(n & 1 ? vt : kt, sub, n >> 1); };
+      Operand<BF16> rows_of[2 * kDepth];
 #pragma unroll
-      for (int kk = 0; kk < kDepth; ++kk) {
-        multiply<BF16>(s, by_row.load(kt, sub, kk), q[kk]);
-        multiply<BF16>(dp, by_row.load(vt, sub, kk), dout[kk]);
+      for (int n = 0; n < kAhead; ++n) rows_of[n] = operand(n);
+#pragma unroll
+      for (int n = 0; n < 2 * kDepth; ++n) {
+        if (n + kAhead < 2 * kDepth) rows_of[n + kAhead] = operand(n + kAhead);
+        if (n & 1)
+          multiply<BF16>(dp, rows_of[n], dout[n >> 1]);
+        else
+          multiply<BF16>(s, rows_of[n], q[n >> 1]);
+        if constexpr (BF16) pin();
       }
 #pragma unroll
       for (int r = 0; r < 16; ++r) s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], factor, -log_sum)) * (dp[r] - dot);
@@ -117,11 +126,15 @@ __global__ void __launch_bounds__(kWaves * kWave, BF16 ? 2 : 1) attention_dq_ker
         for (int r = 0; r < 16; ++r)
           if (32 * sub + result_row(r) >= left) s[r] = 0.0f;
       }
+      Operand<BF16> columns[2 * kDt];
 #pragma unroll
-      for (int step = 0; step < 2; ++step) {
-        const Operand<BF16> ds = result_operand<BF16>(s, step);
+      for (int n = 0; n < kDt; ++n) columns[n] = by_column.load(kt, 2 * sub, n);
 #pragma unroll
-        for (int dt = 0; dt < kDt; ++dt) multiply<BF16>(dq[dt], by_column.load(kt, 2 * sub + step, dt), ds);
+      for (int n = 0; n < 2 * kDt; ++n) {
+        const Operand<BF16> ds = result_operand<BF16>(s, n / kDt);
+        if (n < kDt) columns[n + kDt] = by_column.load(kt, 2 * sub + 1, n);
+        multiply<BF16>(dq[n % kDt], columns[n], ds);
+        if constexpr (BF16) pin();
       }
     }
   };
@@ -263,9 +276,7 @@ __global__ void __launch_bounds__(kWaves * kWave, 1) attention_dkv_kernel(AttnAr
       for (int r = 0; r < 16; ++r) l[r] = result_row(r) < see ? INFINITY : l[r];  // P = 0
     }
     Operand<BF16> do_col = by_column.load(dot, 0, 0), q_col = by_column.load(qt, 0, 0);
-#if defined(__HIP_DEVICE_COMPILE__)
-    __builtin_amdgcn_sched_barrier(0);
-#endif
+    if constexpr (BF16) pin();
     // A product of the next turn's scores, an operand's read two products
     // ahead, and a share of this turn's probabilities, in this order: the
     // matrix cores work on one product while the rest is issued.
@@ -288,9 +299,7 @@ __global__ void __launch_bounds__(kWaves * kWave, 1) attention_dkv_kernel(AttnAr
         s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], factor, -l[r]));
         if (r) dp[r - 1] = s[r - 1] * (dp[r - 1] - d[r - 1]);
       }
-#if defined(__HIP_DEVICE_COMPILE__)
-      if constexpr (BF16) __builtin_amdgcn_sched_barrier(0);
-#endif
+      if constexpr (BF16) pin();
     }
     dp[15] = s[15] * (dp[15] - d[15]);
     Operand<BF16> p[2], ds[2];
@@ -299,27 +308,19 @@ __global__ void __launch_bounds__(kWaves * kWave, 1) attention_dkv_kernel(AttnAr
       p[h] = result_operand<BF16>(s, h);
       ds[h] = result_operand<BF16>(dp, h);
     }
+    // The columns of a product pair are read while the pair before is multiplied.
 #pragma unroll
     for (int n = 0; n < 2 * kDt; ++n) {
-      const int h = n / kDt, dt = n % kDt, next = n + 1 < 2 * kDt ? n + 1 : 0;
+      const int h = n / kDt, dt = n % kDt;
       const Operand<BF16> do_now = do_col, q_now = q_col;
       if (n + 1 < 2 * kDt) {
-        do_col = by_column.load(dot, next / kDt, next % kDt);
-        q_col = by_column.load(qt, next / kDt, next % kDt);
+        do_col = by_column.load(dot, (n + 1) / kDt, (n + 1) % kDt);
+        q_col = by_column.load(qt, (n + 1) / kDt, (n + 1) % kDt);
       }
       multiply<BF16>(dv[dt], do_now, p[h]);
       multiply<BF16>(dk[dt], q_now, ds[h]);
+      if constexpr (BF16) pin();
     }
-#if defined(__HIP_DEVICE_COMPILE__)
-    if constexpr (BF16) {
-#pragma unroll
-      for (int n = 0; n < 2 * kDt; ++n) {
-        __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
-        __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
-      }
-    }
-    __builtin_amdgcn_sched_barrier(0);
-#endif
   };
   // The turn in `qt`; the following one's rows are in next_q, and free_q, the turn before's, takes the one three ahead.
   auto turn = [&](const uint8_t* qt, const uint8_t* dot, const float* stat, const uint8_t* next_q, const uint8_t* next_do, uint8_t* free_q,
