@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 from typing import Any, NamedTuple
 
 import numpy as np
@@ -147,7 +148,7 @@ def lib() -> ctypes.CDLL:
         L.cq_dequant_gemm_q8_workspace.argtypes = [i64, i64, i64, i32, p64]
         L.cq_dequant_gemm_q8.argtypes = [vp, vp, i64, i64, i32, i32, ctypes.POINTER(Q8Table), vp, vp, i64, vp, i32, vp,
                                          i64, vp]
-        hp, sp = ctypes.POINTER(Heads), ctypes.POINTER(Sequences)
+        hp = sp = vp  # cq_heads and cq_sequences, packed or by reference
         rotation = [i32, i64, i32, i32, i32, i32, vp, vp, i32, f32, vp, i32, vp, i32, i32]
         L.cq_qk_norm_rope.argtypes = [hp, hp, hp, *rotation, hp, hp, hp, vp, i32, i64, vp]
         L.cq_qk_norm_rope_grad_workspace.argtypes = [i64, i32, i32, i32, p64]
@@ -864,17 +865,25 @@ def dequant_gemm_q8(packed, norms, n_out: int, k: int, bits: int, table: Q8Table
 
 # -- an attention block and a model's end ------------------------------------------
 
-def _heads_device(heads, flat) -> int:
-    """Index of the one CUDA device of all given tensors: `heads` may be
-    strided (but for a head's values), `flat` are contiguous; (name, tensor or
-    None) pairs."""
-    dev = _device(flat)
-    for name, t in heads:
+# cq_heads and cq_sequences as bytes: building the ctypes structures costs the
+# call of one token 4 us more.
+_pack_heads = struct.Struct("Pqq").pack
+_pack_sequences = struct.Struct("qqqPPPi4x").pack
+
+
+def _heads(named, dev: int = -1):
+    """(device, cq_heads of every tensor): the tensors of `named`, (name,
+    tensor or None), are [rows, heads, head_dim] on one CUDA device (`dev`, if
+    given) and may be strided, but for a head's values."""
+    packed = []
+    for name, t in named:
         if t is None:
+            packed.append(None)
             continue
-        if t.dim() != 3:
-            raise ValueError(f"{name} must be [rows, heads, head_dim], got {tuple(t.shape)}")
-        if t.stride(2) != 1 and t.shape[2] > 1:
+        shape, stride = t.shape, t.stride()
+        if len(shape) != 3:
+            raise ValueError(f"{name} must be [rows, heads, head_dim], got {tuple(shape)}")
+        if stride[2] != 1 and shape[2] > 1:
             raise ValueError(f"{name}: a head's values must be contiguous")
         d = t.get_device()
         if d < 0:
@@ -883,23 +892,23 @@ def _heads_device(heads, flat) -> int:
             dev = d
         elif d != dev:
             raise ValueError(f"{name} is on device {d}, the other tensors on {dev}")
-    return dev
+        packed.append(_pack_heads(t.data_ptr(), stride[0] if shape[0] > 1 else 0, stride[1] if shape[1] > 1 else 0))
+    return dev, packed
 
 
-def _heads(t):
-    """A cq_heads of a [rows, heads, head_dim] tensor (None: NULL)."""
-    if t is None:
-        return None
-    rows, heads, _ = t.shape
-    return ctypes.byref(Heads(t.data_ptr(), t.stride(0) if rows > 1 else 0, t.stride(1) if heads > 1 else 0))
+def _new_heads(like, shape):
+    """A new tensor of heads and its cq_heads."""
+    t = like.new_empty(shape)
+    return t, _pack_heads(t.data_ptr(), shape[1] * shape[2], shape[2])
 
 
 def _same_kind(like_name, like, pairs):
     """Every tensor of `pairs`, (name, tensor or None, shape), has the dtype
     of `like` and its shape."""
+    dtype = like.dtype
     for name, t, shape in pairs:
-        if t is not None and (t.dtype != like.dtype or tuple(t.shape) != tuple(shape)):
-            raise ValueError(f"{name} must be {like.dtype} (as {like_name}) of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+        if t is not None and (t.dtype != dtype or t.shape != shape):
+            raise ValueError(f"{name} must be {dtype} (as {like_name}) of shape {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
 
 
 def _index_bytes(name, t) -> int:
@@ -919,7 +928,8 @@ def _rotation_args(q, k, positions, freqs, q_weight, k_weight, eps, norm, interl
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q and k must be [rows, heads, head_dim]")
     n, qh, d = q.shape
-    _same_kind("q", q, (("k", k, (n, k.shape[1], d)),))
+    if k.dtype != q.dtype or k.shape[0] != n or k.shape[2] != d:
+        raise ValueError(f"k must be {q.dtype} [{n}, heads, {d}], got {k.dtype} {tuple(k.shape)}")
     rotary = 0 if freqs is None else 2 * freqs.numel()
     pb = 8
     if rotary:
@@ -968,16 +978,18 @@ def qk_norm_rope(q, k, positions=None, freqs=None, q_weight=None, k_weight=None,
                         ("v_out", v_out, (rows, kvh, d))))
     heads = (("q", q), ("k", k), ("v", v), ("q_out", q_out), ("k_out", k_out), ("v_out", v_out))
     flat = (("positions", positions), ("freqs", freqs), ("q_weight", q_weight), ("k_weight", k_weight), ("slots", slots))
-    dev = _heads_device(heads, flat)
+    dev, (qp, kp, vp, qo, ko, vo) = _heads(heads, _device(flat))
     if not _here(dev, stream):
         return _elsewhere(dev, stream, heads + flat, lambda: qk_norm_rope(
             q, k, positions, freqs, q_weight, k_weight, eps, norm, interleaved, v, slots, q_out, k_out, v_out))
-    q_out = _out_tensor("q_out", q_out, q.shape, q.dtype, q)
-    k_out = _out_tensor("k_out", k_out, (rows, kvh, d), q.dtype, q)
-    v_out = None if v is None else _out_tensor("v_out", v_out, (rows, kvh, d), q.dtype, q)
+    if q_out is None:
+        q_out, qo = _new_heads(q, q.shape)
+    if k_out is None:
+        k_out, ko = _new_heads(q, k.shape)
+    if v is not None and v_out is None:
+        v_out, vo = _new_heads(q, k.shape)
     _check("cq_qk_norm_rope", lib().cq_qk_norm_rope(
-        _heads(q), _heads(k), _heads(v), *args, _heads(q_out), _heads(k_out), _heads(v_out), _opt(slots),
-        8 if slots is None else _index_bytes("slots", slots), rows, _raw_stream(dev)))
+        qp, kp, vp, *args, qo, ko, vo, _opt(slots), 8 if slots is None else _index_bytes("slots", slots), rows, _raw_stream(dev)))
     return (q_out, k_out) if v is None else (q_out, k_out, v_out)
 
 
@@ -992,32 +1004,33 @@ def qk_norm_rope_grad(dq_out, dk_out, q, k, positions=None, freqs=None, q_weight
     _same_kind("q", q, (("dq_out", dq_out, q.shape), ("dk_out", dk_out, k.shape), ("dq", dq, q.shape), ("dk", dk, k.shape)))
     heads = (("q", q), ("k", k), ("dq_out", dq_out), ("dk_out", dk_out), ("dq", dq), ("dk", dk))
     flat = (("positions", positions), ("freqs", freqs), ("q_weight", q_weight), ("k_weight", k_weight), ("workspace", workspace))
-    dev = _heads_device(heads, flat)
+    dev, (qp, kp, dqo, dko, dqp, dkp) = _heads(heads, _device(flat))
     if not _here(dev, stream):
         return _elsewhere(dev, stream, heads + flat, lambda: qk_norm_rope_grad(
             dq_out, dk_out, q, k, positions, freqs, q_weight, k_weight, eps, norm, interleaved, dq, dk, workspace))
-    dq = _out_tensor("dq", dq, q.shape, q.dtype, q)
-    dk = _out_tensor("dk", dk, k.shape, q.dtype, q)
+    if dq is None:
+        dq, dqp = _new_heads(q, q.shape)
+    if dk is None:
+        dk, dkp = _new_heads(q, k.shape)
     dqw = dkw = ws = None
     wb = 0
     if norm:
         dqw, dkw = q.new_empty(d, dtype=torch.float32), q.new_empty(d, dtype=torch.float32)
         ws, wb = _workspace("cq_qk_norm_rope_grad_workspace", (n, qh, kvh, d), workspace, q)
     _check("cq_qk_norm_rope_grad", lib().cq_qk_norm_rope_grad(
-        _heads(dq_out), _heads(dk_out), _heads(q), _heads(k), *args, _heads(dq), _heads(dk), _opt(dqw), _opt(dkw), _opt(ws), wb,
-        _raw_stream(dev)))
+        dqo, dko, qp, kp, *args, dqp, dkp, _opt(dqw), _opt(dkw), _opt(ws), wb, _raw_stream(dev)))
     return dq, dk, dqw, dkw
 
 
 def _attention_args(q, k, v, sequences, q_starts, k_starts, k_lens, scale):
-    """(Sequences, dtype code, q_heads, kv_heads, head_dim, scale) of an
+    """(cq_sequences, dtype code, q_heads, kv_heads, head_dim, scale) of an
     attention call, checked."""
     code = _dtype_code("q", q)
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q and k must be [rows, heads, head_dim]")
     rows_q, qh, d = q.shape
     rows_k, kvh, _ = k.shape
-    _same_kind("q", q, (("k", k, (rows_k, kvh, d)), ("v", v, (rows_k, kvh, d))))
+    _same_kind("q", q, (("k", k, (rows_k, kvh, d)), ("v", v, k.shape)))
     n = sequences
     for name, t, more in (("q_starts", q_starts, 1), ("k_lens", k_lens, 0), ("k_starts", k_starts, 0 if k_lens is not None else 1)):
         if t is None:
@@ -1033,7 +1046,7 @@ def _attention_args(q, k, v, sequences, q_starts, k_starts, k_lens, scale):
               if t is not None}
     if len(bytes_) > 1:
         raise TypeError("q_starts, k_starts and k_lens must have one dtype")
-    seqs = Sequences(n, rows_q, rows_k, _opt(q_starts), _opt(k_starts), _opt(k_lens), bytes_.pop() if bytes_ else 4)
+    seqs = _pack_sequences(n, rows_q, rows_k, _opt(q_starts) or 0, _opt(k_starts) or 0, _opt(k_lens) or 0, bytes_.pop() if bytes_ else 4)
     return seqs, code, qh, kvh, d, 1.0 / math.sqrt(max(d, 1)) if scale is None else scale
 
 
@@ -1052,21 +1065,23 @@ def attention(q, k, v, sequences=None, q_starts=None, k_starts=None, k_lens=None
     _same_kind("q", q, (("out", out, q.shape),))
     heads = (("q", q), ("k", k), ("v", v), ("out", out))
     flat = (("q_starts", q_starts), ("k_starts", k_starts), ("k_lens", k_lens), ("lse", lse), ("workspace", workspace))
-    dev = _heads_device(heads, flat)
+    dev, (qp, kp, vp, op) = _heads(heads, _device(flat))
     if not _here(dev, stream):
         return _elsewhere(dev, stream, heads + flat, lambda: attention(
             q, k, v, sequences, q_starts, k_starts, k_lens, causal, scale, out, lse, workspace))
-    new = torch.empty if q_starts is None else torch.zeros  # starts may leave rows out
-    out = new(q.shape, dtype=q.dtype, device=q.device) if out is None else out
+    if out is None:
+        out, op = _new_heads(q, q.shape)
+        if q_starts is not None:
+            out.zero_()  # starts may leave rows out
     if lse is None:
-        lse = new(q.shape[:2], dtype=torch.float32, device=q.device)
+        lse = q.new_empty(q.shape[:2], dtype=torch.float32)
+        if q_starts is not None:
+            lse.zero_()
     else:
         _out_tensor("lse", lse, q.shape[:2], torch.float32, q)
-    sp = ctypes.byref(seqs)
-    ws, wb = _workspace("cq_attention_workspace", (sp, code, qh, kvh, d), workspace, q)
+    ws, wb = _workspace("cq_attention_workspace", (seqs, code, qh, kvh, d), workspace, q)
     _check("cq_attention", lib().cq_attention(
-        _heads(q), _heads(k), _heads(v), code, sp, qh, kvh, d, int(bool(causal)), scale, _heads(out), lse.data_ptr(), _opt(ws), wb,
-        _raw_stream(dev)))
+        qp, kp, vp, code, seqs, qh, kvh, d, int(bool(causal)), scale, op, lse.data_ptr(), _opt(ws), wb, _raw_stream(dev)))
     return out, lse
 
 
@@ -1084,20 +1099,27 @@ def attention_grad(dout, q, k, v, out, lse, sequences=None, q_starts=None, k_sta
         raise ValueError(f"lse must be float32 {tuple(q.shape[:2])}, got {lse.dtype} {tuple(lse.shape)}")
     heads = (("q", q), ("k", k), ("v", v), ("dout", dout), ("out", out), ("dq", dq), ("dk", dk), ("dv", dv))
     flat = (("q_starts", q_starts), ("k_starts", k_starts), ("k_lens", k_lens), ("lse", lse), ("workspace", workspace))
-    dev = _heads_device(heads, flat)
+    dev, (qp, kp, vp, dop, op, dqp, dkp, dvp) = _heads(heads, _device(flat))
     if not _here(dev, stream):
         return _elsewhere(dev, stream, heads + flat, lambda: attention_grad(
             dout, q, k, v, out, lse, sequences, q_starts, k_starts, k_lens, causal, scale, dq, dk, dv, workspace))
-    new_q = torch.empty if q_starts is None else torch.zeros
-    new_k = torch.empty if k_starts is None and k_lens is None else torch.zeros
-    dq = new_q(q.shape, dtype=q.dtype, device=q.device) if dq is None else dq
-    dk = new_k(k.shape, dtype=q.dtype, device=q.device) if dk is None else dk
-    dv = new_k(k.shape, dtype=q.dtype, device=q.device) if dv is None else dv
-    sp = ctypes.byref(seqs)
-    ws, wb = _workspace("cq_attention_grad_workspace", (sp, code, qh, kvh, d), workspace, q)
+    if dq is None:
+        dq, dqp = _new_heads(q, q.shape)
+        if q_starts is not None:
+            dq.zero_()  # starts may leave rows out
+    gaps = k_starts is not None or k_lens is not None
+    if dk is None:
+        dk, dkp = _new_heads(q, k.shape)
+        if gaps:
+            dk.zero_()
+    if dv is None:
+        dv, dvp = _new_heads(q, k.shape)
+        if gaps:
+            dv.zero_()
+    ws, wb = _workspace("cq_attention_grad_workspace", (seqs, code, qh, kvh, d), workspace, q)
     _check("cq_attention_grad", lib().cq_attention_grad(
-        _heads(dout), _heads(q), _heads(k), _heads(v), _heads(out), lse.data_ptr(), code, sp, qh, kvh, d, int(bool(causal)), scale,
-        _heads(dq), _heads(dk), _heads(dv), _opt(ws), wb, _raw_stream(dev)))
+        dop, qp, kp, vp, op, lse.data_ptr(), code, seqs, qh, kvh, d, int(bool(causal)), scale, dqp, dkp, dvp, _opt(ws), wb,
+        _raw_stream(dev)))
     return dq, dk, dv
 
 
@@ -1134,11 +1156,12 @@ def token_logprobs(logits, tokens, scale: float = 1.0, top: int = 0, stream=None
     if not _here(dev, stream):
         return _elsewhere(dev, stream, (("logits", logits), ("tokens", tokens)), lambda: token_logprobs(logits, tokens, scale, top))
     rows, vocab = tokens.numel(), logits.shape[-1]
-    logprob, entropy, lse = torch.empty((3, *tokens.shape), dtype=torch.float32, device=logits.device).unbind(0)
+    shape = tokens.shape
+    logprob, entropy, lse = logits.new_empty((3, *shape), dtype=torch.float32).unbind(0)
     ids = lps = None
     if top > 0:
-        ids = torch.empty((*tokens.shape, top), dtype=torch.int64, device=logits.device)
-        lps = torch.empty((*tokens.shape, top), dtype=torch.float32, device=logits.device)
+        ids = logits.new_empty((*shape, top), dtype=torch.int64)
+        lps = logits.new_empty((*shape, top), dtype=torch.float32)
     _check("cq_token_logprobs", lib().cq_token_logprobs(
         logits.data_ptr(), code, rows, vocab, stride, scale, tokens.data_ptr(), tb, logprob.data_ptr(), entropy.data_ptr(),
         lse.data_ptr(), top, _opt(ids), _opt(lps), _raw_stream(dev)))
@@ -1168,7 +1191,7 @@ def token_logprobs_grad(logits, tokens, lse, dlogprob, dentropy=None, entropy=No
         return _elsewhere(dev, stream, named + (("logits", logits), ("dlogits", dlogits)), lambda: token_logprobs_grad(
             logits, tokens, lse, dlogprob, dentropy, entropy, scale, dlogits))
     if dlogits is None:
-        dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        dlogits = logits.new_empty(logits.shape)
     _check("cq_token_logprobs_grad", lib().cq_token_logprobs_grad(
         logits.data_ptr(), code, tokens.numel(), logits.shape[-1], stride, scale, tokens.data_ptr(), tb, lse.data_ptr(),
         dlogprob.data_ptr(), _opt(dentropy), _opt(entropy), dlogits.data_ptr(), out_stride, _raw_stream(dev)))

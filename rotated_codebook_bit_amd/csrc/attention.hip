@@ -194,9 +194,11 @@ __device__ __forceinline__ int64_t split_keys(int64_t keys, int splits, int step
 
 template <bool BF16, int DP>
 struct SplitShape {
-  // Two tiles of keys and of values per wave: 16 KiB (bf16, 128) to 64.
+  // Two tiles of keys and of values per wave, 16 KiB (bf16, 64) to 64: blocks
+  // small enough that at least two share a CU, so that one's start and end run
+  // beside the other's stream of keys.
   static constexpr int kTile = Tile<BF16, DP, 32>::kBytes;
-  static constexpr int kWaves = 4 * kTile * 4 > 131072 ? 2 : 4;
+  static constexpr int kWaves = 2 * 4 * kTile > 65536 ? 1 : 2;
   static constexpr int kStep = 32 * kWaves;  // keys that a block takes in one turn
   static constexpr int kPitch = DP + 4;      // floats per row of a wave's output in shared memory
 };
@@ -232,8 +234,6 @@ __global__ void __launch_bounds__((SplitShape<BF16, DP>::kWaves * kWave), 1) att
   const int64_t seen = row.exists ? keys_seen(seq, row.query, a.causal) : 0;
   const int64_t out_row = seq.q0 + row.query, out_head = static_cast<int64_t>(kv_head) * group + row.head;
 
-  Operand<BF16> q[kDepth];
-  load_row_operands<BF16, DP>(row.exists ? row_data(a.q, out_row, out_head, kElem) : nullptr, a.head_dim, half, q);
   const TileLoader<BF16, DP, 32, 1> k_load(0, lane, a.k.row, a.head_dim), v_load(0, lane, a.v.row, a.head_dim);
   constexpr int kPending = 2 * TileLoader<BF16, DP, 32, 1>::kLoads;  // of one turn
   const RowOperand<BF16, DP> by_row(lane);
@@ -242,19 +242,22 @@ __global__ void __launch_bounds__((SplitShape<BF16, DP>::kWaves * kWave), 1) att
   const uint8_t* const v0 = row_data(a.v, seq.k0, kv_head, kElem);
   const float factor = a.scale * kLog2e;
 
-  RowState st{-INFINITY, 0.0f};
-  f32_x16 o[kDt];
-#pragma unroll
-  for (int dt = 0; dt < kDt; ++dt)
-#pragma unroll
-    for (int r = 0; r < 16; ++r) o[dt][r] = 0.0f;
-
   uint8_t* const even = tiles0 + wave * 2 * T::kBytes;
   uint8_t* const odd = tiles1 + wave * 2 * T::kBytes;
   auto issue = [&](int64_t key, uint8_t* kt) __attribute__((always_inline)) {
     k_load.issue(k0 + key * a.k.row * kElem, seq.nk - key, kt);
     v_load.issue(v0 + key * a.v.row * kElem, seq.nk - key, kt + T::kBytes);
   };
+  int64_t key = begin + 32 * wave;
+  if (key < end) issue(key, even);
+  Operand<BF16> q[kDepth];
+  load_row_operands<BF16, DP>(row.exists ? row_data(a.q, out_row, out_head, kElem) : nullptr, a.head_dim, half, q);
+  RowState st{-INFINITY, 0.0f};
+  f32_x16 o[kDt];
+#pragma unroll
+  for (int dt = 0; dt < kDt; ++dt)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) o[dt][r] = 0.0f;
   auto compute = [&](int64_t key, const uint8_t* kt) __attribute__((always_inline)) {
     f32_x16 s[1];
 #pragma unroll
@@ -299,8 +302,6 @@ __global__ void __launch_bounds__((SplitShape<BF16, DP>::kWaves * kWave), 1) att
     }
     compute(key, now);
   };
-  int64_t key = begin + 32 * wave;
-  if (key < end) issue(key, even);
   while (key < end) {
     turn(key, even, odd);
     key += Shape::kStep;
@@ -311,9 +312,9 @@ __global__ void __launch_bounds__((SplitShape<BF16, DP>::kWaves * kWave), 1) att
 
   // The waves' rows together: each leaves its output, maximum and sum.
   auto part_of = [&](int w) __attribute__((always_inline)) {
-    return reinterpret_cast<float*>((w < W / 2 ? tiles0 : tiles1) + w % (W / 2) * 4 * T::kBytes);
+    return reinterpret_cast<float*>((w % 2 ? tiles1 : tiles0) + w / 2 * 4 * T::kBytes);
   };
-  static_assert(kRows * Shape::kPitch * 4 <= 4 * T::kBytes, "a wave's output fits two of its tiles");
+  static_assert(W <= 2 && kRows * Shape::kPitch * 4 <= W * 2 * T::kBytes, "a wave's output fits one of the arrays");
   float* const part = part_of(wave);
   float sum_a, sum_b;
   both_halves(st.sum, &sum_a, &sum_b);
@@ -447,8 +448,20 @@ __global__ void __launch_bounds__(256) attention_join_kernel(AttnArgs a) {
 
 constexpr int kMostSplits = kWave;  // a lane of the joining wave each
 
-// Few rows per sequence take the split kernel.
-bool few_rows(const AttnSeqs& s, int group) { return s.rows_q * group <= kRows * s.n_seq; }
+// Whether a call takes the split kernel.  Up to 32 rows per sequence and key
+// head (one tile) always do.  More rows do while 128-row blocks would leave most
+// of the card idle over long keys: a block takes 18 ns per key (bf16 heads of
+// 128, 512 blocks at once), a tile of 32 rows some 60 us per 2^20 keys of all
+// CUs, and 20 us more to start, end and join.  Over 8192 keys of 8 heads, 32 query
+// heads: 64 new tokens 47 us (blocks 149), 128 65 (149), 512 276 (150); 8 x 16
+// over 4096 49 (78); 1000 tokens of a prompt, 8 heads of 64 over 2, 33 (19).
+// Float32: 64 tokens 180 (1130), 512 1419 (1137).
+bool few_rows(const AttnSeqs& s, int group, int kv_heads) {
+  if (s.rows_q * group <= kRows * s.n_seq) return true;
+  const int64_t keys = s.rows_k / s.n_seq, blocks = q_tiles(s, group, kBlockRows) * kv_heads;
+  const int64_t units = q_tiles(s, group, kRows) * kv_heads;
+  return keys > 0 && units + 333000 / keys < 300 * ceil_div(blocks, 2 * kCus);
+}
 
 int split_step(int head_dim, bool bf16) {
   if (bf16) return head_dim <= 64 ? SplitShape<true, 64>::kStep : SplitShape<true, 128>::kStep;
@@ -458,7 +471,7 @@ int split_step(int head_dim, bool bf16) {
 template <bool BF16, int DP>
 hipError_t launch_at(const AttnArgs& a, hipStream_t stream) {
   const int group = a.q_heads / a.kv_heads;
-  if (!few_rows(a.seqs, group)) {
+  if (!few_rows(a.seqs, group, a.kv_heads)) {
     const int64_t tiles = q_tiles(a.seqs, group, kBlockRows);
     attention_kernel<BF16, DP><<<dim3(static_cast<uint32_t>(tiles * a.kv_heads)), dim3(kWaves * kWave), 0, stream>>>(a, tiles);
     return hipGetLastError();
@@ -472,14 +485,18 @@ hipError_t launch_at(const AttnArgs& a, hipStream_t stream) {
 
 }  // namespace
 
+// Splits of the keys: two blocks per CU where tiles of rows alone are fewer, and
+// at most 2048 keys each, so that sequences of different lengths do not leave
+// the card to the longest (64 tokens over up to 8192 keys of 8 heads, bf16: 238
+// us in pieces of 4096, 227 of 2048, 252 of 512).  More blocks than fit at once
+// each pay their start again (16 tokens over 2048 keys: 512 blocks 31 us, 2048 46).
 int attention_splits(const AttnSeqs& s, int q_heads, int kv_heads, int head_dim, bool bf16) {
   const int group = q_heads / kv_heads;
-  if (!few_rows(s, group)) return 1;
+  if (!few_rows(s, group, kv_heads)) return 1;
   const int64_t units = q_tiles(s, group, kRows) * kv_heads;
   const int64_t longest = s.k_starts ? s.rows_k : s.rows_k / s.n_seq, step = split_step(head_dim, bf16);
-  const int64_t fill = ceil_div(4 * kCus, units);
-  const int64_t want = fill < ceil_div(longest, 8 * step) ? ceil_div(longest, 8 * step) : fill;
-  const int64_t most = ceil_div(longest, 2 * step);
+  const int64_t fill = ceil_div(2 * kCus, units), by_length = ceil_div(longest, 2048);
+  const int64_t want = fill < by_length ? by_length : fill, most = ceil_div(longest, 2 * step);
   const int64_t splits = want < most ? want : most;
   return static_cast<int>(splits < 1 ? 1 : splits > kMostSplits ? kMostSplits : splits);
 }
@@ -491,7 +508,7 @@ int64_t attention_workspace(const AttnSeqs& s, int q_heads, int kv_heads, int he
 
 int64_t attention_blocks(const AttnSeqs& s, int q_heads, int kv_heads, int head_dim, bool bf16) {
   const int group = q_heads / kv_heads;
-  if (!few_rows(s, group)) return q_tiles(s, group, kBlockRows) * kv_heads;
+  if (!few_rows(s, group, kv_heads)) return q_tiles(s, group, kBlockRows) * kv_heads;
   return q_tiles(s, group, kRows) * kv_heads * attention_splits(s, q_heads, kv_heads, head_dim, bf16);
 }
 

@@ -122,6 +122,20 @@ def test_cache(heads, kv_heads, d, new, dtype):
 
 
 @TYPES
+@pytest.mark.parametrize("new,lens", [(20, [3000, 1000, 20]), (64, [2900]), (200, [4000]), (37, [3000] * 4)])
+def test_new_tokens_over_a_long_cache(new, lens, dtype):
+    cap, heads, kv_heads, d, b = max(lens), 8, 2, 128, len(lens)
+    q = randn(b * new, heads, d, dtype=dtype)
+    k, v = randn(b * cap, kv_heads, d, dtype=dtype, seed=1), randn(b * cap, kv_heads, d, dtype=dtype, seed=2)
+    out, lse = cq.attention(q, k, v, sequences=b, k_lens=torch.tensor(lens, device=DEV))
+    for i, n in enumerate(lens):
+        rows, keys = slice(i * new, (i + 1) * new), slice(i * cap, i * cap + n)
+        want, tol = attend(q[rows], k[keys], v[keys], 1 / math.sqrt(d), True)
+        close(out[rows], want["out"], tol["out"], ("out", n))
+        close(lse[rows], want["lse"], tol["lse"], ("lse", n))
+
+
+@TYPES
 def test_one_long_cache_of_one_token(dtype):
     n, heads, d = 40000, 4, 128
     q, k, v = randn(1, heads, d, dtype=dtype), randn(n, 1, d, dtype=dtype, seed=1), randn(n, 1, d, dtype=dtype, seed=2)
