@@ -26,6 +26,12 @@ constexpr int kGroups = 64;  // of threads; as many as there are lanes to rank t
 constexpr int kList = 2048;  // candidates in shared memory
 static_assert(kMaxTop <= kGroups, "a floor that kMaxTop values reach");
 
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kNothing = -10000.0f;  // a power of two that is 0 in float32
+
+// The larger of two, NaN if one is.
+__device__ __forceinline__ float at_least(float x, float y) { return __builtin_elementwise_maximum(x, y); }
+
 // Floats as integers of the same order: NaN above all, both zeros equal.
 __device__ __forceinline__ uint32_t order_of(float x) {
   const uint32_t u = __builtin_bit_cast(uint32_t, x + 0.0f);
@@ -187,14 +193,18 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(LogprobArgs a) {
       hold_value(g);
     }
   }
-  const float factor = a.scale * 1.4426950408889634f;
+  // In powers of two.  v - ref first, then the factor: against a rounded ref *
+  // factor it would be one operation less, but the largest term would not be
+  // exactly 1, and a certain token's log probability not 0 (or above it).
+  const float factor = a.scale * kLog2e;
   float sum = 0.0f, weighted = 0.0f;
   each_piece([&](int, const float (&v)[V]) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const float d = v[j] - ref, e = __builtin_amdgcn_exp2f(d * factor);
+      const float t = at_least((v[j] - ref) * factor, kNothing);  // -inf: 0 * t has to stay 0
+      const float e = __builtin_amdgcn_exp2f(t);
       sum += e;
-      weighted = __builtin_fmaf(e, fmaxf(d, -3.0e38f), weighted);  // 0 * -inf stays 0
+      weighted = __builtin_fmaf(e, t, weighted);
     }
   });
   sum = wave_sum(sum);
@@ -214,16 +224,16 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(LogprobArgs a) {
     sum += red[1][i];
     weighted += red[2][i];
   }
-  const float log_sum = logf(sum);
+  const float log_sum = __builtin_log2f(sum);
+  auto log_prob = [&](float v) __attribute__((always_inline)) {
+    return sum == 0.0f ? -INFINITY : __builtin_fmaf(v - ref, a.scale, -log_sum * kLn2);
+  };
   if (tid == 0) {
-    const float lse = __builtin_fmaf(ref, a.scale, log_sum);
-    if (a.lse) a.lse[row] = lse;
-    if (a.entropy) a.entropy[row] = sum == 0.0f ? 0.0f : log_sum - a.scale * (weighted / sum);
+    if (a.lse) a.lse[row] = __builtin_fmaf(ref, a.scale, log_sum * kLn2);
+    if (a.entropy) a.entropy[row] = sum == 0.0f ? 0.0f : (log_sum - weighted / sum) * kLn2;
     if (a.logprob) {
       const int64_t t = a.token_bytes == 4 ? static_cast<const int32_t*>(a.tokens)[row] : static_cast<const int64_t*>(a.tokens)[row];
-      float lp = 0.0f;
-      if (t >= 0 && t < a.vocab) lp = sum == 0.0f ? -INFINITY : (load_elem<BF16>(logits, t) - ref) * a.scale - log_sum;
-      a.logprob[row] = lp;
+      a.logprob[row] = t >= 0 && t < a.vocab ? log_prob(load_elem<BF16>(logits, t)) : 0.0f;
     }
   }
   if (a.top <= 0) return;
@@ -231,6 +241,10 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(LogprobArgs a) {
   // Values that reach the floor.
   const float least = floor_value;
   each_piece([&](int first, const float (&v)[V]) {
+    float piece_top = v[0];
+#pragma unroll
+    for (int j = 1; j < V; ++j) piece_top = at_least(piece_top, v[j]);
+    if (piece_top < least) return;  // nearly all; a NaN is not below
     uint32_t reach = 0;
 #pragma unroll
     for (int j = 0; j < V; ++j) reach |= v[j] < least ? 0u : 1u << j;
@@ -248,9 +262,8 @@ __global__ void __launch_bounds__(NT) logprobs_kernel(LogprobArgs a) {
   });
   __syncthreads();
   auto put = [&](int rank, uint64_t key) __attribute__((always_inline)) {
-    const float x = value_of(static_cast<uint32_t>(key >> 32));
     a.top_ids[row * a.top + rank] = 0xFFFFFFFFu - static_cast<uint32_t>(key);
-    a.top_logprobs[row * a.top + rank] = sum == 0.0f ? -INFINITY : (x - ref) * a.scale - log_sum;
+    a.top_logprobs[row * a.top + rank] = log_prob(value_of(static_cast<uint32_t>(key >> 32)));
   };
   const int n = listed;
   if (n <= kList) {
@@ -300,12 +313,16 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(LogprobArgs
   const int64_t t = a.token_bytes == 4 ? static_cast<const int32_t*>(a.tokens)[row] : static_cast<const int64_t*>(a.tokens)[row];
   const float lse = a.lse[row], g = t >= 0 && t < a.vocab ? a.dlogprob[row] : 0.0f;
   const float h = a.dentropy ? a.dentropy[row] : 0.0f, entropy = a.dentropy ? a.entropy[row] : 0.0f;
-  const bool empty = lse == -INFINITY;  // nothing but -inf: no gradient
+  // In powers of two, t = log2 p: dlogits = -p (hs t + ks), plus the token's share.
+  // A row of nothing but -inf has lse -inf; any other c leaves its p at 0.
+  const float factor = a.scale * kLog2e;
+  float ref = 0.0f, c = lse == -INFINITY ? 0.0f : lse * kLog2e;
+  const float hs = h * a.scale * kLn2, ks = lse != lse ? lse : (lse == -INFINITY ? 0.0f : __builtin_fmaf(h, entropy, g) * a.scale);
   // Far from zero a float32 lse says little about the sum next to the maximum
   // (at 1024 its step is 2^-13; a row of the type's lowest value would be all
   // certain): such a row is summed again.
-  float ref = 0.0f, log_sum = lse;
-  if (fabsf(lse) > 1024.0f && fabsf(lse) < INFINITY) {
+  const bool far = fabsf(lse) > 1024.0f && fabsf(lse) < INFINITY;
+  if (far) {
     __shared__ float red[2][kGradThreads / kWave];
     float top = -INFINITY, sum = 0.0f;
     for (int i = threadIdx.x; i < p.pieces(); i += kGradThreads) {
@@ -321,11 +338,12 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(LogprobArgs
       float v[V];
       unpack_piece<BF16>(p.inside(i, p.load(i)), v);
 #pragma unroll
-      for (int j = 0; j < V; ++j) sum += __builtin_amdgcn_exp2f((v[j] - ref) * a.scale * 1.4426950408889634f);
+      for (int j = 0; j < V; ++j) sum += __builtin_amdgcn_exp2f((v[j] - ref) * factor);
     }
-    log_sum = logf(over_waves<kGradThreads / kWave>(wave_sum(sum), red[1], [](float x, float y) { return x + y; }));
+    c = __builtin_log2f(over_waves<kGradThreads / kWave>(wave_sum(sum), red[1], [](float x, float y) { return x + y; }));
     __syncthreads();  // in place: every wave has read the row before one writes
   }
+  const float hit = lse == -INFINITY ? 0.0f : g * a.scale;
   for (;;) {
 #pragma unroll
     for (int k = 0; k < kGradPieces; ++k) {
@@ -334,13 +352,18 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(LogprobArgs
       if (e >= p.vocab) break;
       float v[V];
       unpack_piece<BF16>(r[k], v);
+      if (far) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] -= ref;
+      }
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        const float logp = __builtin_fmaf(v[j] - ref, a.scale, -log_sum);
-        const float prob = empty ? 0.0f : __builtin_amdgcn_exp2f(logp * 1.4426950408889634f);
-        float d = prob == 0.0f ? 0.0f : -prob * __builtin_fmaf(h, logp + entropy, g);
-        if (e + j == t) d += empty ? 0.0f : g;
-        v[j] = d * a.scale;
+        const float x = at_least(__builtin_fmaf(v[j], factor, -c), kNothing);
+        v[j] = -__builtin_amdgcn_exp2f(x) * __builtin_fmaf(hs, x, ks);
+      }
+      if (t >= e && t < e + V) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] += e + j == t ? hit : 0.0f;
       }
       if (together && e >= 0 && e + V <= p.vocab) {
         *reinterpret_cast<uint4*>(out + static_cast<int64_t>(e) * kElem) = pack_piece<BF16>(v);
