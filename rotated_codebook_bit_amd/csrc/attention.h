@@ -305,16 +305,24 @@ struct TileLoader {
       off[i] = byte < head_bytes ? row * row_bytes + byte : 0x80000000u;
     }
   }
-  // `first`: the first row's values; valid: rows that exist (0 or below: all zeros).
+#if defined(__HIP_DEVICE_COMPILE__)
+  // The tile whose first row is at `first`; rows: of it that exist (at most ROWS; 0 or below: all zeros).
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t source(const uint8_t* first, int rows) const {
+    const int bytes = __builtin_amdgcn_readfirstlane(rows > 0 ? static_cast<int>((rows - 1) * row_bytes + head_bytes) : 0);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(first), 0, bytes, 0x00020000);
+  }
+  // Load i < kLoads of the tile.
+  __device__ __forceinline__ void issue(__amdgpu_buffer_rsrc_t src, int i, int rows, uint8_t* tile) const {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (lds_void_ptr)(tile + 16 * ((i * WAVES + wave) * kWave)), 16,
+                                             static_cast<int>(first_row + i * kRowsPerLoad) >= rows ? 0x80000000u : off[i], 0, 0, 0);
+  }
+#endif
   __device__ __forceinline__ void issue(const uint8_t* first, int64_t valid, uint8_t* tile) const {
 #if defined(__HIP_DEVICE_COMPILE__)
-    const uint32_t n = __builtin_amdgcn_readfirstlane(valid >= ROWS ? ROWS : valid > 0 ? static_cast<int>(valid) : 0);
-    const int bytes = __builtin_amdgcn_readfirstlane(n ? static_cast<int>((n - 1) * row_bytes + head_bytes) : 0);
-    const auto src = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(first), 0, bytes, 0x00020000);
+    const int rows = __builtin_amdgcn_readfirstlane(valid >= ROWS ? ROWS : valid > 0 ? static_cast<int>(valid) : 0);
+    const auto src = source(first, rows);
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (lds_void_ptr)(tile + 16 * ((i * WAVES + wave) * kWave)), 16,
-                                               n < ROWS && first_row + i * kRowsPerLoad >= n ? 0x80000000u : off[i], 0, 0, 0);
+    for (int i = 0; i < kLoads; ++i) issue(src, i, rows, tile);
 #endif
   }
 };

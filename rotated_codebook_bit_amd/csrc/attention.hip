@@ -101,8 +101,8 @@ __global__ void __launch_bounds__(kWaves * kWave, BF16 ? 2 : 1) attention_kernel
   const TileLoader<BF16, DP, kTileKeys, kWaves> k_load(wave, lane, a.k.row, a.head_dim), v_load(wave, lane, a.v.row, a.head_dim);
   const RowOperand<BF16, DP> by_row(lane);
   const ColumnOperand<BF16, DP> by_column(lane);
-  const uint8_t* const k0 = row_data(a.k, seq.k0, kv_head, kElem);
-  const uint8_t* const v0 = row_data(a.v, seq.k0, kv_head, kElem);
+  [[maybe_unused]] const uint8_t* const k0 = row_data(a.k, seq.k0, kv_head, kElem);
+  [[maybe_unused]] const uint8_t* const v0 = row_data(a.v, seq.k0, kv_head, kElem);
   const float factor = a.scale * kLog2e;
 
   RowState st{-INFINITY, 0.0f};
@@ -113,14 +113,41 @@ __global__ void __launch_bounds__(kWaves * kWave, BF16 ? 2 : 1) attention_kernel
     for (int r = 0; r < 16; ++r) o[dt][r] = 0.0f;
 
   const int64_t n_tiles = (block_keys + kTileKeys - 1) / kTileKeys;
-  auto issue = [&](int64_t t, uint8_t* kt, uint8_t* vt) __attribute__((always_inline)) {
+  // The loads of a tile: begin(), then load(i) for each i < kLoads.  Spread over
+  // the products of the tile before: in one stretch they wait for each other,
+  // and the wave with them.
+  constexpr int kLoads = 2 * TileLoader<BF16, DP, kTileKeys, kWaves>::kLoads;
+  [[maybe_unused]] int keys_here = 0;  // of the tile being loaded; past the last: none
+#if defined(__HIP_DEVICE_COMPILE__)
+  __amdgpu_buffer_rsrc_t k_src, v_src;
+#endif
+  auto begin = [&](int64_t t) __attribute__((always_inline)) {
     const int64_t key = t * kTileKeys;
-    k_load.issue(k0 + key * a.k.row * kElem, seq.nk - key, kt);
-    v_load.issue(v0 + key * a.v.row * kElem, seq.nk - key, vt);
+    keys_here = __builtin_amdgcn_readfirstlane(t < n_tiles ? static_cast<int>(min(seq.nk - key, int64_t(kTileKeys))) : 0);
+#if defined(__HIP_DEVICE_COMPILE__)
+    k_src = k_load.source(k0 + key * a.k.row * kElem, keys_here);
+    v_src = v_load.source(v0 + key * a.v.row * kElem, keys_here);
+#endif
   };
-  auto compute = [&](int64_t t, const uint8_t* kt, const uint8_t* vt) __attribute__((always_inline)) {
+  auto load = [&](int i, uint8_t* kt, uint8_t* vt) __attribute__((always_inline)) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    if (i < kLoads / 2)
+      k_load.issue(k_src, i, keys_here, kt);
+    else
+      v_load.issue(v_src, i - kLoads / 2, keys_here, vt);
+#endif
+  };
+  auto load_all = [&](uint8_t* kt, uint8_t* vt) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) load(i, kt, vt);
+  };
+  auto compute = [&](int64_t t, const uint8_t* kt, const uint8_t* vt, uint8_t* next_k, uint8_t* next_v) __attribute__((always_inline)) {
     const int64_t key = t * kTileKeys;
-    if (key >= wave_keys) return;
+    begin(t + 1);
+    if (key >= wave_keys) {
+      load_all(next_k, next_v);
+      return;
+    }
     f32_x16 s[kSubs];
 #pragma unroll
     for (int sub = 0; sub < kSubs; ++sub)
@@ -132,6 +159,8 @@ __global__ void __launch_bounds__(kWaves * kWave, BF16 ? 2 : 1) attention_kernel
     for (int n = 0; n < kAhead; ++n) keys[n] = by_row.load(kt, n % kSubs, n / kSubs);
 #pragma unroll
     for (int n = 0; n < kSubs * kDepth; ++n) {
+      static_assert(kSubs * kDepth % kLoads == 0, "loads at even distances");
+      if (n % (kSubs * kDepth / kLoads) == 0) load(n / (kSubs * kDepth / kLoads), next_k, next_v);
       if (n + kAhead < kSubs * kDepth) keys[n + kAhead] = by_row.load(kt, (n + kAhead) % kSubs, (n + kAhead) / kSubs);
       multiply<BF16>(s[n % kSubs], keys[n], q[n / kSubs]);
       if constexpr (BF16) pin();
@@ -161,18 +190,20 @@ __global__ void __launch_bounds__(kWaves * kWave, BF16 ? 2 : 1) attention_kernel
     }
   };
 
-  if (n_tiles > 0) issue(0, k_tile0, v_tile0);
+  if (n_tiles > 0) {
+    begin(0);
+    load_all(k_tile0, v_tile0);
+  }
   for (int64_t t = 0; t < n_tiles; t += 2) {
     wait_loads<0>();
     __syncthreads();
-    if (t + 1 < n_tiles) issue(t + 1, k_tile1, v_tile1);
-    compute(t, k_tile0, v_tile0);
+    compute(t, k_tile0, v_tile0, k_tile1, v_tile1);
     if (t + 1 >= n_tiles) break;
     wait_loads<0>();
     __syncthreads();
-    if (t + 2 < n_tiles) issue(t + 2, k_tile0, v_tile0);
-    compute(t + 1, k_tile1, v_tile1);
+    compute(t + 1, k_tile1, v_tile1, k_tile0, v_tile0);
   }
+  wait_loads<0>();  // none is under way into memory that is given back
 
   float sum_a, sum_b;
   both_halves(st.sum, &sum_a, &sum_b);

@@ -79,8 +79,8 @@ __global__ void __launch_bounds__(kWaves * kWave, BF16 ? 2 : 1) attention_dq_ker
   const TileLoader<BF16, DP, kTileKeys, kWaves> k_load(wave, lane, a.k.row, a.head_dim), v_load(wave, lane, a.v.row, a.head_dim);
   const RowOperand<BF16, DP> by_row(lane);
   const ColumnOperand<BF16, DP> by_column(lane);
-  const uint8_t* const k0 = row_data(a.k, seq.k0, kv_head, kElem);
-  const uint8_t* const v0 = row_data(a.v, seq.k0, kv_head, kElem);
+  [[maybe_unused]] const uint8_t* const k0 = row_data(a.k, seq.k0, kv_head, kElem);
+  [[maybe_unused]] const uint8_t* const v0 = row_data(a.v, seq.k0, kv_head, kElem);
   const float factor = a.scale * kLog2e;
 
   f32_x16 dq[kDt];
@@ -90,14 +90,41 @@ __global__ void __launch_bounds__(kWaves * kWave, BF16 ? 2 : 1) attention_dq_ker
     for (int r = 0; r < 16; ++r) dq[dt][r] = 0.0f;
 
   const int64_t n_tiles = (block_keys + kTileKeys - 1) / kTileKeys;
-  auto issue = [&](int64_t t, uint8_t* kt, uint8_t* vt) __attribute__((always_inline)) {
+  // The loads of a tile: begin(), then load(i) for each i < kLoads.  Spread over
+  // the products of the tile before: in one stretch they wait for each other,
+  // and the wave with them.
+  constexpr int kLoads = 2 * TileLoader<BF16, DP, kTileKeys, kWaves>::kLoads;
+  [[maybe_unused]] int keys_here = 0;  // of the tile being loaded; past the last: none
+#if defined(__HIP_DEVICE_COMPILE__)
+  __amdgpu_buffer_rsrc_t k_src, v_src;
+#endif
+  auto begin = [&](int64_t t) __attribute__((always_inline)) {
     const int64_t key = t * kTileKeys;
-    k_load.issue(k0 + key * a.k.row * kElem, seq.nk - key, kt);
-    v_load.issue(v0 + key * a.v.row * kElem, seq.nk - key, vt);
+    keys_here = __builtin_amdgcn_readfirstlane(t < n_tiles ? static_cast<int>(min(seq.nk - key, int64_t(kTileKeys))) : 0);
+#if defined(__HIP_DEVICE_COMPILE__)
+    k_src = k_load.source(k0 + key * a.k.row * kElem, keys_here);
+    v_src = v_load.source(v0 + key * a.v.row * kElem, keys_here);
+#endif
   };
-  auto compute = [&](int64_t t, const uint8_t* kt, const uint8_t* vt) __attribute__((always_inline)) {
+  auto load = [&](int i, uint8_t* kt, uint8_t* vt) __attribute__((always_inline)) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    if (i < kLoads / 2)
+      k_load.issue(k_src, i, keys_here, kt);
+    else
+      v_load.issue(v_src, i - kLoads / 2, keys_here, vt);
+#endif
+  };
+  auto load_all = [&](uint8_t* kt, uint8_t* vt) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) load(i, kt, vt);
+  };
+  auto compute = [&](int64_t t, const uint8_t* kt, const uint8_t* vt, uint8_t* next_k, uint8_t* next_v) __attribute__((always_inline)) {
     const int64_t key = t * kTileKeys;
-    if (key >= wave_keys) return;
+    begin(t + 1);
+    if (key >= wave_keys) {
+      load_all(next_k, next_v);
+      return;
+    }
     const int left = static_cast<int>(min(seen - key, int64_t(kTileKeys))) - 4 * half;
     const bool masked = key + kTileKeys > all_see;
 #pragma unroll
@@ -112,6 +139,9 @@ __global__ void __launch_bounds__(kWaves * kWave, BF16 ? 2 : 1) attention_dq_ker
       for (int n = 0; n < kAhead; ++n) rows_of[n] = operand(n);
 #pragma unroll
       for (int n = 0; n < 2 * kDepth; ++n) {
+        constexpr int kApart = kSubs * 2 * kDepth / kLoads;  // products between loads
+        static_assert(kApart * kLoads == kSubs * 2 * kDepth, "loads at even distances");
+        if ((sub * 2 * kDepth + n) % kApart == 0) load((sub * 2 * kDepth + n) / kApart, next_k, next_v);
         if (n + kAhead < 2 * kDepth) rows_of[n + kAhead] = operand(n + kAhead);
         if (n & 1)
           multiply<BF16>(dp, rows_of[n], dout[n >> 1]);
@@ -139,18 +169,21 @@ __global__ void __launch_bounds__(kWaves * kWave, BF16 ? 2 : 1) attention_dq_ker
     }
   };
 
-  if (n_tiles > 0) issue(0, k_tile0, v_tile0);
+  if (n_tiles > 0) {
+    begin(0);
+    load_all(k_tile0, v_tile0);
+  }
   for (int64_t t = 0; t < n_tiles; t += 2) {
     wait_loads<0>();
     __syncthreads();
-    if (t + 1 < n_tiles) issue(t + 1, k_tile1, v_tile1);
-    compute(t, k_tile0, v_tile0);
+    compute(t, k_tile0, v_tile0, k_tile1, v_tile1);
     if (t + 1 >= n_tiles) break;
     wait_loads<0>();
     __syncthreads();
-    if (t + 2 < n_tiles) issue(t + 2, k_tile0, v_tile0);
-    compute(t + 1, k_tile1, v_tile1);
+    compute(t + 1, k_tile1, v_tile1, k_tile0, v_tile0);
   }
+  wait_loads<0>();  // none is under way into memory that is given back
+
   store_columns<BF16, DP>(dq, a.scale, row.exists ? row_data(a.dq, at, head, kElem) : nullptr, a.head_dim, half);
 }
 
@@ -214,38 +247,58 @@ __global__ void __launch_bounds__(kWaves * kWave, 1) attention_dkv_kernel(AttnAr
     for (int r = 0; r < 16; ++r) dk[dt][r] = dv[dt][r] = 0.0f;
 
   // A stream's turns: the rows from first_row on of heads stream, stream + HEADS, ... of the group.
-  int head = stream;                     // being loaded
-  int64_t load_row = first_row, this_row = first_row;
-  const uint8_t *q_at, *do_at;
-  float* stat_at;
+  int head = stream, load_turn = 0;  // being loaded
+  const int last_turn = static_cast<int>(per_head) - 1, last_rows = static_cast<int>(seq.nq - first_row - int64_t(last_turn) * kTurnRows);
+  [[maybe_unused]] const uint8_t *q_at, *do_at;
+  [[maybe_unused]] const float* stat_at;
   auto start_head = [&]() __attribute__((always_inline)) {
     const int64_t h = static_cast<int64_t>(kv_head) * group + (head < group ? head : 0);
-    load_row = first_row;
     q_at = row_data(a.q, seq.q0 + first_row, h, kElem);
     do_at = row_data(a.dout, seq.q0 + first_row, h, kElem);
     stat_at = (wave ? dots(a, h) : log_sums(a, h)) + seq.q0 + first_row;
   };
   start_head();
-  auto issue = [&](uint8_t* qt, uint8_t* dot, float* stat) __attribute__((always_inline)) {
-    const int64_t left = head < group ? seq.nq - load_row : 0;  // past the last head: zeros, which add nothing
-    q_load.issue(q_at, left, qt + stream * T::kBytes);
-    do_load.issue(do_at, left, dot + stream * T::kBytes);
+  const int64_t q_turn = kTurnRows * a.q.row * kElem, do_turn = kTurnRows * a.dout.row * kElem;
+  // The loads of a turn: begin(), then load(i) for each i < kLoads.  Spread over
+  // a turn's products: in one stretch they wait for each other, and the wave with them.
+  [[maybe_unused]] int rows_here = 0;  // of the turn being loaded; past the last head: none, zeros add nothing
 #if defined(__HIP_DEVICE_COMPILE__)
+  __amdgpu_buffer_rsrc_t q_src, do_src;
+#endif
+  auto begin = [&](float* stat) __attribute__((always_inline)) {
+    rows_here = __builtin_amdgcn_readfirstlane(head >= group ? 0 : load_turn < last_turn ? kTurnRows : last_rows);
+#if defined(__HIP_DEVICE_COMPILE__)
+    q_src = q_load.source(q_at, rows_here);
+    do_src = do_load.source(do_at, rows_here);
     if (wave < 2) {
       // Rows past the sequence read as zeros: P = 1 there, times dout = 0.
-      const auto src = __builtin_amdgcn_make_buffer_rsrc(
-          stat_at, 0, __builtin_amdgcn_readfirstlane(static_cast<int>(min(left, int64_t(kTurnRows)) * 4)), 0x00020000);
+      const auto src = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(stat_at), 0, rows_here * 4, 0x00020000);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (lds_void_ptr)(stat + (2 * stream + wave) * kWave), 4, lane * 4, 0, 0, 0);
     }
 #endif
-    load_row += kTurnRows;
-    q_at += kTurnRows * a.q.row * kElem;
-    do_at += kTurnRows * a.dout.row * kElem;
-    stat_at += kTurnRows;
-    if (load_row >= seq.nq) {
+    if (load_turn < last_turn) {
+      ++load_turn;
+      q_at += q_turn;
+      do_at += do_turn;
+      stat_at += kTurnRows;
+    } else {
+      load_turn = 0;
       head += HEADS;
       start_head();
     }
+  };
+  auto load = [&](int i, uint8_t* qt, uint8_t* dot) __attribute__((always_inline)) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    if (i < kLoads / 2)
+      q_load.issue(q_src, i, rows_here, qt + stream * T::kBytes);
+    else
+      do_load.issue(do_src, i - kLoads / 2, rows_here, dot + stream * T::kBytes);
+#endif
+  };
+  auto issue = [&](uint8_t* qt, uint8_t* dot, float* stat) __attribute__((always_inline)) {
+    begin(stat);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) load(i, qt, dot);
   };
   // Scores and dout . v of a turn's rows.
   auto scores = [&](const uint8_t* qt, const uint8_t* dot, f32_x16& s, f32_x16& dp) __attribute__((always_inline)) {
@@ -257,10 +310,14 @@ __global__ void __launch_bounds__(kWaves * kWave, 1) attention_dkv_kernel(AttnAr
       multiply<BF16>(dp, by_row.load(dot, 0, kk), v[kk]);
     }
   };
+  // The first turns of a head, whose rows do not all see the wave's last key;
+  // of a head's rows from first_row on, those before see0 (+ 4 half) do not see the lane's.
+  const int masked_turns = a.causal ? static_cast<int>(cut((wave_key + 31 - ahead - first_row + kTurnRows - 1) / kTurnRows, 0, per_head)) : 0;
+  const int see0 = static_cast<int>(cut(key - ahead - first_row, 0, (wave + 2) * kTurnRows)) - 4 * half;
   // From a turn's scores to its probabilities (s) and dS (dp), then the sums;
   // the next turn's scores meanwhile, in one stretch of code without branches.
-  auto step = [&](int64_t i, const uint8_t* qt, const uint8_t* dot, const float* stat, const uint8_t* next_q, const uint8_t* next_do,
-                  f32_x16& s, f32_x16& dp, f32_x16& next_s, f32_x16& next_dp) __attribute__((always_inline)) {
+  auto step = [&](int i, const uint8_t* qt, const uint8_t* dot, const float* stat, const uint8_t* next_q, const uint8_t* next_do,
+                  uint8_t* free_q, uint8_t* free_do, f32_x16& s, f32_x16& dp, f32_x16& next_s, f32_x16& next_dp) __attribute__((always_inline)) {
     float l[16], d[16];
     stat += stream * 2 * kWave;
 #pragma unroll
@@ -270,12 +327,19 @@ __global__ void __launch_bounds__(kWaves * kWave, 1) attention_dkv_kernel(AttnAr
       l[4 * g] = ls.x, l[4 * g + 1] = ls.y, l[4 * g + 2] = ls.z, l[4 * g + 3] = ls.w;
       d[4 * g] = dd.x, d[4 * g + 1] = dd.y, d[4 * g + 2] = dd.z, d[4 * g + 3] = dd.w;
     }
-    if (a.causal && i + ahead < wave_key + 31) {
-      const int see = static_cast<int>(cut(key - ahead - i, 0, kTurnRows)) - 4 * half;  // rows from here on see the key
+    if (i < masked_turns) {
+      const int see = see0 - i * kTurnRows;  // rows from here on see the key
 #pragma unroll
       for (int r = 0; r < 16; ++r) l[r] = result_row(r) < see ? INFINITY : l[r];  // P = 0
     }
-    Operand<BF16> do_col = by_column.load(dot, 0, 0), q_col = by_column.load(qt, 0, 0);
+    constexpr int kColumns = BF16 ? 2 : 1;  // pairs of columns read ahead
+    Operand<BF16> do_col[2 * kDt], q_col[2 * kDt];
+    auto columns = [&](int n) __attribute__((always_inline)) {
+      do_col[n] = by_column.load(dot, n / kDt, n % kDt);
+      q_col[n] = by_column.load(qt, n / kDt, n % kDt);
+    };
+#pragma unroll
+    for (int n = 0; n < kColumns; ++n) columns(n);
     if constexpr (BF16) pin();
     // A product of the next turn's scores, an operand's read two products
     // ahead, and a share of this turn's probabilities, in this order: the
@@ -289,6 +353,8 @@ __global__ void __launch_bounds__(kWaves * kWave, 1) attention_dkv_kernel(AttnAr
     for (int r = 0; r < 16; ++r) next_s[r] = next_dp[r] = 0.0f;
 #pragma unroll
     for (int n = 0; n < kProducts; ++n) {
+      static_assert(kProducts % kLoads == 0, "loads at even distances");
+      if (n % (kProducts / kLoads) == 0) load(n / (kProducts / kLoads), free_q, free_do);
       if (n + kAhead < kProducts) ops[n + kAhead] = operand(n + kAhead);
       if (n & 1)
         multiply<BF16>(next_dp, ops[n], v[n >> 1]);
@@ -308,20 +374,16 @@ __global__ void __launch_bounds__(kWaves * kWave, 1) attention_dkv_kernel(AttnAr
       p[h] = result_operand<BF16>(s, h);
       ds[h] = result_operand<BF16>(dp, h);
     }
-    // The columns of a product pair are read while the pair before is multiplied.
 #pragma unroll
     for (int n = 0; n < 2 * kDt; ++n) {
       const int h = n / kDt, dt = n % kDt;
-      const Operand<BF16> do_now = do_col, q_now = q_col;
-      if (n + 1 < 2 * kDt) {
-        do_col = by_column.load(dot, (n + 1) / kDt, (n + 1) % kDt);
-        q_col = by_column.load(qt, (n + 1) / kDt, (n + 1) % kDt);
-      }
-      multiply<BF16>(dv[dt], do_now, p[h]);
-      multiply<BF16>(dk[dt], q_now, ds[h]);
+      if (n + kColumns < 2 * kDt) columns(n + kColumns);
+      multiply<BF16>(dv[dt], do_col[n], p[h]);
+      multiply<BF16>(dk[dt], q_col[n], ds[h]);
       if constexpr (BF16) pin();
     }
   };
+  int this_turn = 0;  // of its head
   // The turn in `qt`; the following one's rows are in next_q, and free_q, the turn before's, takes the one three ahead.
   auto turn = [&](const uint8_t* qt, const uint8_t* dot, const float* stat, const uint8_t* next_q, const uint8_t* next_do, uint8_t* free_q,
                   uint8_t* free_do, float* free_stat, f32_x16& s, f32_x16& dp, f32_x16& next_s, f32_x16& next_dp)
@@ -332,10 +394,10 @@ __global__ void __launch_bounds__(kWaves * kWave, 1) attention_dkv_kernel(AttnAr
     else
       wait_loads<kLoads>();
     __syncthreads();
-    issue(free_q, free_do, free_stat);
-    const int64_t i = this_row;
-    this_row = i + kTurnRows >= seq.nq ? first_row : i + kTurnRows;
-    step(i, qt, dot, stat, next_q, next_do, s, dp, next_s, next_dp);
+    begin(free_stat);
+    const int i = this_turn;
+    this_turn = i == last_turn ? 0 : i + 1;
+    step(i, qt, dot, stat, next_q, next_do, free_q, free_do, s, dp, next_s, next_dp);
   };
 
   // Turns by the ring's length, so that each place in it is an array of its own.
