@@ -581,12 +581,12 @@ typedef struct {
  * row that sees no key has out 0 and lse -infinity.  lse: float32
  * [rows_q][q_heads], nullable.  Rows of out and lse in no sequence, and keys in
  * none, are not touched.  Scores, sums and out are float32, out rounded once; bf16
- * calls with more than 32 rows and heads per sequence and key head round the
- * probabilities to bf16.  Sequences may share key rows.  A value of k or v that is
+ * calls over many rows round the probabilities to bf16 too, half a step of each
+ * (few rows over long caches keep 16 bits of them).  Sequences may share key rows.  A value of k or v that is
  * not finite may reach any row of out of the sequences whose key it is, seen or
  * not, and no other.
  * head_dim: a multiple of 8, at most 128; q_heads a multiple of kv_heads;
- * scale > 0.  workspace: cq_attention_workspace bytes (0 for many calls: NULL);
+ * 0 < scale <= 2^127.  workspace: cq_attention_workspace bytes (0 for many calls: NULL);
  * how the keys are split, and so its size, depends on the sizes, head_dim,
  * dtype and on whether q_starts and k_starts are NULL. */
 int cq_attention_workspace(const cq_sequences* seqs, int dtype, int q_heads, int kv_heads, int head_dim, int64_t* bytes);
@@ -597,7 +597,9 @@ int cq_attention(const cq_heads* q, const cq_heads* k, const cq_heads* v, int dt
 /* Gradient of cq_attention at its inputs, its out and its lse: dq (rows_q,
  * q_heads), dk and dv (rows_k, kv_heads; summed over the group's query heads)
  * of what reaches out.  Rows in no sequence are not touched.  Every key row may
- * belong to one sequence only.  workspace: cq_attention_grad_workspace bytes. */
+ * belong to one sequence only.  A row that sees no key has dq 0 and gives nothing
+ * to dk and dv.  A value of the inputs that is not finite may reach any gradient
+ * of its sequence, seen or not, and no other.  workspace: cq_attention_grad_workspace bytes. */
 int cq_attention_grad_workspace(const cq_sequences* seqs, int dtype, int q_heads, int kv_heads, int head_dim,
                                 int64_t* bytes);
 int cq_attention_grad(const cq_heads* dout, const cq_heads* q, const cq_heads* k, const cq_heads* v, const cq_heads* out,
@@ -607,7 +609,7 @@ int cq_attention_grad(const cq_heads* dout, const cq_heads* q, const cq_heads* k
 
 /* Per row of logits (rows of vocab values of `dtype`, row r at logits + r *
  * row_stride values, logits 16-byte aligned, row_stride >= vocab), x = scale *
- * logits, scale > 0 (one over a temperature), in float32:
+ * logits, 0 < scale <= 2^127 (one over a temperature), in float32:
  *   lse = log sum exp(x),  logprob = x[tokens[r]] - lse (token_bytes 4 or 8; a
  * token outside [0, vocab): 0),  entropy = -sum p log p with p = exp(x - lse),
  * and the `top` (0 .. 64, at most vocab) largest logits, equal ones by lower

@@ -1023,8 +1023,8 @@ def qk_norm_rope_grad(dq_out, dk_out, q, k, positions=None, freqs=None, q_weight
 
 
 def _attention_args(q, k, v, sequences, q_starts, k_starts, k_lens, scale):
-    """(cq_sequences, dtype code, q_heads, kv_heads, head_dim, scale) of an
-    attention call, checked."""
+    """(cq_sequences, their number, dtype code, q_heads, kv_heads, head_dim,
+    scale) of an attention call, checked."""
     code = _dtype_code("q", q)
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q and k must be [rows, heads, head_dim]")
@@ -1047,7 +1047,7 @@ def _attention_args(q, k, v, sequences, q_starts, k_starts, k_lens, scale):
     if len(bytes_) > 1:
         raise TypeError("q_starts, k_starts and k_lens must have one dtype")
     seqs = _pack_sequences(n, rows_q, rows_k, _opt(q_starts) or 0, _opt(k_starts) or 0, _opt(k_lens) or 0, bytes_.pop() if bytes_ else 4)
-    return seqs, code, qh, kvh, d, 1.0 / math.sqrt(max(d, 1)) if scale is None else scale
+    return seqs, n, code, qh, kvh, d, 1.0 / math.sqrt(max(d, 1)) if scale is None else scale
 
 
 def attention(q, k, v, sequences=None, q_starts=None, k_starts=None, k_lens=None, causal: bool = True, scale=None, out=None,
@@ -1061,7 +1061,7 @@ def attention(q, k, v, sequences=None, q_starts=None, k_starts=None, k_lens=None
     sequence sees all its keys.  scale: 1 / sqrt(D) by default.  Rows of no
     sequence are zeros (lse 0), or left as they are where out or lse is given."""
     import torch
-    seqs, code, qh, kvh, d, scale = _attention_args(q, k, v, sequences, q_starts, k_starts, k_lens, scale)
+    seqs, n, code, qh, kvh, d, scale = _attention_args(q, k, v, sequences, q_starts, k_starts, k_lens, scale)
     _same_kind("q", q, (("out", out, q.shape),))
     heads = (("q", q), ("k", k), ("v", v), ("out", out))
     flat = (("q_starts", q_starts), ("k_starts", k_starts), ("k_lens", k_lens), ("lse", lse), ("workspace", workspace))
@@ -1069,13 +1069,14 @@ def attention(q, k, v, sequences=None, q_starts=None, k_starts=None, k_lens=None
     if not _here(dev, stream):
         return _elsewhere(dev, stream, heads + flat, lambda: attention(
             q, k, v, sequences, q_starts, k_starts, k_lens, causal, scale, out, lse, workspace))
+    gaps = q_starts is not None or n == 0  # starts may leave rows out
     if out is None:
         out, op = _new_heads(q, q.shape)
-        if q_starts is not None:
-            out.zero_()  # starts may leave rows out
+        if gaps:
+            out.zero_()
     if lse is None:
         lse = q.new_empty(q.shape[:2], dtype=torch.float32)
-        if q_starts is not None:
+        if gaps:
             lse.zero_()
     else:
         _out_tensor("lse", lse, q.shape[:2], torch.float32, q)
@@ -1092,7 +1093,7 @@ def attention_grad(dout, q, k, v, out, lse, sequences=None, q_starts=None, k_sta
     sequence only.  Rows of no sequence are zeros, or left as they are in
     tensors that are given."""
     import torch
-    seqs, code, qh, kvh, d, scale = _attention_args(q, k, v, sequences, q_starts, k_starts, k_lens, scale)
+    seqs, n, code, qh, kvh, d, scale = _attention_args(q, k, v, sequences, q_starts, k_starts, k_lens, scale)
     _same_kind("q", q, (("dout", dout, q.shape), ("out", out, q.shape), ("dq", dq, q.shape), ("dk", dk, k.shape),
                         ("dv", dv, k.shape)))
     if lse.dtype != torch.float32 or lse.shape != q.shape[:2]:
@@ -1105,9 +1106,9 @@ def attention_grad(dout, q, k, v, out, lse, sequences=None, q_starts=None, k_sta
             dout, q, k, v, out, lse, sequences, q_starts, k_starts, k_lens, causal, scale, dq, dk, dv, workspace))
     if dq is None:
         dq, dqp = _new_heads(q, q.shape)
-        if q_starts is not None:
+        if q_starts is not None or n == 0:
             dq.zero_()  # starts may leave rows out
-    gaps = k_starts is not None or k_lens is not None
+    gaps = k_starts is not None or k_lens is not None or n == 0
     if dk is None:
         dk, dkp = _new_heads(q, k.shape)
         if gaps:

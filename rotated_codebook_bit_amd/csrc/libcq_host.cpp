@@ -1515,9 +1515,12 @@ int check_attention(int dtype, const cq_sequences* seqs, int q_heads, int kv_hea
   return check_seqs(seqs, s);
 }
 
+// The kernels take powers of two, so scale / log 2 has to be finite too.
+bool usable_scale(float scale) { return scale > 0.0f && scale <= 0x1p127f; }
+
 int attention_args(int causal, float scale, int q_heads, int kv_heads, int head_dim, cq::AttnArgs* a) {
   if (causal != 0 && causal != 1) return fail(CQ_ERR_ARG, "causal is 0 or 1");
-  if (!(scale > 0.0f) || !std::isfinite(scale)) return fail(CQ_ERR_ARG, "scale must be finite and positive");
+  if (!usable_scale(scale)) return fail(CQ_ERR_ARG, "scale must be positive and at most 2^127");
   a->q_heads = q_heads;
   a->kv_heads = kv_heads;
   a->head_dim = head_dim;
@@ -1530,7 +1533,7 @@ int check_logits(const void* logits, int dtype, int64_t rows, int64_t vocab, int
   if (!is_dtype(dtype)) return fail(CQ_ERR_ARG, "unknown dtype %d", dtype);
   if (rows < 0 || vocab < 0) return fail(CQ_ERR_ARG, "negative size");
   if (row_stride < vocab) return fail(CQ_ERR_ARG, "row_stride is below vocab");
-  if (!(scale > 0.0f) || !std::isfinite(scale)) return fail(CQ_ERR_ARG, "scale must be finite and positive");
+  if (!usable_scale(scale)) return fail(CQ_ERR_ARG, "scale must be positive and at most 2^127");
   if (rows > kMaxIndex || vocab > cq::kMaxVocab || !fits(rows, row_stride, 4))
     return fail(CQ_ERR_UNSUPPORTED, "rows must be at most 2^31 - 2, vocab 2^28");
   if (rows && vocab && !logits) return fail(CQ_ERR_NULL, "logits is NULL");

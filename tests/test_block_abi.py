@@ -102,6 +102,13 @@ def test_refusals(func, base, status, changes):
         assert L.cq_last_error()
 
 
+def test_scales_past_a_power_of_two():
+    # scale / log 2 has to be finite: 3e38 is a float32, 3e38 * 1.44 is not.
+    for func, base in ((L.cq_attention, ATTEND), (L.cq_attention_grad, ATTEND_GRAD), (L.cq_token_logprobs, SCORE), (L.cq_token_logprobs_grad, SCORE_GRAD)):
+        assert func(*replace(base, scale=3e38)) == ARG, func
+    assert L.cq_token_logprobs(*replace(SCORE, scale=2.0**127, rows=0)) == 0
+
+
 def test_empty_calls_succeed():
     assert L.cq_qk_norm_rope(*replace(ROTATE, n=0)) == 0
     assert L.cq_qk_norm_rope_grad(*replace(ROTATE_GRAD, n=0, dqw=None, dkw=None)) == 0

@@ -1,6 +1,6 @@
 """The binding of the attention block's operators refuses host tensors, which a
 kernel must never see, in every place a tensor can be given; no GPU is needed:
-meta tensors stand for the ones that are not at fault."""
+host tensors that claim a device stand for the ones that are not at fault."""
 
 import pytest
 import torch

@@ -85,6 +85,24 @@ def test_long_sequence_and_int64_starts(dtype):
     check_packed([(700, 1300), (257, 257)], 4, 1, 128, dtype, index=torch.int64)
 
 
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
+@pytest.mark.parametrize("heads,kv_heads,d", [(8, 2, 64), (5, 1, 40), (3, 3, 64)])
+@pytest.mark.parametrize("lens", [[(700, 700), (1, 1), (300, 300)], [(513, 600), (0, 500), (200, 900)], [(1037, 1037)], [(600, 300), (64, 700)]],
+                         ids=["prompts", "continued", "one", "empty_rows"])
+def test_float_prompts_of_long_sequences(lens, heads, kv_heads, d, causal):
+    check_packed(lens, heads, kv_heads, d, F32, causal=causal)
+
+
+@TYPES
+def test_no_sequences(dtype):
+    q, k, v = randn(6, 4, 64, dtype=dtype), randn(9, 2, 64, dtype=dtype), randn(9, 2, 64, dtype=dtype)
+    torch.full((1 << 20,), 7.0, device=DEV)  # what new tensors would hold otherwise
+    out, lse = cq.attention(q, k, v, sequences=0)
+    grads = cq.attention_grad(q.clone(), q, k, v, out, lse, sequences=0)
+    for t in (out, lse, *grads):
+        assert (t == 0).all()
+
+
 @TYPES
 def test_large_scores(dtype):
     # scores of up to some hundred: one key takes nearly all of a row, the reference moves often
