@@ -198,9 +198,11 @@ constexpr int result_row(int r) { return 8 * (r / 4) + r % 4; }
 // ROWS rows of DP values (heads of up to DP values, the rest zero) in shared
 // memory, in chunks of 16 bytes.  Chunk c of row r lies at place c ^ key(r)
 // of its row: 16 consecutive rows have their chunk c in 16 different places,
-// so operands read by rows meet all banks, and 4 consecutive rows from 4 r
-// on have a pair of chunks in 4 different pairs of places, so operands read
-// by columns do too.
+// so the 16 lanes that read operands by rows in one cycle meet all 64 banks, and
+// the 4 rows from 4 r on have 2 neighbouring pairs of chunks in 8 different
+// places, so the 32 lanes that read them by columns (bf16) do too.  (With the
+// pairs of 4 rows apart but not the 2 neighbours', every transposing read took
+// twice as long.)
 template <bool BF16, int DP, int ROWS>
 struct Tile {
   static constexpr int kElem = BF16 ? 2 : 4;
@@ -209,7 +211,8 @@ struct Tile {
   static constexpr int kBytes = ROWS * kPitch;
   __device__ static __forceinline__ int key(int row) {
     if (!BF16) return row & 15;
-    return kChunks == 8 ? ((row >> 1 & 3) << 1) | (row >> 3 & 1) : ((row & 7) << 1) | (row >> 3 & 1);
+    const int upper = (row >> 2 & 1) << 1 | (row >> 3 & 1);
+    return kChunks == 8 ? (row >> 1 & 1) << 2 | upper : (row & 3) << 2 | upper;  // 8 chunks: two rows meet all banks
   }
 };
 
