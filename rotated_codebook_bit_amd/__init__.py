@@ -77,7 +77,7 @@ class Sequences(ctypes.Structure):
 
 class TokenLogprobs(NamedTuple):
     """What token_logprobs returns, per row: the token's log probability, the
-    entropy, the log of the sum, and the most probable tokens (None without)."""
+    entropy, the log of the sum, and the most probable tokens (of width 0 without)."""
     logprob: Any
     entropy: Any
     lse: Any
@@ -1148,8 +1148,8 @@ def token_logprobs(logits, tokens, scale: float = 1.0, top: int = 0, stream=None
     """TokenLogprobs(logprob, entropy, lse, top, top_logprob) of logits [..., vocab]
     (float32 or bfloat16) times scale, one over a temperature: log probability
     of tokens [...] (0 for a token outside the vocabulary), entropy and log of
-    the sum, float32 [...], and with top > 0 the most probable tokens, int64
-    [..., top], equal ones by lower index, with their log probabilities."""
+    the sum, float32 [...], and the `top` most probable tokens, int64 [..., top],
+    equal ones by lower index, with their log probabilities."""
     import torch
     code, tb = _dtype_code("logits", logits), _token_bytes(tokens)
     stride = _logit_rows("logits", logits, tokens.shape)
@@ -1159,13 +1159,11 @@ def token_logprobs(logits, tokens, scale: float = 1.0, top: int = 0, stream=None
     rows, vocab = tokens.numel(), logits.shape[-1]
     shape = tokens.shape
     logprob, entropy, lse = logits.new_empty((3, *shape), dtype=torch.float32).unbind(0)
-    ids = lps = None
-    if top > 0:
-        ids = logits.new_empty((*shape, top), dtype=torch.int64)
-        lps = logits.new_empty((*shape, top), dtype=torch.float32)
+    ids = logits.new_empty((*shape, max(top, 0)), dtype=torch.int64)
+    lps = logits.new_empty((*shape, max(top, 0)), dtype=torch.float32)
     _check("cq_token_logprobs", lib().cq_token_logprobs(
         logits.data_ptr(), code, rows, vocab, stride, scale, tokens.data_ptr(), tb, logprob.data_ptr(), entropy.data_ptr(),
-        lse.data_ptr(), top, _opt(ids), _opt(lps), _raw_stream(dev)))
+        lse.data_ptr(), top, ids.data_ptr(), lps.data_ptr(), _raw_stream(dev)))
     return TokenLogprobs(logprob, entropy, lse, ids, lps)
 
 

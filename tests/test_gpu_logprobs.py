@@ -82,7 +82,7 @@ def check(logits, tokens, scale, top):
         lp = logp.gather(1, order)
         close(r.top_logprob, lp, es[:, None] + 4 * U * (2 * lp.abs() + 1), "top_logprob")
     else:
-        assert r.top is None and r.top_logprob is None
+        assert r.top.shape == r.top_logprob.shape == (*r.lse.shape, 0)
     return r, want, tol, logp
 
 
