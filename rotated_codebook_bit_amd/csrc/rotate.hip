@@ -32,28 +32,35 @@ __device__ __forceinline__ int64_t index_at(const void* p, int bytes, int64_t i)
   return bytes == 4 ? static_cast<const int32_t*>(p)[i] : static_cast<const int64_t*>(p)[i];
 }
 
-// 8 values as loaded.
+// 8 values as loaded.  Addresses looked up in shared memory are global ones,
+// which the compiler has to be told: it would take loads that might also meet
+// shared memory, and wait for both.
+typedef uint32_t u32_x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(1))) u32_x4* global_ptr;
 template <bool BF16>
 struct Raw8 {
   uint4 r[BF16 ? 1 : 2];
   __device__ __forceinline__ void load(const uint8_t* p) {
 #pragma unroll
-    for (int i = 0; i < (BF16 ? 1 : 2); ++i) r[i] = reinterpret_cast<const uint4*>(p)[i];
+    for (int i = 0; i < (BF16 ? 1 : 2); ++i) r[i] = __builtin_bit_cast(uint4, static_cast<u32_x4>(((global_ptr)(uint8_t*)p)[i]));
   }
   __device__ __forceinline__ void unpack(float (&v)[8]) const {
     unpack_piece<BF16>(r[0], v);
     if constexpr (!BF16) unpack_piece<BF16>(r[1], v + 4);
   }
-};
-template <bool BF16>
-__device__ __forceinline__ void store8(uint8_t* p, const float (&v)[8]) {
-  if constexpr (BF16) {
-    *reinterpret_cast<uint4*>(p) = pack_piece<true>(v);
-  } else {
-    reinterpret_cast<uint4*>(p)[0] = pack_piece<false>(v);
-    reinterpret_cast<uint4*>(p)[1] = pack_piece<false>(v + 4);
+  __device__ __forceinline__ void pack(const float (&v)[8]) {
+    r[0] = pack_piece<BF16>(v);
+    if constexpr (!BF16) r[1] = pack_piece<BF16>(v + 4);
   }
-}
+  __device__ __forceinline__ void store(uint8_t* p) const {
+#pragma unroll
+    for (int i = 0; i < (BF16 ? 1 : 2); ++i) ((global_ptr)p)[i] = __builtin_bit_cast(u32_x4, r[i]);
+  }
+  __device__ __forceinline__ void choose(bool c, const Raw8& o) {
+#pragma unroll
+    for (int i = 0; i < (BF16 ? 1 : 2); ++i) r[i] = make_uint4(c ? o.r[i].x : r[i].x, c ? o.r[i].y : r[i].y, c ? o.r[i].z : r[i].z, c ? o.r[i].w : r[i].w);
+  }
+};
 
 // A team's sum over its L lanes, the same in all of them.
 template <int L>
@@ -71,84 +78,108 @@ __device__ __forceinline__ float team_sum(float v) {
   return v;
 }
 
-__device__ __forceinline__ void load8_shared(const float* p, float (&v)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+// Weights of values 8 part .. + 7 in shared memory: quads 0 of all parts, then
+// quads 1, so that neighbouring lanes' reads lie side by side in the banks.
+constexpr int kMostDim = 256;
+__device__ __forceinline__ void load8_weights(const float* w, int part, float (&v)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(w)[part], b = reinterpret_cast<const float4*>(w)[kMostDim / 8 + part];
   v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
   v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
+__device__ __forceinline__ int weight_at(int d) { return (d & 4) * (kMostDim / 8) + (d >> 3) * 4 + (d & 3); }
 
-// What a lane does with its 8 values d0 .. d0 + 7 of every head.
-template <int PAIRS>
+// What a lane does with its 8 values d0 .. d0 + 7 of every head, without a
+// branch: lanes past the head work on its first values and store nothing,
+// values that do not turn take cosine 1 and sine 0.
+template <bool BF16, int PAIRS>
 struct LanePart {
   int d0, half;
-  bool live, turns, first;  // inside the head; some values turn; kHalves: all are first of their pair
-  int other;                // kHalves: where its pairs' other halves start
-  __device__ __forceinline__ LanePart(int part, int head_dim, int rotary) {
-    d0 = part * kPiece;
+  bool live, turns;
+  int other;            // kHalves: where its pairs' other halves start
+  uint32_t keep, flip;  // kHalves: applied to the other halves' words: cleared if nothing turns; the sign of their sine
+  const float2* idle;   // kHalves, nothing turns: instead of the token's cosines and sines
+  int entry;            // kHalves: of its first pairs in a token's table
+  template <bool BACK>
+  __device__ __forceinline__ void place(int part, int head_dim, int rotary, const float2* identity) {
+    live = part * kPiece < head_dim;
+    d0 = live ? part * kPiece : 0;
     half = rotary / 2;
-    live = d0 < head_dim;
-    turns = live && d0 < rotary;
-    first = d0 < half;
-    other = first ? d0 + half : d0 - half;
+    turns = d0 < rotary;
+    const bool first = d0 < half;
+    other = !turns ? d0 : first ? d0 + half : d0 - half;
+    keep = turns ? 0xFFFFFFFFu : 0u;
+    flip = turns && first != BACK ? (BF16 ? 0x80008000u : 0x80000000u) : 0u;
+    idle = turns ? nullptr : identity;
+    entry = turns ? (first ? d0 : d0 - half) / 8 : 0;
   }
   // Value j: the place of its pair's other value, or its own if it does not turn.
-  __device__ __forceinline__ int place(int j) const {
+  __device__ __forceinline__ int partner(int j) const {
     const int d = d0 + j;
     return d < half ? d + half : d < 2 * half ? d - half : d;
   }
-  // The pairs' other halves of a row, as they lie in memory.
-  template <bool BF16>
+  // The pairs' other halves of a row.
   __device__ __forceinline__ void load_others(const uint8_t* row, Raw8<BF16>& o) const {
     if constexpr (PAIRS == kHalves) {
       o.load(row + other * (BF16 ? 2 : 4));
     } else if constexpr (PAIRS == kHalvesOdd) {
       float v[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = load_elem<BF16>(row, place(j));
+      for (int j = 0; j < 8; ++j) v[j] = load_elem<BF16>(row, partner(j));
       o.r[0] = pack_piece<BF16>(v);
       if constexpr (!BF16) o.r[1] = pack_piece<BF16>(v + 4);
     }
   }
+  __device__ __forceinline__ void unpack_others(Raw8<BF16> o, float (&v)[8]) const {
+    if constexpr (PAIRS == kHalves) {
+#pragma unroll
+      for (int i = 0; i < (BF16 ? 1 : 2); ++i) {
+        o.r[i].x = (o.r[i].x & keep) ^ flip, o.r[i].y = (o.r[i].y & keep) ^ flip;
+        o.r[i].z = (o.r[i].z & keep) ^ flip, o.r[i].w = (o.r[i].w & keep) ^ flip;
+      }
+    }
+    if constexpr (PAIRS != kNeighbours) o.unpack(v);
+  }
   // The weights of the pairs' other halves.
   __device__ __forceinline__ void other_weights(const float* w, float (&o)[8]) const {
     if constexpr (PAIRS == kHalves) {
-      load8_shared(w + other, o);
+      load8_weights(w, other / 8, o);
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = w[place(j)];
+      for (int j = 0; j < 8; ++j) o[j] = w[weight_at(partner(j))];
     }
   }
-  // Turns y, whose pairs' other halves are o, by the token's table, or back.
+  // Turns y, whose pairs' other halves are o (kHalves: with their sine's sign), by a token's table, or back.
   template <bool BACK>
   __device__ __forceinline__ void turn(float (&y)[8], const float (&o)[8], const float2* table) const {
     if constexpr (PAIRS == kNeighbours) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (d0 + 2 * i >= 2 * half) continue;
-        const float2 cs = table[d0 / 2 + i];
+        const bool turns_here = d0 + 2 * i < 2 * half;
+        const float2 cs = table[turns_here ? d0 / 2 + i : 0];
         const float s = BACK ? -cs.y : cs.y, a = y[2 * i], b = y[2 * i + 1];
-        y[2 * i] = a * cs.x - b * s;
-        y[2 * i + 1] = b * cs.x + a * s;
+        y[2 * i] = turns_here ? a * cs.x - b * s : a;
+        y[2 * i + 1] = turns_here ? b * cs.x + a * s : b;
+      }
+    } else if constexpr (PAIRS == kHalves) {
+      const float4* const from = reinterpret_cast<const float4*>(turns ? table : idle) + entry;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 cs = from[i * (half / 8)];
+        y[2 * i] = y[2 * i] * cs.x + o[2 * i] * cs.y;
+        y[2 * i + 1] = y[2 * i + 1] * cs.z + o[2 * i + 1] * cs.w;
       }
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int d = d0 + j;
-        if (PAIRS == kHalvesOdd && d >= 2 * half) continue;
-        const bool lower = PAIRS == kHalves ? first : d < half;
-        const float2 cs = table[lower ? d : d - half];
-        y[j] = y[j] * cs.x + o[j] * (lower != BACK ? -cs.y : cs.y);
+        const bool lower = d < half, turns_here = d < 2 * half;
+        const float2 cs = table[lower ? d : turns_here ? d - half : 0];
+        const float v = y[j] * cs.x + o[j] * (lower != BACK ? -cs.y : cs.y);
+        y[j] = turns_here ? v : y[j];
       }
     }
   }
 };
-
-// The tensor that a head belongs to, field by field: a choice between the
-// structs themselves would be made between their addresses, and every use then
-// load from memory and wait for all loads under way.
-__device__ __forceinline__ HeadRows pick(bool first, const HeadRows& a, const HeadRows& b) {
-  return HeadRows{first ? a.data : b.data, first ? a.row : b.row, first ? a.head : b.head};
-}
 
 // The (token, head) pairs of a chunk, heads running fastest, dealt to the teams
 // in turn; stepped without a division.
@@ -165,7 +196,38 @@ struct Place {
   }
 };
 
-constexpr int kMostDim = 256, kMostTokens = 128;
+constexpr int kMostTokens = 128;
+constexpr int kMostHeads = 256;  // of a block
+
+// Where the heads lie: looked up, since which tensor a head belongs to, times
+// two strides, costs more instructions per head than its norm.
+struct HeadAt {
+  uint64_t in, out;
+  uint32_t in_row, out_row;  // bytes from a token to the next
+};
+__device__ __forceinline__ uint64_t address(const HeadRows& t, int h, int elem) {
+  return reinterpret_cast<uint64_t>(t.data) + static_cast<uint64_t>(h) * t.head * elem;
+}
+__device__ __forceinline__ uint8_t* row_of(uint64_t at, uint32_t row_bytes, uint32_t row) {
+  return reinterpret_cast<uint8_t*>(static_cast<uint64_t>(row) * row_bytes + at);
+}
+// Heads first .. first + count - 1 of the tensors f(head, &in, &out, &its number there).
+template <class F>
+__device__ __forceinline__ void fill_heads(int first, int count, int elem, HeadAt* to, F f) {
+  for (int i = threadIdx.x; i < count; i += kThreads) {
+    const HeadRows *in, *out;
+    int h;
+    f(first + i, &in, &out, &h);
+    const HeadAt at{address(*in, h, elem), address(*out, h, elem), static_cast<uint32_t>(in->row * elem), static_cast<uint32_t>(out->row * elem)};
+    to[i] = at;
+    wait_lds_writes();
+    hold_value(at.in);
+    hold_value(at.out);
+    hold_value(at.in_row);
+    hold_value(at.out_row);
+  }
+}
+
 // Both weights into shared memory, ones where there are none.
 __device__ __forceinline__ void fill_weights(const RotateArgs& a, float (&w)[2][kMostDim]) {
   for (int i = threadIdx.x; i < 2 * kMostDim; i += kThreads) {
@@ -173,49 +235,73 @@ __device__ __forceinline__ void fill_weights(const RotateArgs& a, float (&w)[2][
     const int d = i % kMostDim;
     float v = 1.0f;
     if (from && d < a.head_dim) v = a.w_bf16 ? bf16_low(static_cast<const uint16_t*>(from)[d]) : static_cast<const float*>(from)[d];
-    w[i / kMostDim][d] = v;
+    w[i / kMostDim][weight_at(d)] = v;
     wait_lds_writes();
     hold_value(v);
   }
 }
 
-// Cosines and sines of tokens first .. first + count - 1 into shared memory.
+// Cosines and sines of tokens first .. first + count - 1 into shared memory:
+// per token in order of the pairs, or (kHalves) pairs 0 and 1 of all runs of 8
+// pairs, then pairs 2 and 3, and so on.
+template <int PAIRS>
 __device__ __forceinline__ void fill_table(const RotateArgs& a, int64_t first, int count, float2* table) {
   const int half = a.rotary_dim / 2;
   for (int i = threadIdx.x; i < count * half; i += kThreads) {
-    const double turns = static_cast<double>(index_at(a.positions, a.position_bytes, first + i / half)) *
-                         (static_cast<double>(a.freqs[i % half]) * 0.3183098861837906715);  // half turns
+    const int t = i / half, j = i % half;
+    const double turns = static_cast<double>(index_at(a.positions, a.position_bytes, first + t)) *
+                         (static_cast<double>(a.freqs[j]) * 0.3183098861837906715);  // half turns
     // Reduced to a turn, the angle in two floats: sin(h + l) = sin h + l cos h.
     const double part = turns - 2.0 * rint(0.5 * turns);
     const float high = static_cast<float>(part), low = static_cast<float>(part - high) * 3.14159265f;
     float s, c;
     sincospif(high, &s, &c);
     const float2 cs = make_float2(__builtin_fmaf(-low, s, c), __builtin_fmaf(low, c, s));
-    table[i] = cs;
+    const int at = PAIRS == kHalves ? (j & 6) * (half / 8) + (j >> 3) * 2 + (j & 1) : j;
+    table[t * half + at] = cs;
     wait_lds_writes();
     hold_value(cs.x);
     hold_value(cs.y);
   }
   __syncthreads();
 }
+__device__ __forceinline__ void fill_identity(float2* identity) {
+  if (threadIdx.x < kMostDim / 2) {
+    const float2 cs = make_float2(1.0f, 0.0f);
+    identity[threadIdx.x] = cs;
+    wait_lds_writes();
+    hold_value(cs.x);
+    hold_value(cs.y);
+  }
+}
 
 // Blocks walk over chunks of `tokens` tokens (a launch per block and chunk
 // would spend its time on weights and first loads: 8192 bf16 tokens of 48 heads
 // of 128, one token per block 151 us) and take of each the heads (queries',
 // keys', values') blockIdx.y * heads .. + heads - 1.  A team has its next two
-// heads' loads under way while it computes one.
+// heads' loads under way while it computes one: three sets of registers in
+// turn (a set moved on to the next would wait for its loads), and no branch
+// between a load and its use, so that the waits count exactly.
 template <bool BF16, int L, int PAIRS>
-__global__ void __launch_bounds__(kThreads, 4) rotate_kernel(RotateArgs a, int tokens, int heads, int64_t chunks) {
+__global__ void __launch_bounds__(kThreads, PAIRS == kHalvesOdd ? 3 : 4) rotate_kernel(RotateArgs a, int tokens, int heads, int64_t chunks) {
   constexpr int kElem = BF16 ? 2 : 4, kTeams = kThreads / L;
   __shared__ __attribute__((aligned(16))) float2 table[kTable];
+  __shared__ __attribute__((aligned(16))) float2 identity[kMostDim / 2];
   __shared__ __attribute__((aligned(16))) float weights[2][kMostDim];
-  __shared__ int64_t rows[kMostTokens];
-  const LanePart<PAIRS> lane(threadIdx.x % L, a.head_dim, a.rotary_dim);
+  __shared__ __attribute__((aligned(16))) HeadAt head_at[kMostHeads];
+  __shared__ int rows[kMostTokens];
+  LanePart<BF16, PAIRS> lane;
+  lane.template place<false>(threadIdx.x % L, a.head_dim, a.rotary_dim, identity);
   const int total = a.q_heads + a.kv_heads * (a.v.data ? 2 : 1), rotated = a.q_heads + a.kv_heads;
   const int h0 = blockIdx.y * heads, nh = total - h0 < heads ? total - h0 : heads, half = a.rotary_dim / 2;
-  fill_weights(a, weights);
+  fill_heads(h0, nh, kElem, head_at, [&](int h, const HeadRows** in, const HeadRows** out, int* number) __attribute__((always_inline)) {
+    const bool is_q = h < a.q_heads, is_v = h >= rotated;
+    *in = is_q ? &a.q : is_v ? &a.v : &a.k;
+    *out = is_q ? &a.q_out : is_v ? &a.v_out : &a.k_out;
+    *number = h - (is_q ? 0 : is_v ? rotated : a.q_heads);
+  });
+  __syncthreads();
 
-  const HeadRows q_in = a.q, k_in = a.k, v_in = a.v, q_to = a.q_out, k_to = a.k_out, v_to = a.v_out;
   struct Item {
     Raw8<BF16> y, o;
   };
@@ -223,68 +309,76 @@ __global__ void __launch_bounds__(kThreads, 4) rotate_kernel(RotateArgs a, int t
   const int tokens_by = kTeams / nh, heads_by = kTeams % nh;
   const float per_value = 1.0f / static_cast<float>(a.head_dim);
   for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const int64_t t0 = c * tokens;
-    const int nt = a.n - t0 < tokens ? static_cast<int>(a.n - t0) : tokens;
-    auto load = [&](const Place& at, Item& it) __attribute__((always_inline)) {
-      const int64_t token = t0 + at.t;
-      const int h = h0 + at.h;
-      const bool is_q = h < a.q_heads, is_v = h >= rotated;
-      const HeadRows from = pick(is_q, q_in, pick(is_v, v_in, k_in));
-      const uint8_t* const row = from.data + (token * from.row + (h - (is_q ? 0 : is_v ? rotated : a.q_heads)) * from.head) * kElem;
-      if (lane.live) it.y.load(row + lane.d0 * kElem);
-      if (lane.turns && !is_v) lane.template load_others<BF16>(row, it.o);
-    };
-    // Three heads in turn: one computed, two on their way.
-    Item now{}, next{}, last{};
+    const uint32_t t0 = static_cast<uint32_t>(c * tokens);
+    const int nt = a.n - t0 < tokens ? static_cast<int>(a.n - t0) : tokens, turns = (nt * nh + kTeams - 1) / kTeams;
     Place at = first, ahead = first;
-    if (ahead.t < nt) load(ahead, now);
-    ahead.step(tokens_by, heads_by, nh);
-    if (ahead.t < nt) load(ahead, next);
-    __syncthreads();  // the last chunk's table is read
+    // The heads past a chunk's last read its last token once more.
+    auto load = [&](Item& it) __attribute__((always_inline)) {
+      const HeadAt& from = head_at[ahead.h];
+      const uint8_t* const row = row_of(from.in, from.in_row, t0 + (ahead.t < nt ? ahead.t : nt - 1));
+      it.y.load(row + lane.d0 * kElem);
+      lane.load_others(row, it.o);
+      ahead.step(tokens_by, heads_by, nh);
+    };
+    Item i0, i1, i2;
+    load(i0);
+    load(i1);
+    if (c == blockIdx.x) {
+      fill_weights(a, weights);
+      fill_identity(identity);
+    } else {
+      __syncthreads();  // the last chunk's table is read
+    }
     if (a.slots)
       for (int i = threadIdx.x; i < nt; i += kThreads) {
-        const int64_t slot = index_at(a.slots, a.slot_bytes, t0 + i), row = slot < a.cache_rows ? slot : -1;
+        const int64_t slot = index_at(a.slots, a.slot_bytes, t0 + i);
+        const int row = slot >= 0 && slot < a.cache_rows ? static_cast<int>(slot) : -1;
         rows[i] = row;  // of the cache, below 0: none
         wait_lds_writes();
         hold_value(row);
       }
-    fill_table(a, t0, nt, table);
-    while (at.t < nt) {
-      ahead.step(tokens_by, heads_by, nh);
-      if (ahead.t < nt) load(ahead, last);
-      const int h = h0 + at.h;
+    fill_table<PAIRS>(a, t0, nt, table);
+    auto work = [&](const Item& it) __attribute__((always_inline)) {
+      const HeadAt& to = head_at[at.h];
+      const int t = at.t < nt ? at.t : nt - 1, h = h0 + at.h;
       const bool is_q = h < a.q_heads, is_v = h >= rotated;
-      float y[8], o[8];
-      now.y.unpack(y);
-      if (!is_v) {
-        now.o.unpack(o);
-        if (a.norm) {
-          float ss = 0.0f;
+      float y[8], o[8], v[8], r = 1.0f;
+      it.y.unpack(y);
+      lane.unpack_others(it.o, o);
+      if (a.norm) {
+        float ss = 0.0f;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) ss = __builtin_fmaf(y[j], y[j], ss);
-          const float r = rsqrtf(__builtin_fmaf(team_sum<L>(ss), per_value, a.eps));
-          const float* const w = weights[is_q ? 0 : 1];
-          float v[8];
-          load8_shared(w + (lane.live ? lane.d0 : 0), v);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) y[j] *= r * v[j];
-          if (PAIRS != kNeighbours && lane.turns) {
-            lane.other_weights(w, v);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] *= r * v[j];
-          }
-        }
-        if (lane.turns) lane.template turn<false>(y, o, table + at.t * half);
+        for (int j = 0; j < 8; ++j) ss = __builtin_fmaf(y[j], y[j], ss);
+        r = rsqrtf(__builtin_fmaf(team_sum<L>(lane.live ? ss : 0.0f), per_value, a.eps));
       }
-      int64_t row = t0 + at.t;
-      if (a.slots && !is_q) row = rows[at.t];
-      if (lane.live && row >= 0) {
-        const HeadRows to = pick(is_q, q_to, pick(is_v, v_to, k_to));
-        store8<BF16>(to.data + (row * to.row + (h - (is_q ? 0 : is_v ? rotated : a.q_heads)) * to.head + lane.d0) * kElem, y);
+      const float* const w = weights[is_q ? 0 : 1];
+      load8_weights(w, lane.d0 / 8, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] *= r * v[j];
+      if constexpr (PAIRS != kNeighbours) {
+        lane.other_weights(w, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] *= r * v[j];
       }
-      now = next;
-      next = last;
+      lane.template turn<false>(y, o, table + t * half);
+      int row = static_cast<int>(t0 + t);
+      if (a.slots && !is_q) row = rows[t];
+      Raw8<BF16> out;
+      out.pack(y);
+      out.choose(is_v, it.y);
+      if (lane.live && at.t < nt && row >= 0) out.store(row_of(to.out, to.out_row, row) + lane.d0 * kElem);
       at.step(tokens_by, heads_by, nh);
+    };
+    for (int i = 0;;) {
+      load(i2);
+      work(i0);
+      if (++i >= turns) break;
+      load(i0);
+      work(i1);
+      if (++i >= turns) break;
+      load(i1);
+      work(i2);
+      if (++i >= turns) break;
     }
   }
 }
@@ -292,84 +386,113 @@ __global__ void __launch_bounds__(kThreads, 4) rotate_kernel(RotateArgs a, int t
 // The gradient's blocks walk over chunks of tokens; the shares of the weights'
 // gradients stay in registers until the last one.
 template <bool BF16, int L, int PAIRS>
-__global__ void __launch_bounds__(kThreads, 4) rotate_grad_kernel(RotateArgs a, int tokens, int64_t chunks) {
+__global__ void __launch_bounds__(kThreads, BF16 && PAIRS != kHalvesOdd ? 4 : 3) rotate_grad_kernel(RotateArgs a, int tokens, int heads, int64_t chunks) {
   constexpr int kElem = BF16 ? 2 : 4, kTeams = kThreads / L;
   __shared__ __attribute__((aligned(16))) float2 table[kTable];
+  __shared__ __attribute__((aligned(16))) float2 identity[kMostDim / 2];
   __shared__ __attribute__((aligned(16))) float weights[2][kMostDim];
-  const LanePart<PAIRS> lane(threadIdx.x % L, a.head_dim, a.rotary_dim);
-  const int heads = a.q_heads + a.kv_heads, half = a.rotary_dim / 2;
-  const HeadRows dq_in = a.dq, dk_in = a.dk, q_in = a.q, k_in = a.k, dq_to = a.q_out, dk_to = a.k_out;
+  __shared__ __attribute__((aligned(16))) HeadAt grad_at[kMostHeads], x_at[kMostHeads];
+  LanePart<BF16, PAIRS> lane;
+  lane.template place<true>(threadIdx.x % L, a.head_dim, a.rotary_dim, identity);
+  const int total = a.q_heads + a.kv_heads, half = a.rotary_dim / 2;
+  const int h0 = blockIdx.y * heads, nh = total - h0 < heads ? total - h0 : heads;
   float dqw[8], dkw[8];
-  fill_weights(a, weights);
 #pragma unroll
   for (int j = 0; j < 8; ++j) dqw[j] = dkw[j] = 0.0f;
+  auto of_head = [&](const HeadRows& q_in, const HeadRows& k_in) __attribute__((always_inline)) {
+    return [&a, &q_in, &k_in](int h, const HeadRows** in, const HeadRows** out, int* number) __attribute__((always_inline)) {
+      const bool is_q = h < a.q_heads;
+      *in = is_q ? &q_in : &k_in;
+      *out = is_q ? &a.q_out : &a.k_out;
+      *number = h - (is_q ? 0 : a.q_heads);
+    };
+  };
+  fill_heads(h0, nh, kElem, grad_at, of_head(a.dq, a.dk));
+  if (a.norm) fill_heads(h0, nh, kElem, x_at, of_head(a.q, a.k));
+  __syncthreads();
 
-  const Place first(threadIdx.x / L, heads);
-  const int tokens_by = kTeams / heads, heads_by = kTeams % heads;
+  struct Item {
+    Raw8<BF16> u, o, x;
+  };
+  const Place first(threadIdx.x / L, nh);
+  const int tokens_by = kTeams / nh, heads_by = kTeams % nh;
   const float per_value = 1.0f / static_cast<float>(a.head_dim);
   for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const int64_t t0 = c * tokens;
-    const int nt = a.n - t0 < tokens ? static_cast<int>(a.n - t0) : tokens;
-    struct Item {
-      Raw8<BF16> u, o, x;
-    };
-    auto load = [&](const Place& at, Item& it) __attribute__((always_inline)) {
-      const int64_t token = t0 + at.t;
-      const bool is_q = at.h < a.q_heads;
-      const int64_t h = at.h - (is_q ? 0 : a.q_heads);
-      const HeadRows grad = pick(is_q, dq_in, dk_in), from = pick(is_q, q_in, k_in);
-      const uint8_t* const g_row = grad.data + (token * grad.row + h * grad.head) * kElem;
-      if (lane.live) it.u.load(g_row + lane.d0 * kElem);
-      if (lane.turns) lane.template load_others<BF16>(g_row, it.o);
-      if (a.norm && lane.live) it.x.load(from.data + (token * from.row + h * from.head + lane.d0) * kElem);
-    };
-    Item now{}, next{}, last{};
+    const uint32_t t0 = static_cast<uint32_t>(c * tokens);
+    const int nt = a.n - t0 < tokens ? static_cast<int>(a.n - t0) : tokens, turns = (nt * nh + kTeams - 1) / kTeams;
     Place at = first, ahead = first;
-    if (ahead.t < nt) load(ahead, now);
-    ahead.step(tokens_by, heads_by, heads);
-    if (ahead.t < nt) load(ahead, next);
-    __syncthreads();  // the last chunk's table is read
-    fill_table(a, t0, nt, table);
-    while (at.t < nt) {
-      ahead.step(tokens_by, heads_by, heads);
-      if (ahead.t < nt) load(ahead, last);
-      const int64_t token = t0 + at.t;
-      const bool is_q = at.h < a.q_heads;
-      const int64_t h = at.h - (is_q ? 0 : a.q_heads);
-      const HeadRows to = pick(is_q, dq_to, dk_to);
+    auto load = [&](Item& it) __attribute__((always_inline)) {
+      const uint32_t token = t0 + (ahead.t < nt ? ahead.t : nt - 1);
+      const HeadAt& from = grad_at[ahead.h];
+      const uint8_t* const row = row_of(from.in, from.in_row, token);
+      it.u.load(row + lane.d0 * kElem);
+      lane.load_others(row, it.o);
+      if (a.norm) it.x.load(row_of(x_at[ahead.h].in, x_at[ahead.h].in_row, token) + lane.d0 * kElem);
+      ahead.step(tokens_by, heads_by, nh);
+    };
+    Item i0, i1, i2;
+    load(i0);
+    load(i1);
+    if (c == blockIdx.x) {
+      fill_weights(a, weights);
+      fill_identity(identity);
+    } else {
+      __syncthreads();  // the last chunk's table is read
+    }
+    fill_table<PAIRS>(a, t0, nt, table);
+    auto work = [&](const Item& it) __attribute__((always_inline)) {
+      const HeadAt& to = grad_at[at.h];
+      const int t = at.t < nt ? at.t : nt - 1;
+      const bool is_q = h0 + at.h < a.q_heads, exists = at.t < nt;
       float u[8], o[8];
-      now.u.unpack(u);
-      now.o.unpack(o);
-      if (lane.turns) lane.template turn<true>(u, o, table + at.t * half);
+      it.u.unpack(u);
+      lane.unpack_others(it.o, o);
+      lane.template turn<true>(u, o, table + t * half);
       if (a.norm) {
         float x[8], w[8], ss = 0.0f, dot = 0.0f;
-        now.x.unpack(x);
-        load8_shared(weights[is_q ? 0 : 1] + (lane.live ? lane.d0 : 0), w);
+        it.x.unpack(x);
+        load8_weights(weights[is_q ? 0 : 1], lane.d0 / 8, w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           ss = __builtin_fmaf(x[j], x[j], ss);
           dot = __builtin_fmaf(u[j] * w[j], x[j], dot);
         }
-        const float r = rsqrtf(__builtin_fmaf(team_sum<L>(ss), per_value, a.eps)), k = r * (team_sum<L>(dot) * per_value);
+        const float r = rsqrtf(__builtin_fmaf(team_sum<L>(lane.live ? ss : 0.0f), per_value, a.eps));
+        const float k = r * (team_sum<L>(lane.live ? dot : 0.0f) * per_value);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float xr = x[j] * r, g = u[j];
-          u[j] = r * __builtin_fmaf(-xr, k, g * w[j]);
-          if (is_q)
-            dqw[j] = __builtin_fmaf(g, xr, dqw[j]);
-          else
-            dkw[j] = __builtin_fmaf(g, xr, dkw[j]);
+        for (int j = 0; j < 8; ++j) x[j] *= r;
+        if (exists && is_q) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) dqw[j] = __builtin_fmaf(u[j], x[j], dqw[j]);
         }
+        if (exists && !is_q) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) dkw[j] = __builtin_fmaf(u[j], x[j], dkw[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] = r * __builtin_fmaf(-x[j], k, u[j] * w[j]);
       }
-      if (lane.live) store8<BF16>(to.data + (token * to.row + h * to.head + lane.d0) * kElem, u);
-      now = next;
-      next = last;
-      at.step(tokens_by, heads_by, heads);
+      Raw8<BF16> out;
+      out.pack(u);
+      if (lane.live && exists) out.store(row_of(to.out, to.out_row, t0 + t) + lane.d0 * kElem);
+      at.step(tokens_by, heads_by, nh);
+    };
+    for (int i = 0;;) {
+      load(i2);
+      work(i0);
+      if (++i >= turns) break;
+      load(i0);
+      work(i1);
+      if (++i >= turns) break;
+      load(i1);
+      work(i2);
+      if (++i >= turns) break;
     }
   }
   if (!a.part) return;
   // The teams' shares in team order.
   float* const share = reinterpret_cast<float*>(table);  // [teams][L * 8], 2048 floats
+  const int64_t block = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x;
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
     __syncthreads();
@@ -383,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 4) rotate_grad_kernel(RotateArgs a, 
     for (int d = threadIdx.x; d < a.head_dim; d += kThreads) {
       float sum = 0.0f;
       for (int t = 0; t < kTeams; ++t) sum += share[t * L * kPiece + d];
-      a.part[(static_cast<int64_t>(blockIdx.x) * 2 + which) * a.head_dim + d] = sum;
+      a.part[(block * 2 + which) * a.head_dim + d] = sum;
     }
   }
 }
@@ -421,15 +544,15 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // thread to form a sine, fewer while that leaves compute units idle.
 int tokens_of(int64_t n, int heads, int head_dim) {
   const int teams = kThreads / lanes_of(head_dim);
-  const int64_t most = 4 * teams / heads < 4 ? 4 : 4 * teams / heads, fill = n / (4 * kCus);
+  const int64_t most = 4 * teams / heads < 4 ? 4 : 4 * teams / heads, fill = n / kCus;
   const int64_t tokens = fill < most ? fill : most;
   return static_cast<int>(tokens < 1 ? 1 : tokens);
 }
 // Heads of a block: all, or one token's heads over several blocks while there
 // are few tokens.
 int heads_of(int64_t n, int total, int tokens, int head_dim) {
-  const int teams = kThreads / lanes_of(head_dim);
-  return tokens == 1 && n * ceil_div(total, teams) <= 8 * kCus ? teams : total;
+  const int teams = kThreads / lanes_of(head_dim), heads = tokens == 1 && n * ceil_div(total, teams) <= 8 * kCus ? teams : total;
+  return heads < kMostHeads ? heads : kMostHeads;
 }
 constexpr int kMostBlocks = 4 * kCus;  // as many as fit the card at once
 
@@ -446,8 +569,9 @@ hipError_t launch_at(const RotateArgs& a, hipStream_t s) {
 }
 template <bool BF16, int L, int PAIRS>
 hipError_t launch_grad_at(const RotateArgs& a, int blocks, hipStream_t s) {
-  const int tokens = tokens_of(a.n, a.q_heads + a.kv_heads, a.head_dim);
-  rotate_grad_kernel<BF16, L, PAIRS><<<dim3(blocks), dim3(kThreads), 0, s>>>(a, tokens, ceil_div(a.n, tokens));
+  const int total = a.q_heads + a.kv_heads, tokens = tokens_of(a.n, total, a.head_dim), parts = static_cast<int>(ceil_div(total, kMostHeads));
+  rotate_grad_kernel<BF16, L, PAIRS><<<dim3(blocks / parts, parts), dim3(kThreads), 0, s>>>(
+      a, tokens, total < kMostHeads ? total : kMostHeads, ceil_div(a.n, tokens));
   return hipGetLastError();
 }
 
@@ -488,10 +612,11 @@ hipError_t launch_rotate_heads(const RotateArgs& a, bool bf16, hipStream_t s) {
   return bf16 ? forward<true>(a, s) : forward<false>(a, s);
 }
 
-// One chunk of tokens per block, up to 4 blocks per CU of the MI355X.
+// One chunk of tokens per block, up to 4 blocks per CU, for each kMostHeads heads.
 int rotate_grad_blocks(int64_t n, int q_heads, int kv_heads, int head_dim) {
-  const int64_t chunks = ceil_div(n, tokens_of(n, q_heads + kv_heads, head_dim));
-  return static_cast<int>(chunks < 1024 ? chunks : 1024);
+  const int total = q_heads + kv_heads;
+  const int64_t chunks = ceil_div(n, tokens_of(n, total, head_dim));
+  return static_cast<int>((chunks < kMostBlocks ? chunks : kMostBlocks) * ceil_div(total, kMostHeads));
 }
 
 hipError_t launch_rotate_heads_grad(RotateArgs a, bool bf16, float* dq_weight, float* dk_weight, float* ws, hipStream_t s) {

@@ -129,6 +129,33 @@ def test_variants(case, dtype):
 
 
 @TYPES
+@pytest.mark.parametrize("n,qh,kvh,d,rot", [(3, 300, 30, 32, 32), (700, 257, 1, 16, 16), (1, 600, 200, 64, 32)])
+def test_many_heads(n, qh, kvh, d, rot, dtype):
+    check(n, qh, kvh, d, rot, dtype)
+
+
+@TYPES
+@pytest.mark.parametrize("rot,interleaved", [(16, False), (20, False), (24, True)])
+def test_values_only_move_and_what_does_not_turn_stays_apart(rot, interleaved, dtype):
+    n, d = 9, 64
+    q, k, v, positions, freqs = inputs(n, 4, 2, d, rot, dtype)
+    q, k, v = q.clone(), k.clone(), v.clone()
+    odd = torch.tensor([math.inf, -math.inf, math.nan, -0.0], device=DEV).to(dtype)
+    v[:4, 0, 3], v[4:8, 1, 50] = odd, odd
+    q[2, 1, rot + 1], q[2, 1, 63], k[5, 0, 40] = -math.inf, math.nan, math.inf
+    qo, ko, vo = cq.qk_norm_rope(q, k, positions, freqs, norm=False, interleaved=interleaved, v=v)
+    bits = torch.int16 if dtype == BF16 else torch.int32
+    assert torch.equal(vo.view(bits), v.view(bits))
+    assert torch.isfinite(qo[..., :rot]).all() and torch.isfinite(ko[..., :rot]).all()
+    for out, x in ((qo, q), (ko, k)):
+        assert torch.equal(out[..., rot:].nan_to_num(7.0), x[..., rot:].nan_to_num(7.0))
+    dq, dk, _, _ = cq.qk_norm_rope_grad(q, k, q, k, positions, freqs, norm=False, interleaved=interleaved)
+    for out, x in ((dq, q), (dk, k)):
+        assert torch.isfinite(out[..., :rot]).all()
+        assert torch.equal(out[..., rot:].nan_to_num(7.0), x[..., rot:].nan_to_num(7.0))
+
+
+@TYPES
 def test_many_tokens(dtype):
     check(20000, 4, 1, 64, 64, dtype)
 
