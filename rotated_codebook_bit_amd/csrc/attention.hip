@@ -225,26 +225,31 @@ __device__ __forceinline__ int64_t split_keys(int64_t keys, int splits, int step
 
 template <bool BF16, int DP>
 struct SplitShape {
-  // Two tiles of keys and of values per wave, 16 KiB (bf16, 64) to 64: blocks
-  // small enough that at least two share a CU, so that one's start and end run
-  // beside the other's stream of keys.
-  static constexpr int kTile = Tile<BF16, DP, 32>::kBytes;
-  static constexpr int kWaves = 2 * 4 * kTile > 65536 ? 1 : 2;
+  // bf16: two tiles of keys and of values per wave, as memory bounds it.  Float32:
+  // one of each, as it is bound by the matrix cores and needs a wave for each
+  // SIMD.  Blocks are small enough that two share a CU, so that one's start and
+  // end run beside the other's stream of keys.
+  static constexpr int kTile = Tile<BF16, DP, 32>::kBytes, kBuffers = BF16 ? 2 : 1;
+  static constexpr int kWaves = !BF16 && DP == 64 ? 4 : 2;
   static constexpr int kStep = 32 * kWaves;  // keys that a block takes in one turn
   static constexpr int kPitch = DP + 4;      // floats per row of a wave's output in shared memory
+  static constexpr int kPart = kRows * kPitch * 4;
+  // Each of two arrays: keys and values of a turn of all waves (bf16), or all keys or all values (float32).
+  static constexpr int kArray = kWaves * kBuffers * kTile;
+  static_assert(kWaves / 2 * kPart <= kArray, "half of the waves' outputs fit one of the arrays");
 };
 
 // A block takes one tile of up to 32 rows and one split of its keys; each wave
 // walks over its own tiles of 32 keys, which only it loads and reads, so no
 // wave waits for another before the end.
 template <bool BF16, int DP>
-__global__ void __launch_bounds__((SplitShape<BF16, DP>::kWaves * kWave), 1) attention_split_kernel(AttnArgs a, int64_t tiles) {
+__global__ void __launch_bounds__((SplitShape<BF16, DP>::kWaves * kWave), (SplitShape<BF16, DP>::kWaves / 2)) attention_split_kernel(AttnArgs a, int64_t tiles) {
   typedef SplitShape<BF16, DP> Shape;
   typedef Tile<BF16, DP, 32> T;
   constexpr int kElem = T::kElem, kDepth = DP / 16, kDt = DP / 32, W = Shape::kWaves;
   // Two arrays, not one indexed by the turn: the compiler has to see that the
   // loads under way do not meet the tile being read, or waits for them.
-  __shared__ __attribute__((aligned(16))) uint8_t tiles0[W * 2 * T::kBytes], tiles1[W * 2 * T::kBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t tiles0[Shape::kArray], tiles1[Shape::kArray];
   __shared__ float tops[W][kRows], sums[W][kRows];
   const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), half = lane >> 5;
   const int group = a.q_heads / a.kv_heads;
@@ -266,21 +271,24 @@ __global__ void __launch_bounds__((SplitShape<BF16, DP>::kWaves * kWave), 1) att
   const int64_t out_row = seq.q0 + row.query, out_head = static_cast<int64_t>(kv_head) * group + row.head;
 
   const TileLoader<BF16, DP, 32, 1> k_load(0, lane, a.k.row, a.head_dim), v_load(0, lane, a.v.row, a.head_dim);
-  constexpr int kPending = 2 * TileLoader<BF16, DP, 32, 1>::kLoads;  // of one turn
+  constexpr int kLoads = TileLoader<BF16, DP, 32, 1>::kLoads;  // of a tile
   const RowOperand<BF16, DP> by_row(lane);
   const ColumnOperand<BF16, DP> by_column(lane);
   const uint8_t* const k0 = row_data(a.k, seq.k0, kv_head, kElem);
   const uint8_t* const v0 = row_data(a.v, seq.k0, kv_head, kElem);
   const float factor = a.scale * kLog2e;
 
-  uint8_t* const even = tiles0 + wave * 2 * T::kBytes;
-  uint8_t* const odd = tiles1 + wave * 2 * T::kBytes;
-  auto issue = [&](int64_t key, uint8_t* kt) __attribute__((always_inline)) {
-    k_load.issue(k0 + key * a.k.row * kElem, seq.nk - key, kt);
-    v_load.issue(v0 + key * a.v.row * kElem, seq.nk - key, kt + T::kBytes);
+  uint8_t* const even = tiles0 + wave * Shape::kBuffers * T::kBytes;
+  uint8_t* const odd = tiles1 + wave * Shape::kBuffers * T::kBytes;
+  auto load_k = [&](int64_t key, uint8_t* kt) __attribute__((always_inline)) {
+    k_load.issue(k0 + key * a.k.row * kElem, key < end ? seq.nk - key : 0, kt);
+  };
+  auto load_v = [&](int64_t key, uint8_t* vt) __attribute__((always_inline)) {
+    v_load.issue(v0 + key * a.v.row * kElem, key < end ? seq.nk - key : 0, vt);
   };
   int64_t key = begin + 32 * wave;
-  if (key < end) issue(key, even);
+  load_k(key, even);
+  load_v(key, BF16 ? even + T::kBytes : odd);
   Operand<BF16> q[kDepth];
   load_row_operands<BF16, DP>(row.exists ? row_data(a.q, out_row, out_head, kElem) : nullptr, a.head_dim, half, q);
   RowState st{-INFINITY, 0.0f};
@@ -289,8 +297,7 @@ __global__ void __launch_bounds__((SplitShape<BF16, DP>::kWaves * kWave), 1) att
   for (int dt = 0; dt < kDt; ++dt)
 #pragma unroll
     for (int r = 0; r < 16; ++r) o[dt][r] = 0.0f;
-  auto compute = [&](int64_t key, const uint8_t* kt) __attribute__((always_inline)) {
-    f32_x16 s[1];
+  auto scores = [&](int64_t key, const uint8_t* kt, f32_x16 (&s)[1]) __attribute__((always_inline)) {
 #pragma unroll
     for (int r = 0; r < 16; ++r) s[0][r] = 0.0f;
 #pragma unroll
@@ -301,7 +308,8 @@ __global__ void __launch_bounds__((SplitShape<BF16, DP>::kWaves * kWave), 1) att
       for (int r = 0; r < 16; ++r)
         if (result_row(r) >= left) s[0][r] = -INFINITY;
     }
-    soften<1, kDt>(s, factor, st, o);
+  };
+  auto add_values = [&](const f32_x16 (&s)[1], const uint8_t* vt) __attribute__((always_inline)) {
 #pragma unroll
     for (int step = 0; step < 2; ++step) {
       const Operand<BF16> p = result_operand<BF16>(s[0], step);
@@ -315,37 +323,58 @@ __global__ void __launch_bounds__((SplitShape<BF16, DP>::kWaves * kWave), 1) att
       }
 #pragma unroll
       for (int dt = 0; dt < kDt; ++dt) {
-        const Operand<BF16> v = by_column.load(kt + T::kBytes, step, dt);
+        const Operand<BF16> v = by_column.load(vt, step, dt);
         multiply<BF16>(o[dt], v, p);
         if constexpr (BF16) multiply<BF16>(o[dt], v, rest);
       }
     }
   };
 
-  // One turn's loads are under way while the turn before is computed.
-  auto turn = [&](int64_t key, const uint8_t* now, uint8_t* next) __attribute__((always_inline)) {
-    if (key + Shape::kStep < end) {
-      wait_lds_writes();  // the last turn's reads of the other half are done
-      issue(key + Shape::kStep, next);
-      wait_loads<kPending>();
-    } else {
-      wait_loads<0>();
+  if constexpr (BF16) {
+    // One turn's loads are under way while the turn before is computed.
+    auto turn = [&](int64_t key, const uint8_t* now, uint8_t* next) __attribute__((always_inline)) {
+      if (key + Shape::kStep < end) {
+        wait_lds_writes();  // the last turn's reads of the other half are done
+        load_k(key + Shape::kStep, next);
+        load_v(key + Shape::kStep, next + T::kBytes);
+        wait_loads<2 * kLoads>();
+      } else {
+        wait_loads<0>();
+      }
+      f32_x16 s[1];
+      scores(key, now, s);
+      soften<1, kDt>(s, factor, st, o);
+      add_values(s, now + T::kBytes);
+    };
+    while (key < end) {
+      turn(key, even, odd);
+      key += Shape::kStep;
+      if (key >= end) break;
+      turn(key, odd, even);
+      key += Shape::kStep;
     }
-    compute(key, now);
-  };
-  while (key < end) {
-    turn(key, even, odd);
-    key += Shape::kStep;
-    if (key >= end) break;
-    turn(key, odd, even);
-    key += Shape::kStep;
+  } else {
+    // The next keys are under way once these scores are formed, the next values
+    // once these are added.  Past the end: zeros, which nothing reads.
+    for (; key < end; key += Shape::kStep) {
+      f32_x16 s[1];
+      wait_loads<kLoads>();  // all but the values
+      scores(key, even, s);
+      wait_lds_writes();  // every read of the keys is done
+      load_k(key + Shape::kStep, even);
+      soften<1, kDt>(s, factor, st, o);
+      wait_loads<kLoads>();  // all but the next keys
+      add_values(s, odd);
+      wait_lds_writes();
+      load_v(key + Shape::kStep, odd);
+    }
   }
+  wait_loads<0>();  // none is under way into memory that is used again
 
   // The waves' rows together: each leaves its output, maximum and sum.
   auto part_of = [&](int w) __attribute__((always_inline)) {
-    return reinterpret_cast<float*>((w % 2 ? tiles1 : tiles0) + w / 2 * 4 * T::kBytes);
+    return reinterpret_cast<float*>((w % 2 ? tiles1 : tiles0) + w / 2 * Shape::kPart);
   };
-  static_assert(W <= 2 && kRows * Shape::kPitch * 4 <= W * 2 * T::kBytes, "a wave's output fits one of the arrays");
   float* const part = part_of(wave);
   float sum_a, sum_b;
   both_halves(st.sum, &sum_a, &sum_b);
