@@ -508,16 +508,17 @@ __global__ void __launch_bounds__(256) attention_join_kernel(AttnArgs a) {
 
 constexpr int kMostSplits = kWave;  // a lane of the joining wave each
 
-// Float32 prompts of heads of up to 64 in at most two 128-row blocks per CU: the
-// matrix cores' float32 rate bounds them, so the block with the most keys, 69
-// ns each, ends last.  The split kernel takes 43 ns and four times the blocks,
-// but 8 us more.  One prompt of 4096 tokens, 8 heads over 2: 178 us (blocks
-// 283); 3 of 8192 tokens 308 (385); 13 of 4001 53 (71); 8 of 2000 tokens, 32 heads over 8 (more
-// blocks): 67 (60); 7 of 700 (fewer keys): 30 (27).  Heads of 128 leave room
-// for 2 waves per CU: 2424 (1176).
-bool float_prompts(const AttnSeqs& s, int group, int kv_heads, int head_dim, bool bf16) {
-  return !bf16 && head_dim <= 64 && s.rows_q * group > kRows * s.n_seq && s.rows_k >= 256 * s.n_seq &&
-         s.rows_q * group * kv_heads <= 2 * kCus * kBlockRows;
+// Float32 prompts in at most two 128-row blocks per CU: the matrix cores'
+// float32 rate bounds them, so the block with the most keys, 69 ns each (heads of
+// 64; 280 of 128), ends last.  The split kernel deals them to 4 waves (2) and four
+// times the blocks, but takes some 8 us more.  Split (blocks), 8 heads of 64 over 2:
+// one prompt of 4096 tokens 165 us (283), 3 of 8192 264 (385), 13 of 4001 48 (71), 7
+// of 700 (fewer keys) 31 (27); 32 heads of 64 over 8, 16 of 8192 tokens (more blocks):
+// 360 (315).  Heads of 128: 6 of 3000 tokens, 4 heads over 1, 65 (144); 16 of 64 rows
+// over 4096 keys of 8 heads 170 (554); 4 of 500 43 (33); one of 4096, 32 heads over 8,
+// 1208 (1179).
+bool float_prompts(const AttnSeqs& s, int group, int kv_heads, bool bf16) {
+  return !bf16 && s.rows_q * group > kRows * s.n_seq && s.rows_k >= 256 * s.n_seq && s.rows_q * group * kv_heads <= 2 * kCus * kBlockRows;
 }
 
 // Whether a call takes the split kernel.  Up to 32 rows per sequence and key
@@ -527,9 +528,8 @@ bool float_prompts(const AttnSeqs& s, int group, int kv_heads, int head_dim, boo
 // CUs, and 20 us more to start, end and join.  Over 8192 keys of 8 heads, 32 query
 // heads: 64 new tokens 47 us (blocks 149), 128 65 (149), 512 276 (150); 8 x 16
 // over 4096 49 (78); 1000 tokens of a prompt, 8 heads of 64 over 2, 33 (19).
-// Float32: 64 tokens 180 (1130), 512 1419 (1137).
-bool few_rows(const AttnSeqs& s, int group, int kv_heads, int head_dim, bool bf16) {
-  if (s.rows_q * group <= kRows * s.n_seq || float_prompts(s, group, kv_heads, head_dim, bf16)) return true;
+bool few_rows(const AttnSeqs& s, int group, int kv_heads, bool bf16) {
+  if (s.rows_q * group <= kRows * s.n_seq || float_prompts(s, group, kv_heads, bf16)) return true;
   const int64_t keys = s.rows_k / s.n_seq, blocks = q_tiles(s, group, kBlockRows) * kv_heads;
   const int64_t units = q_tiles(s, group, kRows) * kv_heads;
   return keys > 0 && units + 333000 / keys < 300 * ceil_div(blocks, 2 * kCus);
@@ -543,7 +543,7 @@ int split_step(int head_dim, bool bf16) {
 template <bool BF16, int DP>
 hipError_t launch_at(const AttnArgs& a, hipStream_t stream) {
   const int group = a.q_heads / a.kv_heads;
-  if (!few_rows(a.seqs, group, a.kv_heads, a.head_dim, BF16)) {
+  if (!few_rows(a.seqs, group, a.kv_heads, BF16)) {
     const int64_t tiles = q_tiles(a.seqs, group, kBlockRows);
     attention_kernel<BF16, DP><<<dim3(static_cast<uint32_t>(tiles * a.kv_heads)), dim3(kWaves * kWave), 0, stream>>>(a, tiles);
     return hipGetLastError();
@@ -564,11 +564,11 @@ hipError_t launch_at(const AttnArgs& a, hipStream_t stream) {
 // each pay their start again (16 tokens over 2048 keys: 512 blocks 31 us, 2048 46).
 int attention_splits(const AttnSeqs& s, int q_heads, int kv_heads, int head_dim, bool bf16) {
   const int group = q_heads / kv_heads;
-  if (!few_rows(s, group, kv_heads, head_dim, bf16)) return 1;
+  if (!few_rows(s, group, kv_heads, bf16)) return 1;
   const int64_t units = q_tiles(s, group, kRows) * kv_heads;
   const int64_t longest = s.k_starts ? s.rows_k : s.rows_k / s.n_seq, step = split_step(head_dim, bf16);
   const int64_t fill = ceil_div(2 * kCus, units);
-  const int64_t by_length = float_prompts(s, group, kv_heads, head_dim, bf16) ? 1 : ceil_div(longest, 2048);
+  const int64_t by_length = float_prompts(s, group, kv_heads, bf16) ? 1 : ceil_div(longest, 2048);
   const int64_t want = fill < by_length ? by_length : fill, most = ceil_div(longest, 2 * step);
   const int64_t splits = want < most ? want : most;
   return static_cast<int>(splits < 1 ? 1 : splits > kMostSplits ? kMostSplits : splits);
@@ -581,7 +581,7 @@ int64_t attention_workspace(const AttnSeqs& s, int q_heads, int kv_heads, int he
 
 int64_t attention_blocks(const AttnSeqs& s, int q_heads, int kv_heads, int head_dim, bool bf16) {
   const int group = q_heads / kv_heads;
-  if (!few_rows(s, group, kv_heads, head_dim, bf16)) return q_tiles(s, group, kBlockRows) * kv_heads;
+  if (!few_rows(s, group, kv_heads, bf16)) return q_tiles(s, group, kBlockRows) * kv_heads;
   return q_tiles(s, group, kRows) * kv_heads * attention_splits(s, q_heads, kv_heads, head_dim, bf16);
 }
 

@@ -86,7 +86,7 @@ def test_long_sequence_and_int64_starts(dtype):
 
 
 @pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
-@pytest.mark.parametrize("heads,kv_heads,d", [(8, 2, 64), (5, 1, 40), (3, 3, 64)])
+@pytest.mark.parametrize("heads,kv_heads,d", [(8, 2, 64), (5, 1, 40), (3, 3, 64), (4, 2, 128), (3, 1, 72)])
 @pytest.mark.parametrize("lens", [[(700, 700), (1, 1), (300, 300)], [(513, 600), (0, 500), (200, 900)], [(1037, 1037)], [(600, 300), (64, 700)]],
                          ids=["prompts", "continued", "one", "empty_rows"])
 def test_float_prompts_of_long_sequences(lens, heads, kv_heads, d, causal):
