@@ -76,7 +76,7 @@ constexpr int kTileKeys = 64;
 // 2.1 GHz that the card holds under this load; a step that took a tenth of
 // shared memory's cycles away left the time as it was and the clock lower.
 template <bool BF16, int DP>
-__global__ void __launch_bounds__(kWaves * kWave, BF16 ? 2 : 1) attention_kernel(AttnArgs a, int64_t tiles) {
+__global__ void __launch_bounds__(kWaves * kWave, BF16 ? 2 : 1) attention_kernel(AttnArgs a) {
   typedef Tile<BF16, DP, kTileKeys> T;
   constexpr int kElem = T::kElem, kSubs = kTileKeys / 32, kDepth = DP / 16, kDt = DP / 32;
   __shared__ __attribute__((aligned(16))) uint8_t k_tile0[T::kBytes], k_tile1[T::kBytes], v_tile0[T::kBytes], v_tile1[T::kBytes];
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kWaves * kWave, BF16 ? 2 : 1) attention_kernel
   const int kv_head = static_cast<int>(blockIdx.x % a.kv_heads);
   SeqRows seq;
   int64_t tile;
-  if (!find_tile(a.seqs, tiles - 1 - blockIdx.x / a.kv_heads,
+  if (!find_tile<true, !BF16>(a.seqs, blockIdx.x / a.kv_heads,
                  [&](const SeqRows& s) { return (s.nq * group + kBlockRows - 1) / kBlockRows; }, &seq, &tile))
     return;
   const int64_t rows = seq.nq * group, r0 = tile * kBlockRows + wave * kRows;
@@ -252,7 +252,7 @@ struct SplitShape {
 // 12.4 us for 34 MB, start and end of 512 blocks.  Float32, heads of 128, 2.0 GB:
 // 424 us, 4.7 TB/s (806 with two tiles of each per wave and half the waves).
 template <bool BF16, int DP>
-__global__ void __launch_bounds__((SplitShape<BF16, DP>::kWaves * kWave), (SplitShape<BF16, DP>::kWaves / 2)) attention_split_kernel(AttnArgs a, int64_t tiles) {
+__global__ void __launch_bounds__((SplitShape<BF16, DP>::kWaves * kWave), (SplitShape<BF16, DP>::kWaves / 2)) attention_split_kernel(AttnArgs a) {
   typedef SplitShape<BF16, DP> Shape;
   typedef Tile<BF16, DP, 32> T;
   constexpr int kElem = T::kElem, kDepth = DP / 16, kDt = DP / 32, W = Shape::kWaves;
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__((SplitShape<BF16, DP>::kWaves * kWave), (Split
   const int kv_head = static_cast<int>(blockIdx.x / a.splits % a.kv_heads);
   SeqRows seq;
   int64_t tile;
-  if (!find_tile(a.seqs, tiles - 1 - blockIdx.x / a.splits / a.kv_heads,
+  if (!find_tile<true, !BF16>(a.seqs, blockIdx.x / a.splits / a.kv_heads,
                  [&](const SeqRows& s) { return (s.nq * group + kRows - 1) / kRows; }, &seq, &tile))
     return;
   const int64_t rows = seq.nq * group, r0 = tile * kRows;
@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(256) attention_join_kernel(AttnArgs a) {
   const int kv_head = static_cast<int>(blockIdx.x % a.kv_heads);
   SeqRows seq;
   int64_t tile;
-  if (!find_tile(a.seqs, blockIdx.x / a.kv_heads, [&](const SeqRows& s) { return (s.nq * group + kRows - 1) / kRows; }, &seq, &tile))
+  if (!find_tile<true, false>(a.seqs, blockIdx.x / a.kv_heads, [&](const SeqRows& s) { return (s.nq * group + kRows - 1) / kRows; }, &seq, &tile))
     return;
   const int64_t rows = seq.nq * group, r0 = tile * kRows;
   const int64_t keys = keys_seen(seq, row_of(min(r0 + kRows, rows) - 1, rows, group).query, a.causal);
@@ -522,9 +522,9 @@ constexpr int kMostSplits = kWave;  // a lane of the joining wave each
 // float32 rate bounds them, so the block with the most keys, 69 ns each (heads of
 // 64; 280 of 128), ends last.  The split kernel deals them to 4 waves (2) and four
 // times the blocks, but takes some 8 us more.  Split (blocks), 8 heads of 64 over 2:
-// one prompt of 4096 tokens 165 us (283), 3 of 8192 264 (385), 13 of 4001 48 (71), 7
+// one prompt of 4096 tokens 163 us (283), 3 of 8192 258 (385), 13 of 4001 44 (71), 7
 // of 700 (fewer keys) 31 (27); 32 heads of 64 over 8, 16 of 8192 tokens (more blocks):
-// 360 (315).  Heads of 128: 6 of 3000 tokens, 4 heads over 1, 65 (144); 16 of 64 rows
+// 360 (283).  Heads of 128: 6 of 3000 tokens, 4 heads over 1, 65 (144); 16 of 64 rows
 // over 4096 keys of 8 heads 170 (554); 4 of 500 43 (33); one of 4096, 32 heads over 8,
 // 1208 (1179).
 bool float_prompts(const AttnSeqs& s, int group, int kv_heads, bool bf16) {
@@ -555,12 +555,12 @@ hipError_t launch_at(const AttnArgs& a, hipStream_t stream) {
   const int group = a.q_heads / a.kv_heads;
   if (!few_rows(a.seqs, group, a.kv_heads, BF16)) {
     const int64_t tiles = q_tiles(a.seqs, group, kBlockRows);
-    attention_kernel<BF16, DP><<<dim3(static_cast<uint32_t>(tiles * a.kv_heads)), dim3(kWaves * kWave), 0, stream>>>(a, tiles);
+    attention_kernel<BF16, DP><<<dim3(static_cast<uint32_t>(tiles * a.kv_heads)), dim3(kWaves * kWave), 0, stream>>>(a);
     return hipGetLastError();
   }
-  const int64_t tiles = q_tiles(a.seqs, group, kRows), units = tiles * a.kv_heads;
+  const int64_t units = q_tiles(a.seqs, group, kRows) * a.kv_heads;
   attention_split_kernel<BF16, DP>
-      <<<dim3(static_cast<uint32_t>(units * a.splits)), dim3(SplitShape<BF16, DP>::kWaves * kWave), 0, stream>>>(a, tiles);
+      <<<dim3(static_cast<uint32_t>(units * a.splits)), dim3(SplitShape<BF16, DP>::kWaves * kWave), 0, stream>>>(a);
   if (a.splits > 1) attention_join_kernel<BF16, DP><<<dim3(static_cast<uint32_t>(units)), dim3(256), 0, stream>>>(a);
   return hipGetLastError();
 }

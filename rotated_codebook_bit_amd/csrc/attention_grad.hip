@@ -31,7 +31,7 @@ __device__ __forceinline__ float* dots(const AttnArgs& a, int64_t head) {
 // sequences, 32 heads of 128 over 8, bf16: 288 us, 0.99 PFLOP/s; the matrix cores
 // are busy 54% of the cycles, the vector units 43%, shared memory's reads 28%.
 template <bool BF16, int DP>
-__global__ void __launch_bounds__(kWaves * kWave, BF16 ? 2 : 1) attention_dq_kernel(AttnArgs a, int64_t tiles) {
+__global__ void __launch_bounds__(kWaves * kWave, BF16 ? 2 : 1) attention_dq_kernel(AttnArgs a) {
   typedef Tile<BF16, DP, kTileKeys> T;
   constexpr int kElem = T::kElem, kSubs = kTileKeys / 32, kDepth = DP / 16, kDt = DP / 32;
   __shared__ __attribute__((aligned(16))) uint8_t k_tile0[T::kBytes], k_tile1[T::kBytes], v_tile0[T::kBytes], v_tile1[T::kBytes];
@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(kWaves * kWave, BF16 ? 2 : 1) attention_dq_ker
   const int kv_head = static_cast<int>(blockIdx.x % a.kv_heads);
   SeqRows seq;
   int64_t tile;
-  if (!find_tile(a.seqs, tiles - 1 - blockIdx.x / a.kv_heads,
+  if (!find_tile<true, !BF16>(a.seqs, blockIdx.x / a.kv_heads,
                  [&](const SeqRows& s) { return (s.nq * group + kBlockRows - 1) / kBlockRows; }, &seq, &tile))
     return;
   const int64_t rows = seq.nq * group, r0 = tile * kBlockRows + wave * kRows;
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kWaves * kWave, 1) attention_dkv_kernel(AttnAr
   const int kv_head = static_cast<int>(blockIdx.x % a.kv_heads);
   SeqRows seq;
   int64_t tile;
-  if (!find_tile(a.seqs, blockIdx.x / a.kv_heads, [&](const SeqRows& s) { return (s.nk + kBlockKeys - 1) / kBlockKeys; }, &seq,
+  if (!find_tile<false, true>(a.seqs, blockIdx.x / a.kv_heads, [&](const SeqRows& s) { return (s.nk + kBlockKeys - 1) / kBlockKeys; }, &seq,
                  &tile))
     return;
   const int64_t key0 = tile * kBlockKeys, wave_key = key0 + wave * kRows, key = wave_key + (lane & 31);
@@ -476,7 +476,7 @@ hipError_t launch_at(const AttnArgs& a, hipStream_t stream) {
   const int group = a.q_heads / a.kv_heads;
   const int64_t tiles = q_tiles(a.seqs, group, kBlockRows);
   if (tiles)
-    attention_dq_kernel<BF16, DP><<<dim3(static_cast<uint32_t>(tiles * a.kv_heads)), dim3(kWaves * kWave), 0, stream>>>(a, tiles);
+    attention_dq_kernel<BF16, DP><<<dim3(static_cast<uint32_t>(tiles * a.kv_heads)), dim3(kWaves * kWave), 0, stream>>>(a);
   const bool two = two_streams(group, a.head_dim, BF16);
   const dim3 grid(static_cast<uint32_t>(k_tiles(a.seqs, (two ? 2 : 4) * kRows) * a.kv_heads)), block(kWaves * kWave);
   if (grid.x == 0) return hipGetLastError();
