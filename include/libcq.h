@@ -530,7 +530,7 @@ typedef struct {
  * (slot_bytes 4 or 8, slots in [0, cache_rows); other slots: the row is not
  * written) or, slots NULL, as its row i.  v, v_out (both or neither NULL): values
  * copied to the same rows.  Rows of a cache that no slot names stay as they
- * are; of equal slots any one's row may stay.  q_out may be q, without slots
+ * are; a row that two slots name may mix both.  q_out may be q, without slots
  * k_out may be k and v_out v (same data and strides).  head_dim: a multiple of
  * 8, at most 256; rotary_dim even, at most head_dim. */
 int cq_qk_norm_rope(const cq_heads* q, const cq_heads* k, const cq_heads* v, int dtype, int64_t n, int q_heads,

@@ -961,7 +961,8 @@ def qk_norm_rope(q, k, positions=None, freqs=None, q_weight=None, k_weight=None,
     neighbours with interleaved=True).  Tensors of heads may be strided, e.g.
     parts of one projection's output.  slots [n]: key row i (and v's) goes to row
     slots[i] of k_out and v_out, a cache [rows, kv_heads, D] given by the caller;
-    slots outside it write nothing.  Without slots the outputs may be given too,
+    slots outside it write nothing, a row that two slots name may mix both.
+    Without slots the outputs may be given too,
     q_out=q and k_out=k among them."""
     args = _rotation_args(q, k, positions, freqs, q_weight, k_weight, eps, norm, interleaved)
     n, kvh, d = k.shape

@@ -94,6 +94,13 @@ def test_float_prompts_of_long_sequences(lens, heads, kv_heads, d, causal):
 
 
 @TYPES
+@pytest.mark.parametrize("count", [64, 65, 130])
+def test_many_sequences_of_several_tiles(count, dtype):
+    # around the 64 sequences that one wave orders at once
+    check_packed([(k * 53 % 170, k * 53 % 170 + k % 3) for k in range(count)], 4, 2, 64, dtype)
+
+
+@TYPES
 def test_no_sequences(dtype):
     q, k, v = randn(6, 4, 64, dtype=dtype), randn(9, 2, 64, dtype=dtype), randn(9, 2, 64, dtype=dtype)
     torch.full((1 << 20,), 7.0, device=DEV)  # what new tensors would hold otherwise
