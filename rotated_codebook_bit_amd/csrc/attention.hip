@@ -70,8 +70,8 @@ constexpr int kTileKeys = 64;
 // Prompts: a block of 4 waves owns 128 rows and walks over tiles of 64 keys,
 // the next tile on its way into the other half of shared memory meanwhile.
 // Two blocks share a CU, so that one's exponentials run beside the other's
-// products.  One prompt of 8192 tokens, 32 heads of 128 over 8, bf16: 543 us,
-// 1.01 PFLOP/s, where a large library product reaches 1.36: the matrix cores are
+// products.  One prompt of 8192 tokens, 32 heads of 128 over 8, bf16: 520 to
+// 543 us, 1.01 to 1.06 PFLOP/s, where a large library product reaches 1.36: the matrix cores are
 // busy 60% of the cycles, the vector units 56%, shared memory's reads 30%, at the
 // 2.1 GHz that the card holds under this load; a step that took a tenth of
 // shared memory's cycles away left the time as it was and the clock lower.
@@ -248,7 +248,7 @@ struct SplitShape {
 // A block takes one tile of up to 32 rows and one split of its keys; each wave
 // walks over its own tiles of 32 keys, which only it loads and reads, so no
 // wave waits for another before the end.  64 tokens over caches of up to 8192 keys
-// (1.3 GB, bf16): 262 us, 4.95 TB/s, a large copy's rate; one token over 8192 keys:
+// (1.3 GB, bf16): 255 to 262 us, 5.0 TB/s, a large copy's rate; one token over 8192 keys:
 // 12.4 us for 34 MB, start and end of 512 blocks.  Float32, heads of 128, 2.0 GB:
 // 424 us, 4.7 TB/s (806 with two tiles of each per wave and half the waves).
 template <bool BF16, int DP>

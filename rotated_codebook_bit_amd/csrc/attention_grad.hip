@@ -206,9 +206,9 @@ __global__ void __launch_bounds__(kWaves * kWave, BF16 ? 2 : 1) attention_dq_ker
 // two waves of 32 keys each, halve the longest block, and their sums meet in
 // shared memory (same tokens: 545 us, 590 with one stream).
 //
-// 8192 tokens in 3 sequences, 32 heads of 128 over 8, bf16: 486 to 545 us, 0.70 to
-// 0.78 PFLOP/s; the matrix cores are busy 44% of the cycles, the vector units 34%,
-// waves wait 22%, and the longest blocks end 15% after the average one.  Two
+// 8192 tokens in 3 sequences, 32 heads of 128 over 8, bf16: 466 to 526 us, 0.72 to
+// 0.81 PFLOP/s; the matrix cores are busy 44% of the cycles, the vector units 34%,
+// waves wait 22%, and the last blocks end 10% after the average one.  Two
 // waves per SIMD do not fit the registers (with part of v read from shared
 // memory 705 us).
 constexpr int kTurnRows = 32;

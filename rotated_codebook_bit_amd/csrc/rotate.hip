@@ -12,8 +12,8 @@
 // Memory bounds it at many tokens: every value is read and written once, 16
 // bytes per lane.  8192 bf16 tokens of 32 + 8 heads of 128, with 8 heads of values
 // into a cache: 37.5 us for 201 MB, 5.4 TB/s, past a large copy's 4.8 (part stays
-// in the last cache), the vector units busy 79%; the gradient 45.2 us for 252 MB,
-// 5.6 TB/s, and 7.4 to add the blocks' shares of the weights' gradients.  A head is a team of lanes of 8 values each; a lane needs
+// in the last cache), the vector units busy 77%; the gradient 46.3 us for 252 MB,
+// 5.4 TB/s, and 7.4 to add the blocks' shares of the weights' gradients.  A head is a team of lanes of 8 values each; a lane needs
 // its pairs' other halves too, which lie in the same row, R / 2 values away:
 // it loads them as well (from the cache), which costs no exchange between
 // lanes.  Angles far out lose their bits in float32 (at position 10^5 the
