@@ -572,6 +572,7 @@ hipError_t launch_at(const AttnArgs& a, hipStream_t stream) {
 // the card to the longest (64 tokens over up to 8192 keys of 8 heads, bf16: 238
 // us in pieces of 4096, 227 of 2048, 252 of 512).  More blocks than fit at once
 // each pay their start again (16 tokens over 2048 keys: 512 blocks 31 us, 2048 46).
+// Float32 prompts are not cut by length: their rows, not their keys, fill the card.
 int attention_splits(const AttnSeqs& s, int q_heads, int kv_heads, int head_dim, bool bf16) {
   const int group = q_heads / kv_heads;
   if (!few_rows(s, group, kv_heads, bf16)) return 1;
