@@ -156,6 +156,29 @@ def test_values_only_move_and_what_does_not_turn_stays_apart(rot, interleaved, d
 
 
 @TYPES
+def test_offsets_past_32_bits(dtype):
+    # a cache with rows 2^22 values apart, 5 to 10 GB
+    rows, stride = 1200, 1 << 22
+    q, k, v, positions, freqs = inputs(5, 2, 2, 64, 64, dtype)
+    buf = torch.zeros(rows * stride, dtype=dtype, device=DEV)
+    cache_k, cache_v = buf.as_strided((rows, 2, 64), (stride, 64, 1)), buf.as_strided((rows, 2, 64), (stride, 64, 1), 128)
+    slots = torch.tensor([1199, 3, 700, -1, 1150], device=DEV)
+    cq.qk_norm_rope(q, k, positions, freqs, v=v, slots=slots, k_out=cache_k, v_out=cache_v)
+    _, want, _ = cq.qk_norm_rope(q, k, positions, freqs, v=v)
+    for i, slot in enumerate(slots.tolist()):
+        if slot >= 0:
+            assert torch.equal(cache_k[slot], want[i]) and torch.equal(cache_v[slot], v[i])
+    # the same rows as inputs of the gradient
+    at = slots[slots >= 0].sort().values
+    g = buf.as_strided((rows, 2, 64), (stride, 64, 1))
+    x = torch.zeros_like(cache_k.contiguous()) + 1
+    dq, dk, _, _ = cq.qk_norm_rope_grad(g, g, x, x, torch.arange(rows, device=DEV), freqs, norm=False)
+    small, _, _, _ = cq.qk_norm_rope_grad(g[at], g[at], x[at], x[at], at, freqs, norm=False)
+    assert torch.equal(dq[at], small) and torch.equal(dk[at], small) and torch.count_nonzero(dq) == torch.count_nonzero(small)
+    del buf
+
+
+@TYPES
 def test_many_tokens(dtype):
     check(20000, 4, 1, 64, 64, dtype)
 
