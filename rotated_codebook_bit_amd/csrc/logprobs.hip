@@ -36,16 +36,17 @@ constexpr float kNothing = -10000.0f;  // a power of two that is 0 in float32
 __device__ __forceinline__ float at_least(float x, float y) { return __builtin_elementwise_maximum(x, y); }
 
 // Floats as integers of the same order: NaN above all, both zeros equal.
+constexpr uint32_t kNanOrder = 0xFFFFFFFEu;  // not ~0, so that every key, token 0's too, is below ~0
 __device__ __forceinline__ uint32_t order_of(float x) {
   const uint32_t u = __builtin_bit_cast(uint32_t, x + 0.0f);
-  if (x != x) return 0xFFFFFFFFu;
+  if (x != x) return kNanOrder;
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 __device__ __forceinline__ float value_of(uint32_t order) {
-  if (order == 0xFFFFFFFFu) return __builtin_nanf("");
+  if (order == kNanOrder) return __builtin_nanf("");
   return __builtin_bit_cast(float, order & 0x80000000u ? order & 0x7FFFFFFFu : ~order);
 }
-// Larger keys come first: by value, then by lower index.  No value has key 0.
+// Larger keys come first: by value, then by lower index.  No value has key 0 or ~0.
 __device__ __forceinline__ uint64_t key_of(float x, uint32_t index) {
   return static_cast<uint64_t>(order_of(x)) << 32 | (0xFFFFFFFFu - index);
 }
