@@ -318,14 +318,14 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(LogprobArgs
   const float lse = a.lse[row], g = t >= 0 && t < a.vocab ? a.dlogprob[row] : 0.0f;
   const float h = a.dentropy ? a.dentropy[row] : 0.0f, entropy = a.dentropy ? a.entropy[row] : 0.0f;
   // In powers of two, t = log2 p: dlogits = -p (hs t + ks), plus the token's share.
-  // A row of nothing but -inf has lse -inf; any other c leaves its p at 0.
   const float factor = a.scale * kLog2e;
-  float ref = 0.0f, c = lse == -INFINITY ? 0.0f : lse * kLog2e;
-  const float hs = h * a.scale * kLn2, ks = lse != lse ? lse : (lse == -INFINITY ? 0.0f : __builtin_fmaf(h, entropy, g) * a.scale);
+  float ref = 0.0f, c = lse * kLog2e;
   // Far from zero a float32 lse says little about the sum next to the maximum
   // (at 1024 its step is 2^-13; a row of the type's lowest value would be all
-  // certain): such a row is summed again.
-  const bool far = fabsf(lse) > 1024.0f && fabsf(lse) < INFINITY;
+  // certain), and an infinite one nothing (the largest logit times the scale may
+  // leave float32): such a row is summed again.
+  const bool far = fabsf(lse) > 1024.0f;
+  bool dead = false;  // a row of nothing but -inf: every p is 0
   if (far) {
     __shared__ float red[2][kGradThreads / kWave];
     float top = -INFINITY, sum = 0.0f;
@@ -338,6 +338,8 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(LogprobArgs
 #pragma unroll
     for (int d = 1; d < kWave; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
     ref = over_waves<kGradThreads / kWave>(top, red[0], [](float x, float y) { return fmaxf(x, y); });
+    dead = ref == -INFINITY;
+    if (dead) ref = 0.0f;
     for (int i = threadIdx.x; i < p.pieces(); i += kGradThreads) {
       float v[V];
       unpack_piece<BF16>(p.inside(i, p.load(i)), v);
@@ -345,9 +347,11 @@ __global__ void __launch_bounds__(kGradThreads) logprobs_grad_kernel(LogprobArgs
       for (int j = 0; j < V; ++j) sum += __builtin_amdgcn_exp2f((v[j] - ref) * factor);
     }
     c = __builtin_log2f(over_waves<kGradThreads / kWave>(wave_sum(sum), red[1], [](float x, float y) { return x + y; }));
+    if (dead) c = 0.0f;
     __syncthreads();  // in place: every wave has read the row before one writes
   }
-  const float hit = lse == -INFINITY ? 0.0f : g * a.scale;
+  const float hs = h * a.scale * kLn2, ks = lse != lse ? lse : dead ? 0.0f : __builtin_fmaf(h, entropy, g) * a.scale;
+  const float hit = dead ? 0.0f : g * a.scale;
   for (;;) {
 #pragma unroll
     for (int k = 0; k < kGradPieces; ++k) {
