@@ -1382,19 +1382,23 @@ Lattice lattice(const cq_heads* t, int64_t rows, int heads, int head_dim, int dt
   return Lattice{reinterpret_cast<uintptr_t>(t->data), rows, heads, t->row_stride * b, t->head_stride * b, head_dim * b};
 }
 
-// Whether two tensors share memory.  Parts of one projection's output
-// interleave: with equal row strides they are apart if their columns are, with
-// equal head strides too if their places within a head's stride are.
+// Whether two tensors share memory.  Parts of one projection's output, or
+// keys and values of one cache, interleave: with equal row strides they are
+// apart if their columns are, with equal head strides if what they span within
+// one is (heads first), and with both equal, one a multiple of the other, if
+// their places within the smaller stride are.
 bool share(const Lattice& a, const Lattice& b) {
   if (a.at >= b.end() || b.at >= a.end()) return false;
-  const int64_t wa = (a.heads - 1) * a.head + a.width, wb = (b.heads - 1) * b.head + b.width;
-  auto apart = [](int64_t period, int64_t shift, int64_t na, int64_t nb) {
+  const int64_t shift = static_cast<int64_t>(b.at - a.at);
+  auto apart = [&](int64_t period, int64_t na, int64_t nb) {  // two periodic runs of bytes
     const int64_t d = ((shift % period) + period) % period;
     return d >= na && d + nb <= period;
   };
-  const int64_t shift = static_cast<int64_t>(b.at - a.at);
-  if (a.rows > 1 && b.rows > 1 && a.row == b.row && a.row > 0 && apart(a.row, shift, wa, wb)) return false;
-  if (a.row == b.row && a.head == b.head && a.head > 0 && a.row % a.head == 0 && apart(a.head, shift, a.width, b.width)) return false;
+  const bool rows = a.row == b.row && a.row > 0, heads = a.head == b.head && a.head > 0;
+  if (rows && a.rows > 1 && b.rows > 1 && apart(a.row, (a.heads - 1) * a.head + a.width, (b.heads - 1) * b.head + b.width)) return false;
+  if (heads && a.heads > 1 && b.heads > 1 && apart(a.head, (a.rows - 1) * a.row + a.width, (b.rows - 1) * b.row + b.width)) return false;
+  if (heads && a.row == b.row && a.row % a.head == 0 && apart(a.head, a.width, b.width)) return false;
+  if (rows && a.head == b.head && a.head % a.row == 0 && apart(a.row, a.width, b.width)) return false;
   return true;
 }
 bool share_flat(const Lattice& a, const void* p, int64_t bytes) {
