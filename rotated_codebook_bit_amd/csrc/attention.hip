@@ -15,6 +15,7 @@
 // columns (attention.h).  Probabilities are rounded to bf16 for bf16 inputs
 // (their sum is taken in float32 before): an error of half a step of each
 // probability, as large as that of the stored output itself.
+#include <algorithm>
 #include <type_traits>
 
 #include "attention.h"
@@ -223,10 +224,15 @@ __global__ void __launch_bounds__(kWaves * kWave, BF16 ? 2 : 1) attention_kernel
 
 // ---- Few rows: the keys split over waves and blocks -------------------------------
 
-// Keys of split s of a tile of rows whose last row sees `keys`.
-__device__ __forceinline__ int64_t split_keys(int64_t keys, int splits, int step) {
-  const int64_t each = (keys + splits - 1) / splits;
-  return (each + step - 1) / step * step;
+constexpr int kPieceKeys = 2048;
+
+// Keys of a split of a tile of rows whose last row sees `keys`: the usual
+// number of pieces, or as many as the grid has of half of kPieceKeys.
+__device__ __forceinline__ int64_t split_keys(int64_t keys, const AttnArgs& a, int step) {
+  const uint32_t n = static_cast<uint32_t>(keys), half = kPieceKeys / 2;
+  const uint32_t pieces = min(max(static_cast<uint32_t>(a.pieces), (n + half - 1) / half), static_cast<uint32_t>(a.splits));
+  const uint32_t each = (n + pieces - 1) / pieces;
+  return static_cast<int64_t>((each + step - 1) / step * step);
 }
 
 template <bool BF16, int DP>
@@ -262,16 +268,20 @@ __global__ void __launch_bounds__((SplitShape<BF16, DP>::kWaves * kWave), (Split
   __shared__ float tops[W][kRows], sums[W][kRows];
   const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), half = lane >> 5;
   const int group = a.q_heads / a.kv_heads;
-  const int split = static_cast<int>(blockIdx.x % a.splits);
-  const int kv_head = static_cast<int>(blockIdx.x / a.splits % a.kv_heads);
+  // Pieces that a tile may not have come behind those that all have: among them
+  // they would leave the last of those few places of the card at a time.
+  const uint32_t units = gridDim.x / a.splits, sure = units * a.pieces, at = blockIdx.x;
+  const uint32_t unit = at < sure ? at / a.pieces : (at - sure) % units;
+  const int split = static_cast<int>(at < sure ? at % a.pieces : a.pieces + (at - sure) / units);
+  const int kv_head = static_cast<int>(unit % a.kv_heads);
   SeqRows seq;
   int64_t tile;
-  if (!find_tile<true, !BF16>(a.seqs, blockIdx.x / a.splits / a.kv_heads,
+  if (!find_tile<true, !BF16>(a.seqs, unit / a.kv_heads,
                  [&](const SeqRows& s) { return (s.nq * group + kRows - 1) / kRows; }, &seq, &tile))
     return;
   const int64_t rows = seq.nq * group, r0 = tile * kRows;
   const int64_t keys = keys_seen(seq, row_of(min(r0 + kRows, rows) - 1, rows, group).query, a.causal);
-  const int64_t each = split_keys(keys, a.splits, Shape::kStep);
+  const int64_t each = split_keys(keys, a, Shape::kStep);
   const int64_t begin = split * each, end = min(begin + each, keys);
   if (split > 0 && begin >= keys) return;  // the first split writes rows that see nothing
   const Row row = row_of(r0 + (lane & 31), rows, group);
@@ -460,7 +470,7 @@ __global__ void __launch_bounds__(256) attention_join_kernel(AttnArgs a) {
     return;
   const int64_t rows = seq.nq * group, r0 = tile * kRows;
   const int64_t keys = keys_seen(seq, row_of(min(r0 + kRows, rows) - 1, rows, group).query, a.causal);
-  const int64_t each = split_keys(keys, a.splits, SplitShape<BF16, DP>::kStep);
+  const int64_t each = split_keys(keys, a, SplitShape<BF16, DP>::kStep);
   const int live = keys <= each ? 1 : static_cast<int>((keys + each - 1) / each);
   const int d = lane % kQuads * 4;
   const int64_t pitch = a.head_dim + 4, step = a.seqs.rows_q * a.q_heads * pitch;
@@ -568,32 +578,45 @@ hipError_t launch_at(const AttnArgs& a, hipStream_t stream) {
 }  // namespace
 
 // Splits of the keys: two blocks per CU where tiles of rows alone are fewer, and
-// at most 2048 keys each, so that sequences of different lengths do not leave
-// the card to the longest (64 tokens over up to 8192 keys of 8 heads, bf16: 238
+// pieces of at most 2048 keys, so that sequences of different lengths do not
+// leave the card to the longest (64 tokens over up to 8192 keys of 8 heads, bf16: 238
 // us in pieces of 4096, 227 of 2048, 252 of 512).  More blocks than fit at once
 // each pay their start again (16 tokens over 2048 keys: 512 blocks 31 us, 2048 46).
 // Float32 prompts are not cut by length: their rows, not their keys, fill the card.
-int attention_splits(const AttnSeqs& s, int q_heads, int kv_heads, int head_dim, bool bf16) {
+//
+// That is for a sequence of the mean length, within 16 rounds of the card (a
+// cache may be larger than what it holds).  With k_starts one sequence may have
+// nearly all keys: a tile with more than the mean's is cut further by its own
+// length (split_keys), as the grid has blocks for all keys in one sequence, within
+// 4 rounds; those that a tile does not use have to start all the same.  bf16, 32
+// heads of 128 over 8, by k_lens alone and by k_starts too: 64 tokens over up to 8192
+// keys 232 and 232 us, 256 over up to 4096 427 and 430, 16 over 2048 32 and 37, 8 over 8192 53
+// and 58; all of the same in 1, 2, 4, 8 and 16 pieces, 64 tokens over one cache of 8192 keys
+// and 63 of 100: 159, 92, 55, 75, 121.
+AttnSplits attention_splits(const AttnSeqs& s, int q_heads, int kv_heads, int head_dim, bool bf16) {
   const int group = q_heads / kv_heads;
-  if (!few_rows(s, group, kv_heads, bf16)) return 1;
-  const int64_t units = q_tiles(s, group, kRows) * kv_heads;
-  const int64_t longest = s.k_starts ? s.rows_k : s.rows_k / s.n_seq, step = split_step(head_dim, bf16);
-  const int64_t fill = ceil_div(2 * kCus, units);
-  const int64_t by_length = float_prompts(s, group, kv_heads, bf16) ? 1 : ceil_div(longest, 2048);
-  const int64_t want = fill < by_length ? by_length : fill, most = ceil_div(longest, 2 * step);
-  const int64_t splits = want < most ? want : most;
-  return static_cast<int>(splits < 1 ? 1 : splits > kMostSplits ? kMostSplits : splits);
+  if (!few_rows(s, group, kv_heads, bf16)) return {1, 1};
+  const int64_t units = q_tiles(s, group, kRows) * kv_heads, step = split_step(head_dim, bf16), fill = ceil_div(2 * kCus, units);
+  const int64_t mean = ceil_div(s.rows_k, s.n_seq), longest = s.k_starts ? s.rows_k : mean;
+  // As many as wanted, of at least two steps of `keys`.
+  auto pieces = [&](int64_t wanted, int64_t keys) {
+    return static_cast<int>(std::max(std::min({wanted, ceil_div(keys, 2 * step), int64_t(kMostSplits)}), int64_t(1)));
+  };
+  auto by_length = [&](int64_t keys, int64_t rounds) { return std::min(ceil_div(keys, kPieceKeys), (rounds * 2 * kCus + units / 2) / units); };
+  if (float_prompts(s, group, kv_heads, bf16)) return {pieces(fill, longest), pieces(fill, longest)};
+  const int usual = pieces(std::max(fill, by_length(mean, 16)), mean);
+  return {usual, std::max(usual, pieces(by_length(longest, 4), longest))};
 }
 
 int64_t attention_workspace(const AttnSeqs& s, int q_heads, int kv_heads, int head_dim, bool bf16) {
-  const int splits = attention_splits(s, q_heads, kv_heads, head_dim, bf16);
+  const int splits = attention_splits(s, q_heads, kv_heads, head_dim, bf16).splits;
   return splits > 1 ? splits * s.rows_q * q_heads * (head_dim + 4) * 4 : 0;
 }
 
 int64_t attention_blocks(const AttnSeqs& s, int q_heads, int kv_heads, int head_dim, bool bf16) {
   const int group = q_heads / kv_heads;
   if (!few_rows(s, group, kv_heads, bf16)) return q_tiles(s, group, kBlockRows) * kv_heads;
-  return q_tiles(s, group, kRows) * kv_heads * attention_splits(s, q_heads, kv_heads, head_dim, bf16);
+  return q_tiles(s, group, kRows) * kv_heads * attention_splits(s, q_heads, kv_heads, head_dim, bf16).splits;
 }
 
 hipError_t launch_attention(const AttnArgs& a, bool bf16, hipStream_t s) {

@@ -756,10 +756,14 @@ struct AttnArgs {
   // output, its maximum (in powers of two) and sum.  Gradient: per head and
   // row the log of the sum in powers of two, and sum(dout * out).
   float* ws;
-  int splits;
+  // Forward: a tile of rows has its keys cut into `pieces`, or more if they
+  // are many, but at most `splits` (1: none, no workspace).
+  int pieces, splits;
 };
-// Splits of the keys (1: none, no workspace) and workspace bytes of a call.
-int attention_splits(const AttnSeqs& s, int q_heads, int kv_heads, int head_dim, bool bf16);
+struct AttnSplits {
+  int pieces, splits;
+};
+AttnSplits attention_splits(const AttnSeqs& s, int q_heads, int kv_heads, int head_dim, bool bf16);
 int64_t attention_workspace(const AttnSeqs& s, int q_heads, int kv_heads, int head_dim, bool bf16);
 int64_t attention_blocks(const AttnSeqs& s, int q_heads, int kv_heads, int head_dim, bool bf16);  // of 256 threads, the largest launch
 hipError_t launch_attention(const AttnArgs& a, bool bf16, hipStream_t stream);

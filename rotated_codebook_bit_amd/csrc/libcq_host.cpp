@@ -1715,7 +1715,9 @@ int cq_attention(const cq_heads* q, const cq_heads* k, const cq_heads* v, int dt
   a.out = head_rows(out);
   a.lse = lse;
   a.ws = static_cast<float*>(workspace);
-  a.splits = cq::attention_splits(a.seqs, q_heads, kv_heads, head_dim, bf16);
+  const cq::AttnSplits plan = cq::attention_splits(a.seqs, q_heads, kv_heads, head_dim, bf16);
+  a.pieces = plan.pieces;
+  a.splits = plan.splits;
   return hip_status(cq::launch_attention(a, bf16, static_cast<hipStream_t>(stream)), "attention launch");
 }
 
