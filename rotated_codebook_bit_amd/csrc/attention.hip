@@ -542,14 +542,25 @@ bool float_prompts(const AttnSeqs& s, int group, int kv_heads, bool bf16) {
 }
 
 // Whether a call takes the split kernel.  Up to 32 rows per sequence and key
-// head (one tile) always do.  More rows do while 128-row blocks would leave most
+// head (one tile) do: of every sequence, or (q_starts) on the average, unless one
+// sequence may have most of many rows.  For that one 128-row blocks read its keys a
+// quarter as often, and for the others they are no slower (bf16, 32 heads of 128 over 8,
+// over 4096 keys each, 128-row blocks (split kernel): 300 tokens and a prompt of 8192
+// 1378 us (2152), of 1024 907 (926), 512 x 5 tokens over 2048 826 (842); without caches, 32
+// heads over 32, 8192 tokens in 257 sequences 156 (272), one of 8192 and 300 of 1 662
+// (1460)).  Float32 is bound by the matrix cores, whose work the padded rows are: there
+// they are (10455 (6542), 5587 (1768), 4613 (1554)).
+// More rows do while 128-row blocks would leave most
 // of the card idle over long keys: a block takes 18 ns per key (bf16 heads of
 // 128, 512 blocks at once), a tile of 32 rows some 60 us per 2^20 keys of all
 // CUs, and 20 us more to start, end and join.  Over 8192 keys of 8 heads, 32 query
 // heads: 64 new tokens 47 us (blocks 149), 128 65 (149), 512 276 (150); 8 x 16
 // over 4096 49 (78); 1000 tokens of a prompt, 8 heads of 64 over 2, 33 (19).
+constexpr int64_t kFewTiles = 4 * kCus;  // of 32 rows, all full
 bool few_rows(const AttnSeqs& s, int group, int kv_heads, bool bf16) {
-  if (s.rows_q * group <= kRows * s.n_seq || float_prompts(s, group, kv_heads, bf16)) return true;
+  const int64_t rows = s.rows_q * group;
+  const bool may_be_one = bf16 && s.q_starts && s.rows_q > s.n_seq && rows * kv_heads > kFewTiles * kRows;
+  if ((rows <= kRows * s.n_seq && !may_be_one) || float_prompts(s, group, kv_heads, bf16)) return true;
   const int64_t keys = s.rows_k / s.n_seq, blocks = q_tiles(s, group, kBlockRows) * kv_heads;
   const int64_t units = q_tiles(s, group, kRows) * kv_heads;
   return keys > 0 && units + 333000 / keys < 300 * ceil_div(blocks, 2 * kCus);

@@ -91,3 +91,27 @@ def test_one_long_sequence_among_single_tokens(dtype):
     k, v = randn(sum(lens), 2, 128, dtype=dtype, seed=1), randn(sum(lens), 2, 128, dtype=dtype, seed=2)
     out, lse = cq.attention(q, k, v, q_starts=starts(q_lens), k_starts=at, k_lens=torch.tensor(lens, dtype=torch.int32, device=DEV))
     check(q, k, v, out, lse, q_lens, lens, at.tolist(), range(0, 71, 7))
+
+
+@TYPES
+def test_a_long_prompt_among_single_tokens(dtype):
+    heads, kv_heads, d = 16, 4, 64
+    lens = [1] * 200 + [2500] + [1] * 200
+    n, at = sum(lens), starts(lens)
+    q, k, v = (randn(n, h, d, dtype=dtype, seed=s) for s, h in enumerate((heads, kv_heads, kv_heads)))
+    out, lse = cq.attention(q, k, v, q_starts=at, k_starts=at)
+    check(q, k, v, out, lse, lens, lens, at.tolist(), [0, 1, 199, 200, 201, 400])
+
+
+def test_what_rides_along_leaves_a_long_prompt_as_it_is():
+    """bf16: the same bits for a long prompt whether 10 or 400 single tokens are in
+    its batch, as the same kernel takes it however low the mean length is."""
+    heads, kv_heads, d, long = 16, 4, 64, 2500
+    q, k, v = (randn(long + 400, h, d, dtype=BF16, seed=s) for s, h in enumerate((heads, kv_heads, kv_heads)))
+    results = []
+    for single in (10, 60, 200, 400):
+        at = starts([long] + [1] * single)
+        out, lse = cq.attention(q[:long + single], k[:long + single], v[:long + single], q_starts=at, k_starts=at)
+        results.append((out[:long], lse[:long]))
+    for out, lse in results[1:]:
+        assert torch.equal(out, results[0][0]) and torch.equal(lse, results[0][1])
