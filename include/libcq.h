@@ -599,7 +599,8 @@ int cq_attention(const cq_heads* q, const cq_heads* k, const cq_heads* v, int dt
  * of what reaches out.  Rows in no sequence are not touched.  Every key row may
  * belong to one sequence only.  A row that sees no key has dq 0 and gives nothing
  * to dk and dv.  A value of the inputs that is not finite may reach any gradient
- * of its sequence, seen or not, and no other.  workspace: cq_attention_grad_workspace bytes. */
+ * of its sequence, seen or not, and no other.  bf16: probabilities and dS are rounded
+ * to bf16, half a step of each, and sum(dout out) is taken with the rounded out.  workspace: cq_attention_grad_workspace bytes. */
 int cq_attention_grad_workspace(const cq_sequences* seqs, int dtype, int q_heads, int kv_heads, int head_dim,
                                 int64_t* bytes);
 int cq_attention_grad(const cq_heads* dout, const cq_heads* q, const cq_heads* k, const cq_heads* v, const cq_heads* out,
@@ -628,7 +629,8 @@ int cq_token_logprobs(const void* logits, int dtype, int64_t rows, int64_t vocab
  * dlogprob, dentropy (nullable: zero): float32 [rows].  A token outside
  * [0, vocab) has no logprob, so its dlogprob is not used.  dlogits has `dtype`
  * and out_stride >= vocab; it may be logits (with row_stride).  A row of -infinity
- * has gradient 0. */
+ * has gradient 0; a row whose lse is infinite because its largest logit times
+ * scale leaves float32 has that of its probabilities. */
 int cq_token_logprobs_grad(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t row_stride, float scale,
                            const void* tokens, int token_bytes, const float* lse, const float* dlogprob,
                            const float* dentropy, const float* entropy, void* dlogits, int64_t out_stride,

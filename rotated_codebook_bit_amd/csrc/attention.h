@@ -63,8 +63,13 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
 // come first: within a sequence, or (SORTED, up to 64 sequences) over all of them,
 // so that no long block starts when the others end.  That takes 1 us per block
 // and walks over all sequences' keys at once, which pays where a CU runs one block at
-// a time: gradient of keys and values, and float32 (8192 tokens in 16 sequences, 32 heads
-// of 128 over 8: gradients 225 -> 209 us, float32 1639 -> 1238; but bf16 forward 64 -> 74).
+// a time (gradient of keys and values, float32: 8192 tokens in 16 sequences, 32 heads
+// of 128 over 8, gradients 225 -> 209 us, float32 1639 -> 1238; but bf16 forward 64 -> 74)
+// and where the matrix cores bound the blocks (float32 split kernel, 13 prompts of 4001
+// tokens, 8 heads of 64 over 2, 49 -> 41; no change where memory does).
+// More sequences are walked 64 at a time by every wave, some 0.5 us a turn: little
+// up to some hundreds (512 sequences of 64 tokens, 32 heads of 128 over 8, bf16: 182 us
+// of which 31), most of the time for thousands (4096 of 16: 1662, of which 1200).
 // All lanes of a wave take part and agree on the result.
 template <bool LAST_FIRST, bool SORTED, class Count>
 __device__ __forceinline__ bool find_tile(const AttnSeqs& a, int64_t t, Count count, SeqRows* rows, int64_t* tile) {

@@ -254,7 +254,7 @@ struct SplitShape {
 // A block takes one tile of up to 32 rows and one split of its keys; each wave
 // walks over its own tiles of 32 keys, which only it loads and reads, so no
 // wave waits for another before the end.  64 tokens over caches of up to 8192 keys
-// (1.3 GB, bf16): 255 to 262 us, 5.0 TB/s, a large copy's rate; one token over 8192 keys:
+// (1.3 GB, bf16): 256 us, 5.1 TB/s, a large copy's rate; one token over 8192 keys:
 // 12.4 us for 34 MB, start and end of 512 blocks.  Float32, heads of 128, 2.0 GB:
 // 424 us, 4.7 TB/s (806 with two tiles of each per wave and half the waves).
 template <bool BF16, int DP>
@@ -531,12 +531,11 @@ constexpr int kMostSplits = kWave;  // a lane of the joining wave each
 // Float32 prompts in at most two 128-row blocks per CU: the matrix cores'
 // float32 rate bounds them, so the block with the most keys, 69 ns each (heads of
 // 64; 280 of 128), ends last.  The split kernel deals them to 4 waves (2) and four
-// times the blocks, but takes some 8 us more.  Split (blocks), 8 heads of 64 over 2:
-// one prompt of 4096 tokens 163 us (283), 3 of 8192 258 (385), 13 of 4001 44 (71), 7
-// of 700 (fewer keys) 31 (27); 32 heads of 64 over 8, 16 of 8192 tokens (more blocks):
-// 360 (283).  Heads of 128: 6 of 3000 tokens, 4 heads over 1, 65 (144); 16 of 64 rows
-// over 4096 keys of 8 heads 170 (554); 4 of 500 43 (33); one of 4096, 32 heads over 8,
-// 1208 (1179).
+// times the blocks, but takes some 8 us more.  Split (128-row blocks), 8 heads of 64
+// over 2: one prompt of 4096 tokens 167 us (284), 3 of 8192 in all 249 (354), 13 of 4001
+// 41 (66); 32 heads of 64 over 8, 16 of 8192 in all (more blocks): 324 (249).  Heads of
+// 128: 6 of 3000 in all, 4 heads over 1, 67 (146); 16 of 64 rows over 4096 keys of 8
+// heads 191 (557); one of 4096, 32 heads over 8, 1333 (1185).
 bool float_prompts(const AttnSeqs& s, int group, int kv_heads, bool bf16) {
   return !bf16 && s.rows_q * group > kRows * s.n_seq && s.rows_k >= 256 * s.n_seq && s.rows_q * group * kv_heads <= 2 * kCus * kBlockRows;
 }
@@ -544,18 +543,18 @@ bool float_prompts(const AttnSeqs& s, int group, int kv_heads, bool bf16) {
 // Whether a call takes the split kernel.  Up to 32 rows per sequence and key
 // head (one tile) do: of every sequence, or (q_starts) on the average, unless one
 // sequence may have most of many rows.  For that one 128-row blocks read its keys a
-// quarter as often, and for the others they are no slower (bf16, 32 heads of 128 over 8,
-// over 4096 keys each, 128-row blocks (split kernel): 300 tokens and a prompt of 8192
-// 1378 us (2152), of 1024 907 (926), 512 x 5 tokens over 2048 826 (842); without caches, 32
-// heads over 32, 8192 tokens in 257 sequences 156 (272), one of 8192 and 300 of 1 662
-// (1460)).  Float32 is bound by the matrix cores, whose work the padded rows are: there
-// they are (10455 (6542), 5587 (1768), 4613 (1554)).
-// More rows do while 128-row blocks would leave most
-// of the card idle over long keys: a block takes 18 ns per key (bf16 heads of
-// 128, 512 blocks at once), a tile of 32 rows some 60 us per 2^20 keys of all
-// CUs, and 20 us more to start, end and join.  Over 8192 keys of 8 heads, 32 query
-// heads: 64 new tokens 47 us (blocks 149), 128 65 (149), 512 276 (150); 8 x 16
-// over 4096 49 (78); 1000 tokens of a prompt, 8 heads of 64 over 2, 33 (19).
+// quarter as often, and for the others they are no slower: bf16, 32 heads of 128 over 8,
+// 128-row blocks (split kernel): a prompt of 8192 tokens and 300 of 1, over 4096 keys each,
+// 1393 us (2160), of 1024 902 (1025), 512 x 5 tokens over 2048 823 (846); without caches,
+// 32 heads over 32, 8192 tokens in 257 sequences 152 (270), one of 8192 and 300 of 1 674
+// (1460).  Float32 is bound by the matrix cores, whose work the padded rows are: the
+// same 10599 (6595), 5614 (1893), 4636 (1560), 597 (407), 5180 (4921).
+// More rows do while 128-row blocks would leave most of the card idle over long keys:
+// a block takes 18 ns per key (bf16 heads of 128, 512 blocks at once), a tile of 32 rows
+// some 60 us per 2^20 keys of all CUs, and 20 us more to start, end and join.  Over
+// 8192 keys of 8 heads, 32 query heads, split kernel (128-row blocks): 64 new tokens
+// 49 us (136), 128 68 (135), 512 196 (138); 8 x 16 over 4096 49 (71); 1000 tokens of a
+// prompt, 8 heads of 64 over 2, 30 (17).
 constexpr int64_t kFewTiles = 4 * kCus;  // of 32 rows, all full
 bool few_rows(const AttnSeqs& s, int group, int kv_heads, bool bf16) {
   const int64_t rows = s.rows_q * group;
@@ -589,8 +588,8 @@ hipError_t launch_at(const AttnArgs& a, hipStream_t stream) {
 }  // namespace
 
 // Splits of the keys: two blocks per CU where tiles of rows alone are fewer, and
-// pieces of at most 2048 keys, so that sequences of different lengths do not
-// leave the card to the longest (64 tokens over up to 8192 keys of 8 heads, bf16: 238
+// pieces of at most 2048 keys (64 pieces at most), so that sequences of different
+// lengths do not leave the card to the longest (64 tokens over up to 8192 keys of 8 heads, bf16: 238
 // us in pieces of 4096, 227 of 2048, 252 of 512).  More blocks than fit at once
 // each pay their start again (16 tokens over 2048 keys: 512 blocks 31 us, 2048 46).
 // Float32 prompts are not cut by length: their rows, not their keys, fill the card.
