@@ -580,8 +580,8 @@ typedef struct {
  * causal = 1: only over j <= i + n_k - n_q (the last query sees every key).  A
  * row that sees no key has out 0 and lse -infinity.  lse: float32
  * [rows_q][q_heads], nullable.  Rows of out and lse in no sequence, and keys in
- * none, are not touched.  Scores, sums and out are float32, out rounded once; bf16
- * calls over many rows round the probabilities to bf16 too, half a step of each
+ * none, are not touched.  Scores, sums and out are float32 (scores times log2 e have
+ * to stay within it), out rounded once; bf16 calls over many rows round the probabilities to bf16 too, half a step of each
  * (few rows over long caches keep 16 bits of them).  Sequences may share key rows.  A value of k or v that is
  * not finite may reach any row of out of the sequences whose key it is, seen or
  * not, and no other.

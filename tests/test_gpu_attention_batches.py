@@ -115,3 +115,28 @@ def test_what_rides_along_leaves_a_long_prompt_as_it_is():
         results.append((out[:long], lse[:long]))
     for out, lse in results[1:]:
         assert torch.equal(out, results[0][0]) and torch.equal(lse, results[0][1])
+
+
+@TYPES
+def test_a_captured_call_follows_starts_and_lengths(dtype):
+    """The grid and the workspace come from the sizes; how a tile's keys are cut
+    from what the arrays hold when the graph is replayed."""
+    b, rows_k = 12, 20000
+    q = randn(b, 8, 128, dtype=dtype)
+    k, v = randn(rows_k, 2, 128, dtype=dtype, seed=1), randn(rows_k, 2, 128, dtype=dtype, seed=2)
+    k_at, k_lens = (torch.zeros(b, dtype=torch.int32, device=DEV) for _ in range(2))
+    where = dict(q_starts=starts([1] * b), k_starts=k_at, k_lens=k_lens)
+    cq.attention(q, k, v, **where)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = cq.attention(q, k, v, **where)
+    for lens in ([1600] * b, [18000] + [100] * (b - 1), [3, 0] * (b // 2), [1, 9000, 0, 5, 700, 64, 65, 2048, 33, 31, 4000, 128]):
+        at = starts(lens)[:-1]
+        k_at.copy_(at)
+        k_lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        want = cq.attention(q, k, v, **where)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        check(q, k, v, *got, [1] * b, lens, at.tolist(), range(b))
